@@ -22,6 +22,10 @@ __all__ = [
     "moe_read_device_status", "moe_forward_launch_count", "moe_forward_launch_count_ex", "moe_forward_launch_count_cfg",
     "moe_forward_split_gemms", "moe_profile_forward",
     "workspace_views",
+    "MOE_DTYPE_BF16", "MOE_DTYPE_F16", "MOE_DTYPE_F32", "MOE_DTYPE_U8", "moe_permute", "moe_permute_backward",
+    "moe_unpermute", "moe_unpermute_backward", "moe_topk_route_backward", "moe_quantize_fp8_block",
+    "moe_permute_quantize_fp8_block", "moe_gemm_fp8_block_workspace_bytes", "moe_gemm_fp8_block",
+    "moe_gemm_fp8_block_dgrad",
 ]
 
 MOE_ACT_MXFP8 = 0
@@ -32,6 +36,12 @@ MOE_SCHEDULE_FUSED = 2  # T <= 64: the whole layer in one persistent kernel
 MOE_SCHEDULE_CHAIN_BF16_H = 3  # kernel chain, GEMM1 writes bf16 h, a separate kernel requantises
 MOE_SCHEDULE_CHAIN_SINGLE_CTA = 4  # kernel chain with single-CTA GEMM tiles only (no pair split)
 MOE_SCHEDULE_CHAIN_FP8_Y2 = 5  # kernel chain, GEMM2 rows travel as weighted E4M3 + E8M0 scales
+MOE_DTYPE_BF16 = 0
+MOE_DTYPE_F16 = 1
+MOE_DTYPE_F32 = 2
+MOE_DTYPE_U8 = 3  # moe_permute only: rows of bytes
+_DTYPES = {torch.bfloat16: MOE_DTYPE_BF16, torch.float16: MOE_DTYPE_F16, torch.float32: MOE_DTYPE_F32,
+           torch.uint8: MOE_DTYPE_U8}
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libmoe_topk.so")
 
 STATUS_NAMES = {
@@ -113,6 +123,17 @@ def lib():
     L.moe_forward_ex.argtypes = [ctypes.POINTER(ForwardArgs)]
     L.moe_prepack_scales.restype = i32
     L.moe_prepack_scales.argtypes = [P, i64, i32, P, P]
+    L.moe_permute.argtypes = [P, i64, i32, P, i64, i32, i32, P, i64, i64, P]
+    L.moe_permute_backward.argtypes = [P, i64, i64, i32, P, i64, i32, i32, P, i64, P]
+    L.moe_unpermute.argtypes = [P, i64, i64, i32, P, P, i64, i32, i32, P, i64, P]
+    L.moe_unpermute_backward.argtypes = [P, i64, P, i64, i64, i32, P, P, i64, i32, i32, P, i64, P, P]
+    L.moe_topk_route_backward.argtypes = [P, P, P, i64, i32, i32, P, P]
+    L.moe_quantize_fp8_block.argtypes = [P, i64, i32, i64, i32, i32, P, P, P]
+    L.moe_permute_quantize_fp8_block.argtypes = [P, i64, i32, P, i64, i32, i32, P, P, i64, P]
+    L.moe_gemm_fp8_block_workspace_bytes.argtypes = [i64, i32, i32, i32]
+    L.moe_gemm_fp8_block_workspace_bytes.restype = sz
+    for name in ("moe_gemm_fp8_block", "moe_gemm_fp8_block_dgrad"):
+        getattr(L, name).argtypes = [P, P, P, P, P, i64, i32, i32, i32, P, i32, P, sz, P]
     _lib = L
     return L
 
@@ -336,3 +357,184 @@ def workspace_views(workspace, T, H, I, E, k, fmt=MOE_ACT_MXFP8):
         xs=v(L.xs, rc * H // 32, torch.uint8), a2=v(L.a2, rc * ib, torch.uint8).view(rc, ib),
         a2s=v(L.a2s, rc * I // 32, torch.uint8), y2=v(L.y2, rc * H, torch.bfloat16).view(rc, H),
         status=v(L.status, 8, torch.int32))
+
+
+# ---------------------------------------------------------------- expert rows and FP8 experts
+# The C entry points see only pointers, so these bindings check what a pointer cannot tell:
+# element types, shapes and strides (MOE_ERR_INVALID_ARG naming the tensor).
+
+def _want(ok: bool, where: str, what: str):
+    if not ok:
+        raise MoeError(1, f"{where}: {what}")
+
+
+def _on_gpu(where, *tensors):
+    for t in tensors:
+        if t is not None and not t.is_cuda:
+            raise MoeError(1, f"{where}: every tensor must be on the GPU")
+
+
+def _rows_of(t, where, name):
+    """(row stride, columns) of a row-major matrix with unit column stride."""
+    _want(t.dim() == 2 and (t.stride(1) == 1 or t.shape[1] <= 1), where, f"{name} must be [rows, columns] with unit column stride")
+    return (t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])), t.shape[1]
+
+
+def _table(t, dtype, shape, where, name):
+    _want(t.dtype == dtype and tuple(t.shape) == tuple(shape) and t.is_contiguous(), where,
+          f"{name} must be a contiguous {dtype} tensor of shape {list(shape)}")
+
+
+def _inv(inv, where):
+    _want(inv.dtype == torch.int32 and inv.dim() == 2 and inv.is_contiguous(), where,
+          "inv must be a contiguous int32 tensor [T, k]")
+    return inv.shape
+
+
+def moe_permute(x, inv, rows, stream=None):
+    """rows[inv[t, j]] = x[t]: x [T, H], inv int32 [T, k] (outside [0, R): dropped) -> rows [R, H]."""
+    fn = "moe_permute"
+    T, k = _inv(inv, fn)
+    xs, H = _rows_of(x, fn, "x")
+    rs, Hr = _rows_of(rows, fn, "rows")
+    _want(x.shape[0] == T and Hr == H, fn, "x must be [T, H] and rows [R, H]")
+    _want(x.dtype == rows.dtype and x.dtype in _DTYPES, fn, "x and rows must share a type (bf16, f16, f32, u8)")
+    _on_gpu(fn, x, inv, rows)
+    _check(lib().moe_permute(x.data_ptr(), xs, _DTYPES[x.dtype], inv.data_ptr(), T, H, k, rows.data_ptr(), rs,
+                             rows.shape[0], _stream(stream)), fn)
+
+
+def _gather(fn, rows, inv, topk_w, out, stream):
+    T, k = _inv(inv, fn)
+    rs, H = _rows_of(rows, fn, "the expert rows")
+    os_, Ho = _rows_of(out, fn, "the token rows")
+    _want(out.shape[0] == T and Ho == H, fn, "token rows must be [T, H] and expert rows [R, H]")
+    _want(rows.dtype == out.dtype and rows.dtype in _DTYPES, fn, "both row matrices must share a type (bf16, f16, f32)")
+    if topk_w is not None:
+        _table(topk_w, torch.float32, (T, k), fn, "topk_w")
+    _on_gpu(fn, rows, inv, topk_w, out)
+    L = lib()
+    if topk_w is None:
+        st = L.moe_permute_backward(rows.data_ptr(), rs, rows.shape[0], _DTYPES[rows.dtype], inv.data_ptr(), T, H, k,
+                                    out.data_ptr(), os_, _stream(stream))
+    else:
+        st = L.moe_unpermute(rows.data_ptr(), rs, rows.shape[0], _DTYPES[rows.dtype], inv.data_ptr(),
+                             topk_w.data_ptr(), T, H, k, out.data_ptr(), os_, _stream(stream))
+    _check(st, fn)
+
+
+def moe_permute_backward(d_rows, inv, d_x, stream=None):
+    """Gradient of moe_permute: d_x[t] = sum_j d_rows[inv[t, j]]."""
+    _gather("moe_permute_backward", d_rows, inv, None, d_x, stream)
+
+
+def moe_unpermute(rows, inv, topk_w, out, stream=None):
+    """out[t] = sum_j topk_w[t, j] rows[inv[t, j]]: rows [R, H], topk_w fp32 [T, k] -> out [T, H]."""
+    _want(topk_w is not None, "moe_unpermute", "topk_w is required")
+    _gather("moe_unpermute", rows, inv, topk_w, out, stream)
+
+
+def moe_unpermute_backward(d_out, rows, inv, topk_w, d_rows, d_topk_w, stream=None):
+    """Gradients of moe_unpermute: d_rows[inv[t, j]] = topk_w[t, j] d_out[t] and d_topk_w[t, j] =
+    <d_out[t], rows[inv[t, j]]>.  Either result may be None; rows may be None without d_topk_w."""
+    fn = "moe_unpermute_backward"
+    T, k = _inv(inv, fn)
+    ds, H = _rows_of(d_out, fn, "d_out")
+    _want(d_out.shape[0] == T and d_out.dtype in _DTYPES, fn, "d_out must be [T, H] of bf16, f16 or f32")
+    _table(topk_w, torch.float32, (T, k), fn, "topk_w")
+    _want(d_topk_w is None or rows is not None, fn, "d_topk_w needs rows")
+    R, strides = 0, []
+    for name, t in (("rows", rows if d_topk_w is not None else None), ("d_rows", d_rows)):
+        if t is None:
+            strides.append(0)
+            continue
+        st, Ht = _rows_of(t, fn, name)
+        _want(Ht == H and t.dtype == d_out.dtype, fn, f"{name} must be [R, H] of d_out's type")
+        _want(not strides or not strides[0] or t.shape[0] == R, fn, "rows and d_rows must have the same rows")
+        R = t.shape[0]
+        strides.append(st)
+    if d_topk_w is not None:
+        _table(d_topk_w, torch.float32, (T, k), fn, "d_topk_w")
+    _on_gpu(fn, d_out, rows, inv, topk_w, d_rows, d_topk_w)
+    ptr = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+    _check(lib().moe_unpermute_backward(d_out.data_ptr(), ds, ptr(rows if d_topk_w is not None else None), strides[0],
+                                        R, _DTYPES[d_out.dtype], inv.data_ptr(), topk_w.data_ptr(), T, H, k,
+                                        ptr(d_rows), strides[1], ptr(d_topk_w), _stream(stream)), fn)
+
+
+def moe_topk_route_backward(topk_ids, topk_w, d_topk_w, d_logits, stream=None):
+    """Gradient of moe_topk_route's weights: ids int32, topk_w and d_topk_w fp32 [T, k] -> d_logits fp32 [T, E]."""
+    fn = "moe_topk_route_backward"
+    _want(d_logits.dim() == 2 and topk_ids.dim() == 2, fn, "topk_ids must be [T, k] and d_logits [T, E]")
+    T, E = d_logits.shape
+    shape = (T, topk_ids.shape[1])
+    _table(topk_ids, torch.int32, shape, fn, "topk_ids")
+    _table(topk_w, torch.float32, shape, fn, "topk_w")
+    _table(d_topk_w, torch.float32, shape, fn, "d_topk_w")
+    _table(d_logits, torch.float32, (T, E), fn, "d_logits")
+    _on_gpu(fn, topk_ids, topk_w, d_topk_w, d_logits)
+    _check(lib().moe_topk_route_backward(topk_ids.data_ptr(), topk_w.data_ptr(), d_topk_w.data_ptr(), T, E, shape[1],
+                                         d_logits.data_ptr(), _stream(stream)), fn)
+
+
+def moe_quantize_fp8_block(x, codes, scales, block_rows=1, stream=None):
+    """x [rows, K] -> E4M3 codes u8 [rows, K] and fp32 scales [ceil(rows / block_rows), ceil(K / 128)],
+    block_rows = 1 or 128."""
+    fn = "moe_quantize_fp8_block"
+    xs, K = _rows_of(x, fn, "x")
+    rows = x.shape[0]
+    _want(x.dtype in _DTYPES, fn, "x must be bf16, f16 or f32")
+    _want(block_rows in (1, 128), fn, "block_rows must be 1 or 128")
+    _table(codes, torch.uint8, (rows, K), fn, "codes")
+    _table(scales, torch.float32, (-(-rows // block_rows), -(-K // 128)), fn, "scales")
+    _on_gpu(fn, x, codes, scales)
+    _check(lib().moe_quantize_fp8_block(x.data_ptr(), xs, _DTYPES[x.dtype], rows, K, block_rows, codes.data_ptr(),
+                                        scales.data_ptr(), _stream(stream)), fn)
+
+
+def moe_permute_quantize_fp8_block(x, inv, codes, scales, stream=None):
+    """moe_permute and moe_quantize_fp8_block in one pass: codes u8 [R, K], scales fp32 [R, ceil(K / 128)]."""
+    fn = "moe_permute_quantize_fp8_block"
+    T, k = _inv(inv, fn)
+    xs, K = _rows_of(x, fn, "x")
+    _want(x.shape[0] == T and x.dtype in _DTYPES, fn, "x must be [T, K] of bf16, f16 or f32")
+    R = codes.shape[0]
+    _table(codes, torch.uint8, (R, K), fn, "codes")
+    _table(scales, torch.float32, (R, -(-K // 128)), fn, "scales")
+    _on_gpu(fn, x, inv, codes, scales)
+    _check(lib().moe_permute_quantize_fp8_block(x.data_ptr(), xs, _DTYPES[x.dtype], inv.data_ptr(), T, K, k,
+                                                codes.data_ptr(), scales.data_ptr(), R, _stream(stream)), fn)
+
+
+def moe_gemm_fp8_block_workspace_bytes(M, N, K, E) -> int:
+    return int(lib().moe_gemm_fp8_block_workspace_bytes(int(M), int(N), int(K), int(E)))
+
+
+def _gemm_block(fn, dgrad, x, x_scale, w, w_scale, out, workspace, offsets, stream):
+    _want(w.dim() == 3 and w.dtype == torch.uint8 and w.is_contiguous(), fn, "w must be a contiguous uint8 tensor [E, N, K]")
+    E, N, K = w.shape
+    inner, outer = (N, K) if dgrad else (K, N)
+    M = x.shape[0]
+    _table(x, torch.uint8, (M, inner), fn, "the codes")
+    _table(x_scale, torch.float32, (M, -(-inner // 128)), fn, "the codes' scales")
+    _table(w_scale, torch.float32, (E, -(-N // 128), -(-K // 128)), fn, "w_scale")
+    _want(out.dtype in _DTYPES, fn, "the output must be bf16, f16 or f32")
+    _table(out, out.dtype, (M, outer), fn, "the output")
+    if offsets is not None:
+        _table(offsets, torch.int64, (E + 1,), fn, "offsets")
+    _on_gpu(fn, x, x_scale, w, w_scale, out, workspace, offsets)
+    _check(getattr(lib(), fn)(x.data_ptr(), x_scale.data_ptr(), w.data_ptr(), w_scale.data_ptr(),
+                              None if offsets is None else offsets.data_ptr(), M, N, K, E, out.data_ptr(),
+                              _DTYPES[out.dtype], workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                              _stream(stream)), fn)
+
+
+def moe_gemm_fp8_block(x, x_scale, w, w_scale, out, workspace, offsets=None, stream=None):
+    """FP8 product with block scales: x u8 [M, K], x_scale fp32 [M, ceil(K/128)], w u8 [E, N, K], w_scale fp32
+    [E, ceil(N/128), ceil(K/128)], offsets int64 [E + 1] (None: E = 1, all rows) -> out [M, N]."""
+    _gemm_block("moe_gemm_fp8_block", False, x, x_scale, w, w_scale, out, workspace, offsets, stream)
+
+
+def moe_gemm_fp8_block_dgrad(dy, dy_scale, w, w_scale, dx, workspace, offsets=None, stream=None):
+    """Gradient of moe_gemm_fp8_block with respect to x: dy u8 [M, N], dy_scale fp32 [M, ceil(N/128)] -> dx [M, K]."""
+    _gemm_block("moe_gemm_fp8_block_dgrad", True, dy, dy_scale, w, w_scale, dx, workspace, offsets, stream)

@@ -1,0 +1,402 @@
+// expert_rows.cu -- token rows to expert rows and back, their gradients, and the gradient of the
+// routing weights.  With r(t, j) = inv[t*k + j] the row of token t's slot j:
+//   permute            rows[r(t, j)] = x[t]
+//   permute backward   dx[t] = sum_j drows[r(t, j)]
+//   unpermute          out[t] = sum_j w[t, j] rows[r(t, j)]
+//   unpermute backward drows[r(t, j)] = w[t, j] dout[t];  dw[t, j] = <dout[t], rows[r(t, j)]>
+//   route backward     w = softmax over the k selected logits, so with g_j = w_j (dw_j - sum_i w_i dw_i)
+//                      dlogits[t, ids[t, j]] = g_j and 0 in the other columns
+// All sums run in fp32 in slot order and are rounded once; a pair whose row lies outside [0, R) is
+// dropped: it is neither read nor written, and its dw is 0.
+//
+// Every kernel moves each byte once and is bound by HBM, so work is split by token: a token's row
+// is read once and its k expert rows are touched by the same threads, with all loads of a thread
+// issued before the first use.  A thread's access is the widest power of two (16 bytes at most)
+// that divides the addresses, strides and row length.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <algorithm>
+
+#include "expert_internal.h"
+
+namespace moe {
+namespace {
+
+constexpr int kRowThreads = 256;
+
+template <int VB>
+struct Raw;
+template <>
+struct Raw<16> { using T = uint4; };
+template <>
+struct Raw<8> { using T = uint2; };
+template <>
+struct Raw<4> { using T = uint32_t; };
+template <>
+struct Raw<2> { using T = uint16_t; };
+template <>
+struct Raw<1> { using T = uint8_t; };
+
+template <int DT>
+struct Elem;
+template <>
+struct Elem<kDtBf16> {
+  using T = __nv_bfloat16;
+  static __device__ __forceinline__ float to(T v) { return __bfloat162float(v); }
+  static __device__ __forceinline__ T from(float v) { return __float2bfloat16_rn(v); }
+};
+template <>
+struct Elem<kDtF16> {
+  using T = __half;
+  static __device__ __forceinline__ float to(T v) { return __half2float(v); }
+  static __device__ __forceinline__ T from(float v) { return __float2half_rn(v); }
+};
+template <>
+struct Elem<kDtF32> {
+  using T = float;
+  static __device__ __forceinline__ float to(T v) { return v; }
+  static __device__ __forceinline__ T from(float v) { return v; }
+};
+
+// VB bytes as the elements they hold.
+template <int DT, int VB>
+union Chunk {
+  using E = typename Elem<DT>::T;
+  static constexpr int kN = VB / (int)sizeof(E);
+  typename Raw<VB>::T raw;
+  E e[kN];
+  __device__ __forceinline__ Chunk() {}
+};
+
+struct RowsParams {
+  RowsArgs a;
+  int chunks;    // VB-byte chunks of a row
+  int lg;        // log2 of the threads a row gets
+  int elem;      // bytes of an element
+};
+
+// The k expert rows of token t; -1 for a dropped pair.
+__device__ __forceinline__ void load_rows(const RowsArgs& a, int64_t t, int (&r)[kMaxTopK]) {
+#pragma unroll
+  for (int j = 0; j < kMaxTopK; ++j) {
+    r[j] = -1;
+    if (j < a.k) {
+      const int v = a.inv[t * a.k + j];
+      if (v >= 0 && v < a.R) r[j] = v;
+    }
+  }
+}
+
+// A thread copies U chunks of a token's row to each of its k rows.
+template <int VB, int U>
+__global__ void __launch_bounds__(kRowThreads) permute_kernel(const __grid_constant__ RowsParams p) {
+  using V = typename Raw<VB>::T;
+  const RowsArgs& a = p.a;
+  const int tpr = 1 << p.lg;
+  const int64_t t = (int64_t)blockIdx.x * (kRowThreads >> p.lg) + (threadIdx.x >> p.lg);
+  const int c0 = blockIdx.y * (tpr * U) + (threadIdx.x & (tpr - 1));
+  if (t >= a.T) return;
+  const uint8_t* src = static_cast<const uint8_t*>(a.tokens_in) + t * a.token_stride * p.elem;
+  V v[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int c = c0 + u * tpr;
+    if (c < p.chunks) v[u] = reinterpret_cast<const V*>(src)[c];
+  }
+  int r[kMaxTopK];
+  load_rows(a, t, r);
+#pragma unroll
+  for (int j = 0; j < kMaxTopK; ++j) {
+    if (r[j] < 0) continue;
+    V* dst = reinterpret_cast<V*>(static_cast<uint8_t*>(a.rows_out) + (int64_t)r[j] * a.rows_out_stride * p.elem);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int c = c0 + u * tpr;
+      if (c < p.chunks) dst[c] = v[u];
+    }
+  }
+}
+
+// A thread sums U chunks over the k rows of a token (w null: plain sum).
+template <int DT, int VB, int U>
+__global__ void __launch_bounds__(kRowThreads) unpermute_kernel(const __grid_constant__ RowsParams p) {
+  using C = Chunk<DT, VB>;
+  const RowsArgs& a = p.a;
+  const int tpr = 1 << p.lg;
+  const int64_t t = (int64_t)blockIdx.x * (kRowThreads >> p.lg) + (threadIdx.x >> p.lg);
+  const int c0 = blockIdx.y * (tpr * U) + (threadIdx.x & (tpr - 1));
+  if (t >= a.T) return;
+  int r[kMaxTopK];
+  load_rows(a, t, r);
+  float w[kMaxTopK];
+#pragma unroll
+  for (int j = 0; j < kMaxTopK; ++j) w[j] = j < a.k && a.w != nullptr ? a.w[t * a.k + j] : 1.0f;
+  C v[U][kMaxTopK];
+#pragma unroll
+  for (int j = 0; j < kMaxTopK; ++j) {
+    if (r[j] < 0) continue;
+    const uint8_t* src = static_cast<const uint8_t*>(a.rows_in) + (int64_t)r[j] * a.rows_in_stride * p.elem;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int c = c0 + u * tpr;
+      if (c < p.chunks) v[u][j].raw = reinterpret_cast<const typename Raw<VB>::T*>(src)[c];
+    }
+  }
+  uint8_t* dst = static_cast<uint8_t*>(a.tokens_out) + t * a.token_stride * p.elem;
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int c = c0 + u * tpr;
+    if (c >= p.chunks) continue;
+    C o;
+#pragma unroll
+    for (int i = 0; i < C::kN; ++i) {
+      float acc = 0.0f;
+#pragma unroll
+      for (int j = 0; j < kMaxTopK; ++j)
+        if (r[j] >= 0) acc = fmaf(w[j], Elem<DT>::to(v[u][j].e[i]), acc);
+      o.e[i] = Elem<DT>::from(acc);
+    }
+    reinterpret_cast<typename Raw<VB>::T*>(dst)[c] = o.raw;
+  }
+}
+
+// The threads of a token walk its row: every chunk of dout is read once, scaled into the k rows of
+// drows and multiplied into the k dot products, which are then summed over the threads (warp
+// shuffles, then shared memory in warp order: the same bits on every call).
+template <int DT, int VB, int LG>
+__global__ void __launch_bounds__(kRowThreads) unpermute_backward_kernel(const __grid_constant__ RowsParams p) {
+  using C = Chunk<DT, VB>;
+  using V = typename Raw<VB>::T;
+  constexpr int kTpr = 1 << LG;
+  const RowsArgs& a = p.a;
+  __shared__ float part[kRowThreads / 32][kMaxTopK];
+  const int64_t t = (int64_t)blockIdx.x * (kRowThreads >> LG) + (threadIdx.x >> LG);
+  const bool on = t < a.T;
+  int r[kMaxTopK];
+  float w[kMaxTopK], dot[kMaxTopK];
+#pragma unroll
+  for (int j = 0; j < kMaxTopK; ++j) r[j] = -1, dot[j] = 0.0f, w[j] = 1.0f;
+  if (on) {
+    load_rows(a, t, r);
+    if (a.w != nullptr) {
+#pragma unroll
+      for (int j = 0; j < kMaxTopK; ++j)
+        if (j < a.k) w[j] = a.w[t * a.k + j];
+    }
+    const uint8_t* src = static_cast<const uint8_t*>(a.tokens_in) + t * a.token_stride * p.elem;
+    for (int c = threadIdx.x & (kTpr - 1); c < p.chunks; c += kTpr) {
+      C d, v[kMaxTopK];
+      d.raw = reinterpret_cast<const V*>(src)[c];
+      if (a.dw != nullptr) {
+#pragma unroll
+        for (int j = 0; j < kMaxTopK; ++j)
+          if (r[j] >= 0)
+            v[j].raw = reinterpret_cast<const V*>(static_cast<const uint8_t*>(a.rows_in) +
+                                                  (int64_t)r[j] * a.rows_in_stride * p.elem)[c];
+      }
+      if (a.rows_out != nullptr) {
+#pragma unroll
+        for (int j = 0; j < kMaxTopK; ++j) {
+          if (r[j] < 0) continue;
+          C o;
+#pragma unroll
+          for (int i = 0; i < C::kN; ++i) o.e[i] = Elem<DT>::from(w[j] * Elem<DT>::to(d.e[i]));
+          reinterpret_cast<V*>(static_cast<uint8_t*>(a.rows_out) + (int64_t)r[j] * a.rows_out_stride * p.elem)[c] = o.raw;
+        }
+      }
+      if (a.dw != nullptr) {
+#pragma unroll
+        for (int j = 0; j < kMaxTopK; ++j) {
+          if (r[j] < 0) continue;
+#pragma unroll
+          for (int i = 0; i < C::kN; ++i) dot[j] = fmaf(Elem<DT>::to(d.e[i]), Elem<DT>::to(v[j].e[i]), dot[j]);
+        }
+      }
+    }
+  }
+  if (a.dw == nullptr) return;
+#pragma unroll
+  for (int j = 0; j < kMaxTopK; ++j) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) dot[j] += __shfl_xor_sync(0xffffffffu, dot[j], o);
+  }
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (LG == 5) {
+    if (on && lane == 0) {
+#pragma unroll
+      for (int j = 0; j < kMaxTopK; ++j)
+        if (j < a.k) a.dw[t * a.k + j] = dot[j];
+    }
+    return;
+  }
+  if (lane == 0) {
+#pragma unroll
+    for (int j = 0; j < kMaxTopK; ++j) part[warp][j] = dot[j];
+  }
+  __syncthreads();
+  if (on && threadIdx.x < a.k) {
+    float sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kRowThreads / 32; ++i) sum += part[i][threadIdx.x];
+    a.dw[t * a.k + threadIdx.x] = sum;
+  }
+}
+
+// One warp per token: every lane forms the k gradients and writes whole vectors of the row, each
+// column the sum of the slots that selected it (a column no slot selected gets 0).
+template <int V>
+__global__ void __launch_bounds__(kRowThreads) route_backward_kernel(RouteBackwardArgs a) {
+  const int64_t t = (int64_t)blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5);
+  if (t >= a.T) return;
+  float w[kMaxTopK], g[kMaxTopK];
+  int id[kMaxTopK];
+  float mean = 0.0f;
+#pragma unroll
+  for (int j = 0; j < kMaxTopK; ++j) {
+    id[j] = -1;
+    w[j] = g[j] = 0.0f;
+    if (j < a.k) {
+      id[j] = a.ids[t * a.k + j];
+      w[j] = a.w[t * a.k + j];
+      g[j] = a.dw[t * a.k + j];
+      mean = fmaf(w[j], g[j], mean);
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < kMaxTopK; ++j) g[j] = w[j] * (g[j] - mean);
+  float* row = a.dlogits + t * a.E;
+  for (int c = (threadIdx.x & 31) * V; c < a.E; c += 32 * V) {
+    float o[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      o[i] = 0.0f;
+#pragma unroll
+      for (int j = 0; j < kMaxTopK; ++j)
+        if (id[j] == c + i) o[i] += g[j];
+    }
+    if (V == 4) *reinterpret_cast<float4*>(row + c) = make_float4(o[0], o[1 % V], o[2 % V], o[3 % V]);
+    else row[c] = o[0];
+  }
+}
+
+// The widest access: the largest power of two up to 16 dividing every address, stride and the row.
+int access_bytes(const RowsArgs& a) {
+  const int64_t es = dtype_bytes(a.dtype);
+  uint64_t bits = 16 | (uint64_t)(a.H * es);
+  const auto with = [&](const void* ptr, int64_t stride) {
+    if (ptr != nullptr) bits |= reinterpret_cast<uintptr_t>(ptr) | (uint64_t)(stride * es);
+  };
+  with(a.tokens_in, a.token_stride);
+  with(a.tokens_out, a.token_stride);
+  with(a.rows_in, a.rows_in_stride);
+  with(a.rows_out, a.rows_out_stride);
+  return (int)(bits & (~bits + 1));
+}
+
+// Threads per row: the power of two that leaves each thread about U chunks, at most a block.
+int row_threads_log2(int chunks, int U) {
+  int lg = 0;
+  while (lg < 8 && (U << lg) < chunks) ++lg;
+  return lg;
+}
+
+template <int U>
+dim3 row_grid(const RowsArgs& a, int chunks, int lg) {
+  const int64_t per = kRowThreads >> lg;
+  return dim3((unsigned)((a.T + per - 1) / per), (unsigned)((chunks + (U << lg) - 1) / (U << lg)));
+}
+
+template <int VB, int U>
+cudaError_t permute_vb(const RowsArgs& a, cudaStream_t s) {
+  RowsParams p{a, a.H * dtype_bytes(a.dtype) / VB, 0, dtype_bytes(a.dtype)};
+  p.lg = row_threads_log2(p.chunks, U);
+  permute_kernel<VB, U><<<row_grid<U>(a, p.chunks, p.lg), kRowThreads, 0, s>>>(p);
+  return cudaGetLastError();
+}
+
+template <int DT, int VB>
+cudaError_t unpermute_vb(const RowsArgs& a, cudaStream_t s) {
+  constexpr int U = VB >= 8 ? 1 : 4;
+  RowsParams p{a, a.H * dtype_bytes(a.dtype) / VB, 0, dtype_bytes(a.dtype)};
+  p.lg = row_threads_log2(p.chunks, U);
+  unpermute_kernel<DT, VB, U><<<row_grid<U>(a, p.chunks, p.lg), kRowThreads, 0, s>>>(p);
+  return cudaGetLastError();
+}
+
+template <int DT, int VB>
+cudaError_t backward_vb(const RowsArgs& a, cudaStream_t s) {
+  RowsParams p{a, a.H * dtype_bytes(a.dtype) / VB, 0, dtype_bytes(a.dtype)};
+  if (p.chunks <= 64) {  // short rows: a warp each
+    const unsigned blocks = (unsigned)((a.T + kRowThreads / 32 - 1) / (kRowThreads / 32));
+    unpermute_backward_kernel<DT, VB, 5><<<blocks, kRowThreads, 0, s>>>(p);
+  } else {
+    unpermute_backward_kernel<DT, VB, 8><<<(unsigned)a.T, kRowThreads, 0, s>>>(p);
+  }
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_permute(const RowsArgs& a, cudaStream_t s) {
+  if (a.T == 0 || a.R == 0) return cudaSuccess;
+  switch (access_bytes(a)) {
+    case 16: return permute_vb<16, 4>(a, s);
+    case 8: return permute_vb<8, 4>(a, s);
+    case 4: return permute_vb<4, 8>(a, s);
+    case 2: return permute_vb<2, 8>(a, s);
+    default: return permute_vb<1, 8>(a, s);
+  }
+}
+
+cudaError_t launch_unpermute(const RowsArgs& a, cudaStream_t s) {
+  if (a.T == 0) return cudaSuccess;
+  const int vb = access_bytes(a);
+  if (a.dtype == kDtBf16) {
+    if (vb == 16) return unpermute_vb<kDtBf16, 16>(a, s);
+    if (vb == 8) return unpermute_vb<kDtBf16, 8>(a, s);
+    if (vb == 4) return unpermute_vb<kDtBf16, 4>(a, s);
+    return unpermute_vb<kDtBf16, 2>(a, s);
+  }
+  if (a.dtype == kDtF16) {
+    if (vb == 16) return unpermute_vb<kDtF16, 16>(a, s);
+    if (vb == 8) return unpermute_vb<kDtF16, 8>(a, s);
+    if (vb == 4) return unpermute_vb<kDtF16, 4>(a, s);
+    return unpermute_vb<kDtF16, 2>(a, s);
+  }
+  if (vb == 16) return unpermute_vb<kDtF32, 16>(a, s);
+  if (vb == 8) return unpermute_vb<kDtF32, 8>(a, s);
+  return unpermute_vb<kDtF32, 4>(a, s);
+}
+
+cudaError_t launch_unpermute_backward(const RowsArgs& a, cudaStream_t s) {
+  if (a.T == 0 || (a.rows_out == nullptr && a.dw == nullptr)) return cudaSuccess;
+  const int vb = access_bytes(a);
+  if (a.dtype == kDtBf16) {
+    if (vb == 16) return backward_vb<kDtBf16, 16>(a, s);
+    if (vb == 8) return backward_vb<kDtBf16, 8>(a, s);
+    if (vb == 4) return backward_vb<kDtBf16, 4>(a, s);
+    return backward_vb<kDtBf16, 2>(a, s);
+  }
+  if (a.dtype == kDtF16) {
+    if (vb == 16) return backward_vb<kDtF16, 16>(a, s);
+    if (vb == 8) return backward_vb<kDtF16, 8>(a, s);
+    if (vb == 4) return backward_vb<kDtF16, 4>(a, s);
+    return backward_vb<kDtF16, 2>(a, s);
+  }
+  if (vb == 16) return backward_vb<kDtF32, 16>(a, s);
+  if (vb == 8) return backward_vb<kDtF32, 8>(a, s);
+  return backward_vb<kDtF32, 4>(a, s);
+}
+
+cudaError_t launch_route_backward(const RouteBackwardArgs& a, cudaStream_t s) {
+  if (a.T == 0) return cudaSuccess;
+  const unsigned blocks = (unsigned)((a.T + kRowThreads / 32 - 1) / (kRowThreads / 32));
+  if (a.E % 4 == 0 && reinterpret_cast<uintptr_t>(a.dlogits) % 16 == 0)
+    route_backward_kernel<4><<<blocks, kRowThreads, 0, s>>>(a);
+  else
+    route_backward_kernel<1><<<blocks, kRowThreads, 0, s>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace moe

@@ -7,39 +7,16 @@
 #include <cstring>
 #include <mutex>
 
+#include "api_common.h"
 #include "moe_internal.h"
 #include "moe_topk.h"
 
+namespace moe {
 namespace {
-
-using moe::kMaxExperts;
-using moe::kMaxTopK;
-using moe::kRowTile;
-using moe::kTokensPerChunk;
 
 constexpr uint64_t kDefaultTimeoutNs = 4000000000ull;  // bound of every in-kernel wait
 
-size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
-bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
-moe_status_t check_sizes(int64_t T, int H, int I, int E, int k, moe_act_fmt_t fmt) {
-  if (T < 0 || H <= 0 || I <= 0 || E <= 0 || k <= 0) return MOE_ERR_INVALID_ARG;
-  if (fmt != MOE_ACT_MXFP8 && fmt != MOE_ACT_MXFP4) return MOE_ERR_INVALID_ARG;
-  if (k > E) return MOE_ERR_INVALID_ARG;
-  if (k > kMaxTopK || E > kMaxExperts) return MOE_ERR_UNSUPPORTED_SHAPE;
-  if (H % 128 != 0 || I % 128 != 0) return MOE_ERR_UNSUPPORTED_SHAPE;
-  if (H > 65536 || I > 65536) return MOE_ERR_UNSUPPORTED_SHAPE;
-  // row indices are int32 on the device: keep the padded row space below 2^31
-  const int64_t R = T * (int64_t)k;
-  if (T > (int64_t(1) << 24) || R + (int64_t)127 * std::min<int64_t>(E, R) > (int64_t(1) << 30))
-    return MOE_ERR_UNSUPPORTED_SHAPE;
-  return MOE_OK;
-}
-
-struct DeviceInfo {
-  int ok = -1;  // -1 unknown, 0 unsupported, 1 sm_103
-  int num_sms = 0;
-};
+}  // namespace
 
 moe_status_t device_info(DeviceInfo* out) {
   static DeviceInfo cache[64];
@@ -60,6 +37,61 @@ moe_status_t device_info(DeviceInfo* out) {
   }
   *out = d;
   return d.ok == 1 ? MOE_OK : MOE_ERR_UNSUPPORTED_DEVICE;
+}
+
+uint64_t wait_timeout_ns() {
+  static uint64_t v = 0;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    v = kDefaultTimeoutNs;
+    if (const char* s = getenv("MOE_WAIT_TIMEOUT_NS")) {
+      const unsigned long long x = strtoull(s, nullptr, 10);
+      if (x > 0) v = x;
+    }
+  });
+  return v;
+}
+
+// Test hook for the failure path: MOE_TEST_STALL_PRODUCER=1 makes the GEMM producers issue
+// nothing, so the first wait of the MMA warp expires after MOE_WAIT_TIMEOUT_NS and the kernel
+// reports MOE_ERR_DEVICE_TIMEOUT through the workspace status words (no fault, no hang).
+int test_stall_producer() {
+  static int v = 0;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    if (const char* s = getenv("MOE_TEST_STALL_PRODUCER")) v = atoi(s) != 0;
+  });
+  return v;
+}
+
+}  // namespace moe
+
+namespace {
+
+using moe::aligned;
+using moe::device_info;
+using moe::DeviceInfo;
+using moe::test_stall_producer;
+using moe::wait_timeout_ns;
+using moe::kMaxExperts;
+using moe::kMaxTopK;
+using moe::kRowTile;
+using moe::kTokensPerChunk;
+
+size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
+
+moe_status_t check_sizes(int64_t T, int H, int I, int E, int k, moe_act_fmt_t fmt) {
+  if (T < 0 || H <= 0 || I <= 0 || E <= 0 || k <= 0) return MOE_ERR_INVALID_ARG;
+  if (fmt != MOE_ACT_MXFP8 && fmt != MOE_ACT_MXFP4) return MOE_ERR_INVALID_ARG;
+  if (k > E) return MOE_ERR_INVALID_ARG;
+  if (k > kMaxTopK || E > kMaxExperts) return MOE_ERR_UNSUPPORTED_SHAPE;
+  if (H % 128 != 0 || I % 128 != 0) return MOE_ERR_UNSUPPORTED_SHAPE;
+  if (H > 65536 || I > 65536) return MOE_ERR_UNSUPPORTED_SHAPE;
+  // row indices are int32 on the device: keep the padded row space below 2^31
+  const int64_t R = T * (int64_t)k;
+  if (T > (int64_t(1) << 24) || R + (int64_t)127 * std::min<int64_t>(E, R) > (int64_t(1) << 30))
+    return MOE_ERR_UNSUPPORTED_SHAPE;
+  return MOE_OK;
 }
 
 moe_status_t layout(int64_t T, int H, int I, int E, int k, moe_act_fmt_t fmt, moe_workspace_layout_t* L) {
@@ -107,36 +139,6 @@ moe_status_t layout(int64_t T, int H, int I, int E, int k, moe_act_fmt_t fmt, mo
   L->nchunk = nchunk;
   return MOE_OK;
 }
-
-uint64_t wait_timeout_ns() {
-  static uint64_t v = 0;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    v = kDefaultTimeoutNs;
-    if (const char* s = getenv("MOE_WAIT_TIMEOUT_NS")) {
-      const unsigned long long x = strtoull(s, nullptr, 10);
-      if (x > 0) v = x;
-    }
-  });
-  return v;
-}
-
-// Test hook for the failure path: MOE_TEST_STALL_PRODUCER=1 makes the GEMM producers issue
-// nothing, so the first wait of the MMA warp expires after MOE_WAIT_TIMEOUT_NS and the kernel
-// reports MOE_ERR_DEVICE_TIMEOUT through the workspace status words (no fault, no hang).
-int test_stall_producer() {
-  static int v = 0;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    if (const char* s = getenv("MOE_TEST_STALL_PRODUCER")) v = atoi(s) != 0;
-  });
-  return v;
-}
-
-#define MOE_CUDA_TRY(expr)                          \
-  do {                                              \
-    if ((expr) != cudaSuccess) return MOE_ERR_CUDA; \
-  } while (0)
 
 // The forward's launch sequence.  With `ev` (kForwardKernels + 1 events) an event is
 // recorded before the first kernel and after every kernel, for per-kernel timing.

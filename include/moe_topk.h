@@ -416,6 +416,125 @@ moe_status_t moe_profile_forward(moe_act_fmt_t fmt, const void* x_bf16, const fl
                                  int k, void* workspace, size_t workspace_bytes, void* stream,
                                  int prepacked_scales, int schedule, float* kernel_us);
 
+/* ------------------------------------------------------------------------------------------
+ * Expert rows and FP8 experts as single operators, with their gradients
+ *
+ * The steps of the layer for callers that build their own: token rows to expert rows and back on
+ * the permutation of moe_sort_by_expert, experts kept as FP8 codes with one fp32 scale per block
+ * of 128, and the gradients that train a router (and what lies before it) through such experts:
+ *   moe_topk_route, moe_sort_by_expert, moe_permute_quantize_fp8_block, moe_gemm_fp8_block,
+ *   (activation, moe_quantize_fp8_block, moe_gemm_fp8_block,) moe_unpermute; then backward
+ *   moe_unpermute_backward, moe_quantize_fp8_block, moe_gemm_fp8_block_dgrad,
+ *   moe_permute_backward, moe_topk_route_backward.
+ * The rules of this header hold (device pointers, caller's buffers, argument checks before any
+ * launch, one kernel per call, capturable).  Outputs must not overlap inputs.
+ *
+ * Common arguments
+ *   inv      int32 [T, k]: the expert row of slot j of token t.  The `inv` of moe_sort_by_expert is
+ *            one; any other injective map serves.  A value outside [0, R) marks a dropped pair
+ *            (capacity limits): it is neither read nor written and contributes nothing.
+ *   R        rows of the expert-row matrices, 0 <= R <= 2^30; T <= 2^24, 1 <= k <= 8
+ *   H, K, N  columns, at most 65536.  Matrices are row-major with unit column stride; *_stride is
+ *            the row stride in elements (at least the columns).  Any width and alignment of the
+ *            element's size is served; rows on 16-byte boundaries are the fast case.
+ */
+typedef enum {
+  MOE_DTYPE_BF16 = 0,
+  MOE_DTYPE_F16 = 1,
+  MOE_DTYPE_F32 = 2,
+  MOE_DTYPE_U8 = 3 /* moe_permute only: rows of bytes (codes) */
+} moe_dtype_t;
+
+/*
+ * rows[inv[t, j], :] = x[t, :] for every kept pair; rows that no pair names stay as they are.
+ *   x [T, H] in, rows [R, H] out, both of `dtype`
+ */
+moe_status_t moe_permute(const void* x, int64_t x_stride, moe_dtype_t dtype, const int32_t* inv, int64_t T, int H,
+                         int k, void* rows, int64_t rows_stride, int64_t R, void* stream);
+
+/* Its gradient: d_x[t] = sum_j d_rows[inv[t, j]], fp32 in slot order, rounded once; a token whose
+ * pairs were all dropped gets zeros.  BF16, F16 or F32. */
+moe_status_t moe_permute_backward(const void* d_rows, int64_t d_rows_stride, int64_t R, moe_dtype_t dtype,
+                                  const int32_t* inv, int64_t T, int H, int k, void* d_x, int64_t d_x_stride,
+                                  void* stream);
+
+/*
+ * out[t] = sum_j topk_w[t, j] * rows[inv[t, j]], fp32 in slot order, rounded once; a token whose
+ * pairs were all dropped gets zeros.
+ *   rows [R, H] in, out [T, H] out (BF16, F16 or F32), topk_w fp32 [T, k]
+ */
+moe_status_t moe_unpermute(const void* rows, int64_t rows_stride, int64_t R, moe_dtype_t dtype, const int32_t* inv,
+                           const float* topk_w, int64_t T, int H, int k, void* out, int64_t out_stride, void* stream);
+
+/*
+ * Its gradients: d_rows[inv[t, j]] = topk_w[t, j] * d_out[t] (rows that no pair names stay as they
+ * are) and d_topk_w[t, j] = <d_out[t], rows[inv[t, j]]> in fp32 (0 for a dropped pair).
+ *   d_out [T, H], rows [R, H], d_rows [R, H] of `dtype` (BF16, F16 or F32); d_topk_w fp32 [T, k].
+ *   Either result may be NULL and is then not computed; rows is read for d_topk_w only.
+ */
+moe_status_t moe_unpermute_backward(const void* d_out, int64_t d_out_stride, const void* rows, int64_t rows_stride,
+                                    int64_t R, moe_dtype_t dtype, const int32_t* inv, const float* topk_w, int64_t T,
+                                    int H, int k, void* d_rows, int64_t d_rows_stride, float* d_topk_w, void* stream);
+
+/*
+ * Gradient of moe_topk_route's weights: with g_j = topk_w[t, j] * (d_topk_w[t, j] -
+ * sum_i topk_w[t, i] * d_topk_w[t, i]), d_logits[t, topk_ids[t, j]] = g_j and 0 in the other columns
+ * (an id outside [0, E) has none).
+ *   topk_ids int32, topk_w, d_topk_w fp32 [T, k] in; d_logits fp32 [T, E] out, written whole
+ */
+moe_status_t moe_topk_route_backward(const int32_t* topk_ids, const float* topk_w, const float* d_topk_w, int64_t T,
+                                     int E, int k, float* d_logits, void* stream);
+
+/*
+ * Rows to FP8: E4M3 codes with one fp32 scale per block of block_rows x 128 elements, block_rows
+ * = 1 (activations, gradients) or 128 (weights; for [E, N, K] weights with N % 128 == 0 pass E*N
+ * rows, else one expert a call).  With m the block's largest finite magnitude: scale = m / 448, code = the E4M3 value
+ * nearest to 448 x / m, ties to even (fp32 x within 2^-20 of a tie: either neighbour).  m < 2^-100:
+ * scale 0, signed-zero codes.  A non-finite x becomes the NaN code.
+ *   x      [rows, K] of `dtype` (BF16, F16 or F32)
+ *   codes  u8 [rows, K] out; scales fp32 [ceil(rows / block_rows), ceil(K / 128)] out
+ */
+moe_status_t moe_quantize_fp8_block(const void* x, int64_t x_stride, moe_dtype_t dtype, int64_t rows, int K,
+                                    int block_rows, uint8_t* codes, float* scales, void* stream);
+
+/* moe_permute and moe_quantize_fp8_block (block_rows = 1) in one pass: the codes and scales of
+ * token t go to rows inv[t, j] of codes u8 [R, K] and scales fp32 [R, ceil(K / 128)]. */
+moe_status_t moe_permute_quantize_fp8_block(const void* x, int64_t x_stride, moe_dtype_t dtype, const int32_t* inv,
+                                            int64_t T, int K, int k, uint8_t* codes, float* scales, int64_t R,
+                                            void* stream);
+
+/*
+ * Matrix product in FP8 with a scale for each block of 128, over groups of rows:
+ *   out[r, n] = sum_b x_scale[r, b] * w_scale[e, n / 128, b] * sum_{c in block b} x[r, c] * w[e, n, c]
+ * for the rows offsets[e] <= r < offsets[e + 1] of expert e.  The inner sum of a block runs on the
+ * tensor cores (exact products, fp32 accumulation), the sum over blocks in fp32, rounded once.
+ *   x        E4M3 codes u8 [M, K], 16-byte aligned; x_scale fp32 [M, ceil(K / 128)]
+ *   w        E4M3 codes u8 [E, N, K], 16-byte aligned; w_scale fp32 [E, ceil(N / 128), ceil(K / 128)]
+ *   offsets  int64 [E + 1], device, non-decreasing, as moe_sort_by_expert writes it (values are
+ *            clamped to [0, M]; rows that no group holds are not written); or NULL with E = 1: all
+ *            M rows (a shared expert, a dense projection)
+ *   out      [M, N] BF16, F16 or F32
+ *   K % 16 == 0, E <= 1024; N and M are any
+ *   workspace  device, 256-byte aligned, >= moe_gemm_fp8_block_workspace_bytes(M, N, K, E); holds the
+ *            status words read by moe_read_device_status, reset by every call with M > 0
+ */
+size_t moe_gemm_fp8_block_workspace_bytes(int64_t M, int N, int K, int E);
+moe_status_t moe_gemm_fp8_block(const uint8_t* x, const float* x_scale, const uint8_t* w, const float* w_scale,
+                                const int64_t* offsets, int64_t M, int N, int K, int E, void* out,
+                                moe_dtype_t out_dtype, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Its gradient with respect to x, from the same weights:
+ *   dx[r, c] = sum_b dy_scale[r, b] * w_scale[e, b, c / 128] * sum_{n in block b} dy[r, n] * w[e, n, c]
+ *   dy       E4M3 codes u8 [M, N] with dy_scale fp32 [M, ceil(N / 128)], as moe_quantize_fp8_block
+ *            (block_rows = 1) writes them;  dx [M, K] BF16, F16 or F32
+ * K % 16 == 0 and N % 16 == 0; everything else as above.  (The codes of the weights have no
+ * gradient: such experts are trained through, not trained.)
+ */
+moe_status_t moe_gemm_fp8_block_dgrad(const uint8_t* dy, const float* dy_scale, const uint8_t* w, const float* w_scale,
+                                      const int64_t* offsets, int64_t M, int N, int K, int E, void* dx,
+                                      moe_dtype_t dx_dtype, void* workspace, size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
