@@ -1,93 +1,478 @@
-// gemm_block.cu -- the product in FP8 with a scale for each block of 128:
+// gemm_block.cu -- the product in FP8 with a scale for each block of 128, on CTA pairs:
 //   out[r, n] = sum_b sx[r, b] sw[e, n/128, b] sum_{c in block b} x[r, c] w[e, n, c]
-// and its gradient with respect to the input, where the reduction runs over the weight's rows.
+// and its gradient with respect to the input, where the reduction runs over the weight's rows:
+//   out[r, c] = sum_b sx[r, b] sw[e, b, c/128] sum_{n in block b} x[r, n] w[e, n, c].
 // Rows [offsets[e], offsets[e+1]) of x belong to expert e.
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
-#include <cuda_fp8.h>
+//
+// The scales are general fp32 numbers that change with every block of the reduction, so the tensor
+// cores sum one block (128 products, tcgen05.mma kind::f8f6f4, exact products, fp32 accumulator)
+// and the sum over blocks runs in fp32 registers: each block's accumulator is read from TMEM and
+// added with one multiply-add by sx * sw.  TMEM holds two block accumulators, so the MMAs of the
+// next block run while the last one is read.
+//
+// A tile is 256 rows of one expert by 256 output columns on a cluster of two CTAs (cta_group::2, M =
+// 256): each CTA loads its own 128 rows of x and 128 of the 256 weight rows (or columns) of a
+// 128-wide block of the reduction, 32 KiB a stage.  A single CTA's 128 x 256 tile would need 48 KiB a
+// stage, and shared memory's bandwidth (TMA writes plus the MMA's reads), not the MMA, would bound
+// it.  The weight tile of the gradient is the same box of the same matrix, read by the MMA with its
+// reduction along rows (MN-major descriptor): no transposed copy of the weights exists.
+//   warp 0     TMA producer (converged, copies issued by an elected lane)
+//   warp 1     TMEM owner; in the even CTA the MMA issuer for both
+//   warps 4-11 sums: a thread owns one row and 128 of the 256 columns (one scale block) in 128 fp32
+//              registers; warps whose 32 rows are past the group's end read nothing.  The two
+//              warpgroups take 224 registers a thread, the first warpgroup keeps 56 (setmaxnreg;
+//              128 x 56 + 256 x 224 = 384 x 168, what the block is launched with)
+// Tiles run expert by expert, row tiles fastest, so the pairs running side by side share weight
+// tiles in L2.  Every wait is bounded as in gemm_pair.cu: on expiry the status word records
+// MOE_ERR_DEVICE_TIMEOUT and both CTAs drain before TMEM is freed.
+#include <cuda.h>
 
 #include <algorithm>
+#include <atomic>
 
-#include "expert_internal.h"
+#include "gemm_block_common.cuh"
+#include "gemm_common.cuh"
 
 namespace moe {
 namespace {
 
-constexpr int kT = 64;  // tile: 64 rows x 64 output columns, 16 x 16 threads of 4 x 4
+constexpr int kBThreads = 384;   // 168 registers a thread at launch
+constexpr int kBFirstEpiWarp = 4;
+constexpr int kBCtlRegs = 56, kBEpiRegs = 224;
+static_assert(128 * kBCtlRegs + 256 * kBEpiRegs <= 384 * 168, "register split");
+constexpr int kBEpiWarps = 8;
+constexpr int kBStages = 6;
+constexpr int kBTileRows = 256;                     // rows of a pair tile
+constexpr int kBTileCols = 256;                     // output columns of a pair tile
+constexpr int kBHalfBytes = 128 * 128;              // one operand of a stage in one CTA
+constexpr int kBStageBytes = 2 * kBHalfBytes;
+constexpr int kBOutOff = kBStages * kBStageBytes;   // per-warp staging of unaligned output rows
+constexpr int kBOutBytes = 32 * 16 * 4;             // 32 rows x 16 columns of fp32
+constexpr int kBBarOff = kBOutOff + kBEpiWarps * kBOutBytes;
+constexpr int kBTabOff = kBBarOff + 256;            // per expert: first row, rows, first tile
+constexpr int kBSmemBytes = kBTabOff + 3 * 4 * (kMaxExperts + 1) + 1024;
+static_assert(kBSmemBytes <= 232448, "block GEMM shared memory");
+static_assert(8 * (2 * kBStages + 5) + 8 <= 256, "block GEMM barriers");
 
-__device__ __forceinline__ float e4m3(uint8_t v) {
-  __nv_fp8_e4m3 t;
-  t.__x = v;
-  return (float)t;
+struct BlockParams {  // 64-byte aligned through its CUtensorMap members
+  CUtensorMap tmap_x;  // codes [M, reduction], box 128 B x 128 rows
+  CUtensorMap tmap_w;  // codes [E, N, K], box 128 B x 128 rows x 1
+  GemmBlockArgs a;
+  int out_vec;         // output rows start on 32-byte boundaries
+};
+
+// Instruction descriptor of kind::f8f6f4: fp32 accumulator (bit 4), E4M3 operands, B read along its
+// rows (bit 16) for the gradient, N / 8 at [17, 23), M / 16 at [24, 29).
+__device__ __forceinline__ uint32_t block_idesc(bool dgrad) {
+  return (1u << 4) | ((dgrad ? 1u : 0u) << 16) | ((uint32_t)(kBTileCols >> 3) << 17) |
+         ((uint32_t)(kBTileRows >> 4) << 24);
 }
 
-__device__ __forceinline__ void store_out(void* out, int dtype, int64_t i, float v) {
-  if (dtype == kDtBf16) static_cast<__nv_bfloat16*>(out)[i] = __float2bfloat16_rn(v);
-  else if (dtype == kDtF16) static_cast<__half*>(out)[i] = __float2half_rn(v);
-  else static_cast<float*>(out)[i] = v;
+__device__ __forceinline__ void tc_mma_pair_f8(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                               uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
 }
 
-__global__ void __launch_bounds__(256) gemm_block_plain_kernel(GemmBlockArgs a) {
-  __shared__ float xs[32][kT + 1], ws[32][kT + 1];
-  if (blockIdx.x + blockIdx.y + blockIdx.z == 0 && threadIdx.x < 8) a.status[threadIdx.x] = 0;
-  const int e = blockIdx.z;
-  const int red = a.dgrad ? a.N : a.K, cols = a.dgrad ? a.K : a.N;
-  const int64_t begin = a.offsets ? min(max(a.offsets[e], (int64_t)0), a.M) : 0;
-  const int64_t end = a.offsets ? min(max(a.offsets[e + 1], begin), a.M) : a.M;
-  const int n0 = blockIdx.x * kT, tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  const int NB = (a.N + 127) / 128, KB = (a.K + 127) / 128, RB = (red + 127) / 128;
-  const uint8_t* w = a.w + (int64_t)e * a.N * a.K;
-  const float* wsc = a.w_scale + (int64_t)e * NB * KB;
-  for (int64_t r0 = begin + (int64_t)blockIdx.y * kT; r0 < end; r0 += (int64_t)gridDim.y * kT) {
-    float tot[4][4] = {};
-    for (int b = 0; b < RB; ++b) {
-      float acc[4][4] = {};
-      for (int c0 = b * 128; c0 < min(red, b * 128 + 128); c0 += 32) {
-        for (int i = threadIdx.x; i < 32 * kT; i += 256) {
-          const int c = c0 + (i & 31), r = i >> 5;
-          xs[i & 31][r] = r0 + r < end && c < red ? e4m3(a.x[(r0 + r) * red + c]) : 0.0f;
+// Two fp32 multiply-adds in one instruction: acc += v * s, element by element.
+__device__ __forceinline__ void fma2(float& a0, float& a1, float v0, float v1, uint64_t s2) {
+  uint64_t a, v;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(a) : "f"(a0), "f"(a1));
+  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(v0), "f"(v1));
+  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(a) : "l"(v), "l"(s2));
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a0), "=f"(a1) : "l"(a));
+}
+
+__device__ __forceinline__ void st_global_v8(void* p, const uint32_t (&w)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+               "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
+
+// bounded_wait for the warps that hold their sums in registers: inlined, because a call would have
+// to save the 128 sums around it.  Warp-uniform; false when the CTA aborts or the limit passes.
+__device__ __forceinline__ bool sums_wait(uint32_t bar, uint32_t parity, const Sync& s) {
+  bool ok = mbar_try_wait(bar, parity);
+  uint64_t t0 = 0;
+  for (uint32_t it = 1; !__all_sync(0xffffffffu, ok); ++it) {
+    ok = mbar_try_wait(bar, parity);
+    if ((it & 63u) == 0) {
+      const uint64_t now = clock64();
+      if (t0 == 0) t0 = now;
+      const bool late = now - t0 > 2 * s.timeout_ns;
+      if (__any_sync(0xffffffffu, !ok && late) && !*s.abort_flag) {
+        *s.abort_flag = 1;
+        atomicOr(s.status, kStatusTimeout);
+        if (threadIdx.x % 32 == 0 && atomicCAS(s.status + 1, 0u, 1u) == 0u) {
+          s.status[2] = (bar - s.bar0) / 8;
+          s.status[3] = parity;
+          s.status[4] = blockIdx.x;
+          s.status[5] = threadIdx.x / 32;
+          s.status[6] = (uint32_t)((now - t0) / 2000);
         }
-        for (int i = threadIdx.x; i < 32 * kT; i += 256) {
-          const int c = a.dgrad ? i / kT : i & 31, n = a.dgrad ? i % kT : i >> 5;
-          const bool in = c0 + c < red && n0 + n < cols;
-          ws[c][n] = in ? e4m3(a.dgrad ? w[(int64_t)(c0 + c) * a.K + n0 + n] : w[(int64_t)(n0 + n) * a.K + c0 + c]) : 0.0f;
-        }
-        __syncthreads();
-        for (int c = 0; c < 32; ++c)
-          for (int i = 0; i < 4; ++i)
-            for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(xs[c][ty * 4 + i], ws[c][tx * 4 + j], acc[i][j]);
-        __syncthreads();
       }
-      for (int i = 0; i < 4; ++i) {
-        const int64_t r = r0 + ty * 4 + i;
-        if (r >= end) continue;
-        const float sx = a.x_scale[r * RB + b];
-        for (int j = 0; j < 4; ++j) {
-          const int n = n0 + tx * 4 + j;
-          if (n >= cols) continue;
-          const float sw = a.dgrad ? wsc[b * KB + n / 128] : wsc[(n / 128) * KB + b];
-          tot[i][j] = fmaf(acc[i][j], sx * sw, tot[i][j]);
+      if (__any_sync(0xffffffffu, *s.abort_flag != 0)) return false;
+    }
+  }
+  return true;
+}
+
+struct BlockTile {
+  int e, mt, nt;
+};
+__device__ __forceinline__ BlockTile block_tile(int64_t tile, const int32_t* base, int E, int NT) {
+  int lo = 0, hi = E - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if ((int64_t)base[mid] * NT <= tile) lo = mid;
+    else hi = mid - 1;
+  }
+  const int mt_e = base[lo + 1] - base[lo];
+  const uint32_t local = (uint32_t)(tile - (int64_t)base[lo] * NT);
+  return {lo, (int)(local % (uint32_t)mt_e), (int)(local / (uint32_t)mt_e)};
+}
+
+template <bool DGRAD>
+__global__ void __launch_bounds__(kBThreads, 1) gemm_block_pair_kernel(const __grid_constant__ BlockParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sbase = smem_u32(smem);
+  const uint32_t bar0 = sbase + kBBarOff;
+  auto full_bar = [&](int s) { return bar0 + 8u * s; };
+  auto empty_bar = [&](int s) { return bar0 + 8u * (kBStages + s); };
+  auto tmem_full = [&](int b) { return bar0 + 8u * (2 * kBStages + b); };
+  auto tmem_empty = [&](int b) { return bar0 + 8u * (2 * kBStages + 2 + b); };
+  const uint32_t drain_bar = bar0 + 8u * (2 * kBStages + 4);
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + kBBarOff + 8 * (2 * kBStages + 5));
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
+  int32_t* row_begin = reinterpret_cast<int32_t*>(smem + kBTabOff);
+  int32_t* row_count = row_begin + kMaxExperts + 1;
+  int32_t* tile_base = row_count + kMaxExperts + 1;
+
+  const GemmBlockArgs& a = p.a;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const uint32_t rank = cluster_ctarank();
+  const bool leader = rank == 0;
+  const int E = a.E;
+
+  if (blockIdx.x == 0 && threadIdx.x < 8) a.status[threadIdx.x] = 0;
+  for (int e = threadIdx.x; e < E; e += kBThreads) {
+    const RowSpan sp = group_rows(a.offsets, e, a.M);
+    row_begin[e] = (int32_t)sp.begin;
+    row_count[e] = (int32_t)sp.rows;
+  }
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kBStages; ++s) {
+      mbar_init(full_bar(s), 1);   // expect_tx arrival of the even CTA's producer
+      mbar_init(empty_bar(s), 1);  // the pair's MMA commit
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(tmem_full(b), 1);
+      mbar_init(tmem_empty(b), 2 * kBEpiWarps);  // warps of both CTAs
+    }
+    mbar_init(drain_bar, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+    prefetch_tensormap(&p.tmap_x);
+    prefetch_tensormap(&p.tmap_w);
+  }
+  __syncthreads();
+  if (warp == 2) {  // exclusive prefix of the row tiles per expert
+    int running = 0;
+    for (int e0 = 0; e0 < E; e0 += 32) {
+      const int e = e0 + lane;
+      const int v = e < E ? (row_count[e] + kBTileRows - 1) / kBTileRows : 0;
+      int incl = v;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int n = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += n;
+      }
+      if (e < E) tile_base[e] = running + incl - v;
+      running += __shfl_sync(0xffffffffu, incl, 31);
+    }
+    if (lane == 0) tile_base[E] = running;
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(smem_u32(tmem_holder), 2 * kBTileCols);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  cluster_sync();  // barriers initialised in both CTAs before any remote arrival
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_holder;
+
+  const Sync sync{abort_flag, a.status, a.timeout_ns, bar0};
+  const int red = DGRAD ? a.N : a.K, cols = DGRAD ? a.K : a.N;
+  const int RB = (red + kFp8Block - 1) / kFp8Block;
+  const int NT = (cols + kBTileCols - 1) / kBTileCols;
+  const int64_t total_tiles = (int64_t)tile_base[E] * NT;
+  const int64_t first_tile = cluster_index(), tile_step = cluster_count();
+
+  if (warp < kBFirstEpiWarp) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kBCtlRegs));
+    if (warp == 0) {
+      // ------------------------------------------------------------------ producer
+      const uint32_t lfull0 = mapa_shared(full_bar(0), 0);
+      int slot = 0;
+      uint32_t phase = 0;
+      bool ok = !a.test_stall;  // the test hook leaves every stage unfilled
+      for (int64_t tile = first_tile; ok && tile < total_tiles; tile += tile_step) {
+        const BlockTile bt = block_tile(tile, tile_base, E, NT);
+        const int rows_left = row_count[bt.e] - bt.mt * kBTileRows;
+        const bool peer_real = rows_left > 128;  // the odd CTA has rows in this tile
+        const bool real = leader || peer_real;
+        const int row0 = row_begin[bt.e] + bt.mt * kBTileRows + (int)rank * 128;
+        const int col0 = bt.nt * kBTileCols + (int)rank * 128;
+        const uint32_t tx = (uint32_t)kBHalfBytes * (peer_real ? 4u : 3u);
+        for (int b = 0; b < RB; ++b) {
+          if (!warp_wait(empty_bar(slot), phase ^ 1u, sync, a.timeout_ns)) {
+            ok = false;
+            break;
+          }
+          if (elect_one()) {
+            if (leader) mbar_arrive_expect_tx(full_bar(slot), tx);
+            const uint32_t st = sbase + (uint32_t)slot * kBStageBytes, lfull = lfull0 + 8u * slot;
+            if (DGRAD) tma_load_3d_pair(st + kBHalfBytes, &p.tmap_w, lfull, col0, b * kFp8Block, bt.e);
+            else tma_load_3d_pair(st + kBHalfBytes, &p.tmap_w, lfull, b * kFp8Block, col0, bt.e);
+            if (real) tma_load_2d_pair(st, &p.tmap_x, lfull, b * kFp8Block, row0);
+          }
+          __syncwarp();
+          if (++slot == kBStages) {
+            slot = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      __syncwarp();
+    } else if (warp == 1) {
+      // ------------------------------------------------------------------ MMA issuer (even CTA)
+      if (leader) {
+        int slot = 0;
+        uint32_t phase = 0, buf = 0, acc_phase = 0;
+        bool ok = true, issued = false;
+        // K-major tiles: 128-byte rows, 8-row groups 1024 bytes apart, an MMA step 32 bytes along the
+        // row.  MN-major B (gradient): the same tile read along its rows, a step 32 rows (4096 bytes).
+        const uint64_t a_desc0 = smem_desc(sbase, 16, 1024, kLayoutSwizzle128B);
+        const uint64_t b_desc0 = smem_desc(sbase + kBHalfBytes, 16, 1024, kLayoutSwizzle128B);
+        constexpr uint64_t kSlotStep = kBStageBytes >> 4;
+        constexpr uint64_t kBStep = (DGRAD ? 4096 : 32) >> 4;
+        const uint32_t idesc = block_idesc(DGRAD);
+        for (int64_t tile = first_tile; ok && tile < total_tiles; tile += tile_step) {
+          for (int b = 0; b < RB; ++b) {
+            if (!warp_wait(tmem_empty(buf), acc_phase ^ 1u, sync, a.timeout_ns) ||
+                !warp_wait(full_bar(slot), phase, sync, a.timeout_ns)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const uint64_t so = (uint64_t)slot * kSlotStep;
+            const uint32_t d = tmem_base + buf * kBTileCols;
+            if (elect_one()) {
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                tc_mma_pair_f8(d, a_desc0 + so + 2 * j, b_desc0 + so + kBStep * j, idesc, j > 0 ? 1u : 0u);
+              tc_commit_pair_mc(empty_bar(slot), 0x3);
+              tc_commit_pair_mc(tmem_full(buf), 0x3);
+            }
+            __syncwarp();
+            issued = true;
+            if (++slot == kBStages) {
+              slot = 0;
+              phase ^= 1u;
+            }
+            buf ^= 1u;
+            if (buf == 0) acc_phase ^= 1u;
+          }
+        }
+        if (issued) {
+          // no MMA of the pair may still run when TMEM is freed
+          if (elect_one()) tc_commit_pair(drain_bar);
+          __syncwarp();
+          warp_wait(drain_bar, 0, sync, 100000000ull, true);
+        }
+      }
+      __syncwarp();
+    }
+  } else {
+    // ------------------------------------------------------------------ sums over blocks (both CTAs)
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kBEpiRegs));
+    const int quad = warp & 3, half = (warp - kBFirstEpiWarp) >> 2;
+    const uint32_t leader_empty0 = mapa_shared(tmem_empty(0), 0);
+    const int KB = (a.K + kFp8Block - 1) / kFp8Block, NB = (a.N + kFp8Block - 1) / kFp8Block;
+    const uint32_t tlane = tmem_base + ((uint32_t)(quad * 32) << 16) + (uint32_t)(half * 128);
+    uint32_t buf = 0, acc_phase = 0;
+    bool ok = true;
+    for (int64_t tile = first_tile; ok && tile < total_tiles; tile += tile_step) {
+      const BlockTile bt = block_tile(tile, tile_base, E, NT);
+      const int row_local = bt.mt * kBTileRows + (int)rank * 128 + quad * 32 + lane;
+      const bool valid = row_local < row_count[bt.e];
+      const int col0 = bt.nt * kBTileCols + half * 128;
+      const bool any = __any_sync(0xffffffffu, valid) && col0 < cols;
+      const int64_t row = (int64_t)row_begin[bt.e] + row_local;
+      const int cb = min(col0 / kFp8Block, (DGRAD ? KB : NB) - 1);
+      const float* sx = a.x_scale + (valid ? row : 0) * RB;
+      const float* sw = a.w_scale + (int64_t)bt.e * NB * KB + (DGRAD ? cb : cb * KB);
+      const int sw_step = DGRAD ? KB : 1;
+      float acc[128];
+#pragma unroll
+      for (int i = 0; i < 128; ++i) acc[i] = 0.0f;
+      float s_next = any ? sx[0] * sw[0] : 0.0f;
+      for (int b = 0; b < RB; ++b) {
+        const float s = s_next;
+        if (any && b + 1 < RB) s_next = sx[b + 1] * sw[(int64_t)(b + 1) * sw_step];
+        if (!sums_wait(tmem_full(buf), acc_phase, sync)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        if (any) {
+          uint64_t s2;
+          asm("mov.b64 %0, {%1, %1};" : "=l"(s2) : "f"(s));
+          const uint32_t t = tlane + buf * kBTileCols;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            float v[32];
+            tc_ld_32x32b_x32(t + 32 * c, v);
+            tc_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) fma2(acc[32 * c + i], acc[32 * c + i + 1], v[i], v[i + 1], s2);
+          }
+          tc_fence_before();
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster_relaxed(leader_empty0 + 8u * buf);  // registers hold the block
+        buf ^= 1u;
+        if (buf == 0) acc_phase ^= 1u;
+      }
+      if (!ok || !any) continue;
+      const int dt = a.out_dtype;
+      if (p.out_vec && col0 + 128 <= cols) {
+        // 32-byte stores: every lane fills whole sectors of its own row
+        if (valid) {
+          if (dt == kDtF32) {
+            float* dst = static_cast<float*>(a.out) + row * cols + col0;
+#pragma unroll
+            for (int i = 0; i < 128; i += 8) {
+              uint32_t w[8];
+#pragma unroll
+              for (int q = 0; q < 8; ++q) w[q] = __float_as_uint(acc[i + q]);
+              st_global_v8(dst + i, w);
+            }
+          } else {
+            uint16_t* dst = static_cast<uint16_t*>(a.out) + row * cols + col0;
+#pragma unroll
+            for (int i = 0; i < 128; i += 16) {
+              uint32_t w[8];
+#pragma unroll
+              for (int q = 0; q < 8; ++q) w[q] = out_pair(acc[i + 2 * q], acc[i + 2 * q + 1], dt);
+              st_global_v8(dst + i, w);
+            }
+          }
+        }
+      } else {
+        // Any alignment and the last columns: 16 columns at a time through the warp's staging buffer
+        // (swizzled: conflict-free both ways), then 16 consecutive elements of two rows a store
+        float* buf16 = reinterpret_cast<float*>(smem + kBOutOff + (warp - kBFirstEpiWarp) * kBOutBytes);
+        const int rows_here = min(32, row_count[bt.e] - (row_local - lane));
+        const int64_t row0 = row - lane;
+#pragma unroll
+        for (int c = 0; c < 128; c += 16) {
+          if (col0 + c >= cols) break;
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < 16; ++i) buf16[lane * 16 + (i ^ ((lane >> 1) & 15))] = acc[c + i];
+          __syncwarp();
+          const int col = col0 + c + (lane & 15);
+          for (int r2 = 0; r2 < 16; ++r2) {
+            const int r = 2 * r2 + (lane >> 4);
+            if (r < rows_here && col < cols) {
+              const uint32_t w = out_bits(buf16[r * 16 + ((lane & 15) ^ r2)], dt);
+              const int64_t at = (row0 + r) * cols + col;
+              if (dt == kDtF32) static_cast<uint32_t*>(a.out)[at] = w;
+              else static_cast<uint16_t*>(a.out)[at] = (uint16_t)w;
+            }
+          }
         }
       }
     }
-    for (int i = 0; i < 4; ++i)
-      for (int j = 0; j < 4; ++j) {
-        const int64_t r = r0 + ty * 4 + i;
-        const int n = n0 + tx * 4 + j;
-        if (r < end && n < cols) store_out(a.out, a.out_dtype, r * cols + n, tot[i][j]);
-      }
   }
+
+  tc_fence_before();
+  cluster_sync();  // both CTAs done with the pair's TMEM
+  // After an abort in either CTA, loads that were issued but never waited for may still be landing
+  // in this CTA's shared memory or on the even CTA's barriers: give them time before leaving.
+  const uint32_t peer_abort = ld_shared_cluster_u32(mapa_shared(smem_u32((const void*)abort_flag), rank ^ 1u));
+  if (*abort_flag || peer_abort) {
+    const uint64_t t0 = clock64();
+    while (clock64() - t0 < 2000000ull) {
+    }
+  }
+  cluster_sync();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc_pair(tmem_base, 2 * kBTileCols);
+}
+
+// ---------------------------------------------------------------------- host side
+bool encode_codes(CUtensorMap* m, const uint8_t* base, int rank, const cuuint64_t* dims, const cuuint64_t* strides) {
+  EncodeTiledFn encode = get_encode_fn();
+  if (!encode) return false;
+  const cuuint32_t box[3] = {128, 128, 1};
+  const cuuint32_t es[3] = {1, 1, 1};
+  return encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, (cuuint32_t)rank, const_cast<uint8_t*>(base), dims, strides, box, es,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <bool DGRAD>
+cudaError_t launch_pair(const GemmBlockArgs& a, cudaStream_t s) {
+  static std::atomic<int> ready[64];  // per device: the kernel's shared-memory limit is set
+  int dev = 0;
+  cudaError_t err = cudaGetDevice(&dev);
+  if (err != cudaSuccess) return err;
+  if (dev >= 64) return cudaErrorInvalidDevice;
+  if (!ready[dev].load(std::memory_order_acquire)) {
+    err = cudaFuncSetAttribute(gemm_block_pair_kernel<DGRAD>, cudaFuncAttributeMaxDynamicSharedMemorySize, kBSmemBytes);
+    if (err != cudaSuccess) return err;
+    ready[dev].store(1, std::memory_order_release);
+  }
+  BlockParams p;
+  const cuuint64_t red = (cuuint64_t)(DGRAD ? a.N : a.K);
+  const cuuint64_t xd[2] = {red, (cuuint64_t)a.M}, xst[1] = {red};
+  const cuuint64_t wd[3] = {(cuuint64_t)a.K, (cuuint64_t)a.N, (cuuint64_t)a.E};
+  const cuuint64_t wst[2] = {(cuuint64_t)a.K, (cuuint64_t)a.K * (cuuint64_t)a.N};
+  if (!encode_codes(&p.tmap_x, a.x, 2, xd, xst) || !encode_codes(&p.tmap_w, a.w, 3, wd, wst))
+    return cudaErrorInvalidValue;
+  p.a = a;
+  const int64_t cols = DGRAD ? a.K : a.N;
+  p.out_vec = reinterpret_cast<uintptr_t>(a.out) % 32 == 0 && (cols * dtype_bytes(a.out_dtype)) % 32 == 0;
+  // every group adds at most one partial row tile
+  const int64_t mtiles = (a.M + kBTileRows - 1) / kBTileRows + a.E - 1;
+  const int64_t tiles = mtiles * ((cols + kBTileCols - 1) / kBTileCols);
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.gridDim = dim3((unsigned)(2 * std::min<int64_t>(tiles, a.num_sms / 2)));
+  cfg.blockDim = dim3(kBThreads);
+  cfg.dynamicSmemBytes = kBSmemBytes;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, gemm_block_pair_kernel<DGRAD>, p);
 }
 
 }  // namespace
 
 cudaError_t launch_gemm_block(const GemmBlockArgs& a, cudaStream_t s) {
   if (a.M == 0) return cudaSuccess;
-  const int cols = a.dgrad ? a.K : a.N;
-  const int64_t mt = (a.M + kT - 1) / kT;
-  const dim3 grid((unsigned)((cols + kT - 1) / kT), (unsigned)std::min<int64_t>(mt, 64), (unsigned)a.E);
-  gemm_block_plain_kernel<<<grid, 256, 0, s>>>(a);
-  return cudaGetLastError();
+  return a.dgrad ? launch_pair<true>(a, s) : launch_pair<false>(a, s);
 }
 
 }  // namespace moe

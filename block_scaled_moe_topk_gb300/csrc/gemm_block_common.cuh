@@ -1,0 +1,41 @@
+// gemm_block_common.cuh -- what the kernels of the FP8 block-scaled product share: rounding to the
+// output type and the clamped row ranges of the groups.
+#pragma once
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "expert_internal.h"
+
+namespace moe {
+namespace {
+
+// An fp32 value as the bits of the output type (low 16 bits for BF16 and F16).
+__device__ __forceinline__ uint32_t out_bits(float v, int dtype) {
+  if (dtype == kDtBf16) return __bfloat16_as_ushort(__float2bfloat16_rn(v));
+  if (dtype == kDtF16) return __half_as_ushort(__float2half_rn(v));
+  return __float_as_uint(v);
+}
+
+__device__ __forceinline__ uint32_t out_pair(float lo, float hi, int dtype) {
+  if (dtype == kDtBf16) {
+    const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&b);
+  }
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// Rows [begin, begin + rows) of group e, inside [0, M) whatever the offsets hold.
+struct RowSpan {
+  int64_t begin, rows;
+};
+__device__ __forceinline__ RowSpan group_rows(const int64_t* offsets, int e, int64_t M) {
+  if (offsets == nullptr) return {0, M};
+  const int64_t a = offsets[e], b = offsets[e + 1];
+  const int64_t begin = a < 0 ? 0 : (a > M ? M : a);
+  const int64_t end = b < begin ? begin : (b > M ? M : b);
+  return {begin, end - begin};
+}
+
+}  // namespace
+}  // namespace moe
