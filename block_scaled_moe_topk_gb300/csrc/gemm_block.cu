@@ -18,6 +18,10 @@
 // reduction along rows (MN-major descriptor): no transposed copy of the weights exists.
 //   warp 0     TMA producer (converged, copies issued by an elected lane)
 //   warp 1     TMEM owner; in the even CTA the MMA issuer for both
+//   warps 2, 3 scales: chunks of 8 blocks' scales of the tile's rows into shared memory, eight lanes
+//              a row.  A thread of the summing warps loading its own row's scale instead touches 32
+//              lines an instruction, in competition with the operands for the shared-memory pipe
+//              (the 49152-row product below: 2.51 ms against XXXX)
 //   warps 4-11 sums: a thread owns one row and 128 of the 256 columns (one scale block) in 128 fp32
 //              registers; warps whose 32 rows are past the group's end read nothing.  The two
 //              warpgroups take 224 registers a thread, the first warpgroup keeps 56 (setmaxnreg;
@@ -47,12 +51,16 @@ constexpr int kBTileCols = 256;                     // output columns of a pair 
 constexpr int kBHalfBytes = 128 * 128;              // one operand of a stage in one CTA
 constexpr int kBStageBytes = 2 * kBHalfBytes;
 constexpr int kBOutOff = kBStages * kBStageBytes;   // per-warp staging of unaligned output rows
-constexpr int kBOutBytes = 32 * 16 * 4;             // 32 rows x 16 columns of fp32
-constexpr int kBBarOff = kBOutOff + kBEpiWarps * kBOutBytes;
+constexpr int kBOutBytes = 32 * 32;                 // 32 rows x 32 bytes
+constexpr int kBScaleBlocks = 8;                    // reduction blocks of one scale chunk
+constexpr int kBScaleRows = 130;                    // 128 rows of x, then the weights' two column halves
+constexpr int kBScaleOff = kBOutOff + kBEpiWarps * kBOutBytes;  // two chunks [block][row], fp32
+constexpr int kBScaleBytes = kBScaleBlocks * kBScaleRows * 4;
+constexpr int kBBarOff = kBScaleOff + 2 * kBScaleBytes;
 constexpr int kBTabOff = kBBarOff + 256;            // per expert: first row, rows, first tile
 constexpr int kBSmemBytes = kBTabOff + 3 * 4 * (kMaxExperts + 1) + 1024;
 static_assert(kBSmemBytes <= 232448, "block GEMM shared memory");
-static_assert(8 * (2 * kBStages + 5) + 8 <= 256, "block GEMM barriers");
+static_assert(kBBarOff % 8 == 0 && 8 * (2 * kBStages + 9) + 8 <= 256, "block GEMM barriers");
 
 struct BlockParams {  // 64-byte aligned through its CUtensorMap members
   CUtensorMap tmap_x;  // codes [M, reduction], box 128 B x 128 rows
@@ -76,15 +84,6 @@ __device__ __forceinline__ void tc_mma_pair_f8(uint32_t d, uint64_t adesc, uint6
       "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
       "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
       : "memory");
-}
-
-// Two fp32 multiply-adds in one instruction: acc += v * s, element by element.
-__device__ __forceinline__ void fma2(float& a0, float& a1, float v0, float v1, uint64_t s2) {
-  uint64_t a, v;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(a) : "f"(a0), "f"(a1));
-  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(v0), "f"(v1));
-  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(a) : "l"(v), "l"(s2));
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(a0), "=f"(a1) : "l"(a));
 }
 
 __device__ __forceinline__ void st_global_v8(void* p, const uint32_t (&w)[8]) {
@@ -146,8 +145,10 @@ __global__ void __launch_bounds__(kBThreads, 1) gemm_block_pair_kernel(const __g
   auto empty_bar = [&](int s) { return bar0 + 8u * (kBStages + s); };
   auto tmem_full = [&](int b) { return bar0 + 8u * (2 * kBStages + b); };
   auto tmem_empty = [&](int b) { return bar0 + 8u * (2 * kBStages + 2 + b); };
-  const uint32_t drain_bar = bar0 + 8u * (2 * kBStages + 4);
-  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + kBBarOff + 8 * (2 * kBStages + 5));
+  auto scale_full = [&](int b) { return bar0 + 8u * (2 * kBStages + 4 + b); };
+  auto scale_empty = [&](int b) { return bar0 + 8u * (2 * kBStages + 6 + b); };
+  const uint32_t drain_bar = bar0 + 8u * (2 * kBStages + 8);
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + kBBarOff + 8 * (2 * kBStages + 9));
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
   int32_t* row_begin = reinterpret_cast<int32_t*>(smem + kBTabOff);
   int32_t* row_count = row_begin + kMaxExperts + 1;
@@ -173,6 +174,8 @@ __global__ void __launch_bounds__(kBThreads, 1) gemm_block_pair_kernel(const __g
     for (int b = 0; b < 2; ++b) {
       mbar_init(tmem_full(b), 1);
       mbar_init(tmem_empty(b), 2 * kBEpiWarps);  // warps of both CTAs
+      mbar_init(scale_full(b), 2);               // the two loading warps
+      mbar_init(scale_empty(b), kBEpiWarps);
     }
     mbar_init(drain_bar, 1);
     *abort_flag = 0;
@@ -208,6 +211,7 @@ __global__ void __launch_bounds__(kBThreads, 1) gemm_block_pair_kernel(const __g
 
   const Sync sync{abort_flag, a.status, a.timeout_ns, bar0};
   const int red = DGRAD ? a.N : a.K, cols = DGRAD ? a.K : a.N;
+  const int KB = (a.K + kFp8Block - 1) / kFp8Block, NB = (a.N + kFp8Block - 1) / kFp8Block;
   const int RB = (red + kFp8Block - 1) / kFp8Block;
   const int NT = (cols + kBTileCols - 1) / kBTileCols;
   const int64_t total_tiles = (int64_t)tile_base[E] * NT;
@@ -297,15 +301,53 @@ __global__ void __launch_bounds__(kBThreads, 1) gemm_block_pair_kernel(const __g
         }
       }
       __syncwarp();
+    } else {
+      // ---------------------------------------------------------------- scales (warps 2 and 3)
+      float* scales = reinterpret_cast<float*>(smem + kBScaleOff);
+      const int j = lane & 7, rsub = (warp - 2) * 4 + (lane >> 3);  // this lane's block, and row mod 8
+      const int sw_step = DGRAD ? KB : 1;
+      uint32_t sbuf = 0, sphase = 0;
+      bool ok = true;
+      for (int64_t tile = first_tile; ok && tile < total_tiles; tile += tile_step) {
+        const BlockTile bt = block_tile(tile, tile_base, E, NT);
+        const int row_local = bt.mt * kBTileRows + (int)rank * 128;
+        const int rows_here = min(128, row_count[bt.e] - row_local);
+        const float* sx = a.x_scale + ((int64_t)row_begin[bt.e] + row_local) * RB;
+        // the scale block of column half (lane >> 3): past the last column, the last one (unused)
+        const int cb = min(bt.nt * 2 + ((lane >> 3) & 1), (DGRAD ? KB : NB) - 1);
+        const float* sw = a.w_scale + (int64_t)bt.e * NB * KB + (DGRAD ? cb : cb * KB);
+        for (int b0 = 0; b0 < RB; b0 += kBScaleBlocks) {
+          const bool in = b0 + j < RB;
+          float v[16], wv = 0.0f;
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const int r = i * 8 + rsub;
+            v[i] = in && r < rows_here ? sx[(int64_t)r * RB + b0 + j] : 0.0f;
+          }
+          if (warp == 2 && lane < 16 && in) wv = sw[(int64_t)(b0 + j) * sw_step];
+          if (!warp_wait(scale_empty(sbuf), sphase ^ 1u, sync, a.timeout_ns)) {
+            ok = false;
+            break;
+          }
+          float* dst = scales + sbuf * (kBScaleBytes / 4) + j * kBScaleRows;
+#pragma unroll
+          for (int i = 0; i < 16; ++i) dst[i * 8 + rsub] = v[i];
+          if (warp == 2 && lane < 16) dst[128 + (lane >> 3)] = wv;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(scale_full(sbuf));
+          sbuf ^= 1u;
+          if (sbuf == 0) sphase ^= 1u;
+        }
+      }
     }
   } else {
     // ------------------------------------------------------------------ sums over blocks (both CTAs)
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kBEpiRegs));
     const int quad = warp & 3, half = (warp - kBFirstEpiWarp) >> 2;
     const uint32_t leader_empty0 = mapa_shared(tmem_empty(0), 0);
-    const int KB = (a.K + kFp8Block - 1) / kFp8Block, NB = (a.N + kFp8Block - 1) / kFp8Block;
     const uint32_t tlane = tmem_base + ((uint32_t)(quad * 32) << 16) + (uint32_t)(half * 128);
-    uint32_t buf = 0, acc_phase = 0;
+    const float* scales = reinterpret_cast<const float*>(smem + kBScaleOff);
+    uint32_t buf = 0, acc_phase = 0, sbuf = 0, sphase = 0;
     bool ok = true;
     for (int64_t tile = first_tile; ok && tile < total_tiles; tile += tile_step) {
       const BlockTile bt = block_tile(tile, tile_base, E, NT);
@@ -314,40 +356,44 @@ __global__ void __launch_bounds__(kBThreads, 1) gemm_block_pair_kernel(const __g
       const int col0 = bt.nt * kBTileCols + half * 128;
       const bool any = __any_sync(0xffffffffu, valid) && col0 < cols;
       const int64_t row = (int64_t)row_begin[bt.e] + row_local;
-      const int cb = min(col0 / kFp8Block, (DGRAD ? KB : NB) - 1);
-      const float* sx = a.x_scale + (valid ? row : 0) * RB;
-      const float* sw = a.w_scale + (int64_t)bt.e * NB * KB + (DGRAD ? cb : cb * KB);
-      const int sw_step = DGRAD ? KB : 1;
       float acc[128];
 #pragma unroll
       for (int i = 0; i < 128; ++i) acc[i] = 0.0f;
-      float s_next = any ? sx[0] * sw[0] : 0.0f;
-      for (int b = 0; b < RB; ++b) {
-        const float s = s_next;
-        if (any && b + 1 < RB) s_next = sx[b + 1] * sw[(int64_t)(b + 1) * sw_step];
-        if (!sums_wait(tmem_full(buf), acc_phase, sync)) {
+      for (int b0 = 0; ok && b0 < RB; b0 += kBScaleBlocks) {
+        if (!sums_wait(scale_full(sbuf), sphase, sync)) {
           ok = false;
           break;
         }
-        tc_fence_after();
-        if (any) {
-          uint64_t s2;
-          asm("mov.b64 %0, {%1, %1};" : "=l"(s2) : "f"(s));
-          const uint32_t t = tlane + buf * kBTileCols;
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            float v[32];
-            tc_ld_32x32b_x32(t + 32 * c, v);
-            tc_wait_ld();
-#pragma unroll
-            for (int i = 0; i < 32; i += 2) fma2(acc[32 * c + i], acc[32 * c + i + 1], v[i], v[i + 1], s2);
+        const float* sc = scales + sbuf * (kBScaleBytes / 4);
+        const int nb = min(kBScaleBlocks, RB - b0);
+        for (int b = 0; b < nb; ++b) {
+          const float s = sc[b * kBScaleRows + quad * 32 + lane] * sc[b * kBScaleRows + 128 + half];
+          if (!sums_wait(tmem_full(buf), acc_phase, sync)) {
+            ok = false;
+            break;
           }
-          tc_fence_before();
+          tc_fence_after();
+          if (any) {
+            const uint32_t t = tlane + buf * kBTileCols;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              float v[32];
+              tc_ld_32x32b_x32(t + 32 * c, v);
+              tc_wait_ld();
+#pragma unroll
+              for (int i = 0; i < 32; ++i) acc[32 * c + i] = fmaf(v[i], s, acc[32 * c + i]);
+            }
+            tc_fence_before();
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster_relaxed(leader_empty0 + 8u * buf);  // registers hold the block
+          buf ^= 1u;
+          if (buf == 0) acc_phase ^= 1u;
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive_cluster_relaxed(leader_empty0 + 8u * buf);  // registers hold the block
-        buf ^= 1u;
-        if (buf == 0) acc_phase ^= 1u;
+        if (lane == 0) mbar_arrive(scale_empty(sbuf));
+        sbuf ^= 1u;
+        if (sbuf == 0) sphase ^= 1u;
       }
       if (!ok || !any) continue;
       const int dt = a.out_dtype;
@@ -375,26 +421,43 @@ __global__ void __launch_bounds__(kBThreads, 1) gemm_block_pair_kernel(const __g
           }
         }
       } else {
-        // Any alignment and the last columns: 16 columns at a time through the warp's staging buffer
-        // (swizzled: conflict-free both ways), then 16 consecutive elements of two rows a store
-        float* buf16 = reinterpret_cast<float*>(smem + kBOutOff + (warp - kBFirstEpiWarp) * kBOutBytes);
+        // Any alignment and the last columns: 32 bytes of every row at a time through the warp's
+        // staging buffer (words swizzled: conflict-free both ways), then consecutive elements of a
+        // row by consecutive lanes
+        uint32_t* stage = reinterpret_cast<uint32_t*>(smem + kBOutOff + (warp - kBFirstEpiWarp) * kBOutBytes);
         const int rows_here = min(32, row_count[bt.e] - (row_local - lane));
         const int64_t row0 = row - lane;
+        if (dt == kDtF32) {
 #pragma unroll
-        for (int c = 0; c < 128; c += 16) {
-          if (col0 + c >= cols) break;
-          __syncwarp();
+          for (int c = 0; c < 128; c += 8) {
+            if (col0 + c >= cols) break;
+            __syncwarp();
 #pragma unroll
-          for (int i = 0; i < 16; ++i) buf16[lane * 16 + (i ^ ((lane >> 1) & 15))] = acc[c + i];
-          __syncwarp();
-          const int col = col0 + c + (lane & 15);
-          for (int r2 = 0; r2 < 16; ++r2) {
-            const int r = 2 * r2 + (lane >> 4);
-            if (r < rows_here && col < cols) {
-              const uint32_t w = out_bits(buf16[r * 16 + ((lane & 15) ^ r2)], dt);
-              const int64_t at = (row0 + r) * cols + col;
-              if (dt == kDtF32) static_cast<uint32_t*>(a.out)[at] = w;
-              else static_cast<uint16_t*>(a.out)[at] = (uint16_t)w;
+            for (int i = 0; i < 8; ++i) stage[lane * 8 + (i ^ (lane >> 2))] = __float_as_uint(acc[c + i]);
+            __syncwarp();
+            const int col = col0 + c + (lane & 7);
+            for (int r4 = 0; r4 < 8; ++r4) {
+              const int r = 4 * r4 + (lane >> 3);
+              if (r < rows_here && col < cols)
+                static_cast<uint32_t*>(a.out)[(row0 + r) * cols + col] = stage[r * 8 + ((lane & 7) ^ r4)];
+            }
+          }
+        } else {
+#pragma unroll
+          for (int c = 0; c < 128; c += 16) {
+            if (col0 + c >= cols) break;
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              stage[lane * 8 + (i ^ (lane >> 2))] = out_pair(acc[c + 2 * i], acc[c + 2 * i + 1], dt);
+            __syncwarp();
+            const int col = col0 + c + (lane & 15);
+            for (int r2 = 0; r2 < 16; ++r2) {
+              const int r = 2 * r2 + (lane >> 4);
+              if (r < rows_here && col < cols) {
+                const uint32_t w = stage[r * 8 + (((lane & 15) >> 1) ^ (r >> 2))];
+                static_cast<uint16_t*>(a.out)[(row0 + r) * cols + col] = (uint16_t)(lane & 1 ? w >> 16 : w);
+              }
             }
           }
         }

@@ -9,13 +9,7 @@
 namespace moe {
 namespace {
 
-// An fp32 value as the bits of the output type (low 16 bits for BF16 and F16).
-__device__ __forceinline__ uint32_t out_bits(float v, int dtype) {
-  if (dtype == kDtBf16) return __bfloat16_as_ushort(__float2bfloat16_rn(v));
-  if (dtype == kDtF16) return __half_as_ushort(__float2half_rn(v));
-  return __float_as_uint(v);
-}
-
+// Two fp32 values as the bits of two elements of a 16-bit output type.
 __device__ __forceinline__ uint32_t out_pair(float lo, float hi, int dtype) {
   if (dtype == kDtBf16) {
     const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
