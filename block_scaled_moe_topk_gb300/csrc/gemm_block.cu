@@ -42,15 +42,14 @@ namespace {
 
 constexpr int kBThreads = 384;   // 168 registers a thread at launch
 constexpr int kBFirstEpiWarp = 4;
-constexpr int kBCtlRegs = 56, kBEpiRegs = 224;
+constexpr int kBCtlRegs = 104, kBEpiRegs = 200;
 static_assert(128 * kBCtlRegs + 256 * kBEpiRegs <= 384 * 168, "register split");
 constexpr int kBEpiWarps = 8;
-constexpr int kBStages = 6;
-constexpr int kBTileRows = 256;                     // rows of a pair tile
-constexpr int kBTileCols = 256;                     // output columns of a pair tile
-constexpr int kBHalfBytes = 128 * 128;              // one operand of a stage in one CTA
-constexpr int kBStageBytes = 2 * kBHalfBytes;
-constexpr int kBOutOff = kBStages * kBStageBytes;   // per-warp staging of unaligned output rows
+constexpr int kBTileCols = 256;                     // output columns of a tile
+constexpr int kBHalfBytes = 128 * 128;              // 128 rows of x, or 128 of the tile's weight rows
+constexpr int kBRingBytes = 6 * 2 * kBHalfBytes;    // 192 KiB: 6 stages of a pair's CTA, 4 of a single CTA
+constexpr int kBMaxStages = 6;
+constexpr int kBOutOff = kBRingBytes;   // per-warp staging of unaligned output rows
 constexpr int kBOutBytes = 32 * 32;                 // 32 rows x 32 bytes
 constexpr int kBScaleBlocks = 8;                    // reduction blocks of one scale chunk
 constexpr int kBScaleRows = 130;                    // 128 rows of x, then the weights' two column halves
@@ -60,7 +59,16 @@ constexpr int kBBarOff = kBScaleOff + 2 * kBScaleBytes;
 constexpr int kBTabOff = kBBarOff + 256;            // per expert: first row, rows, first tile
 constexpr int kBSmemBytes = kBTabOff + 3 * 4 * (kMaxExperts + 1) + 1024;
 static_assert(kBSmemBytes <= 232448, "block GEMM shared memory");
-static_assert(kBBarOff % 8 == 0 && 8 * (2 * kBStages + 9) + 8 <= 256, "block GEMM barriers");
+static_assert(kBBarOff % 8 == 0 && 8 * (2 * kBMaxStages + 9) + 8 <= 256, "block GEMM barriers");
+
+// One CTA (G = 1) or a pair (G = 2) works on a tile of 128 G rows by 256 columns; a CTA stages its 128
+// rows of x and 256 / G of the weight rows.
+template <int G>
+struct BlockGeo {
+  static constexpr int kRows = 128 * G;
+  static constexpr int kStageBytes = (1 + 2 / G) * kBHalfBytes;
+  static constexpr int kStages = kBRingBytes / kStageBytes;
+};
 
 struct BlockParams {  // 64-byte aligned through its CUtensorMap members
   CUtensorMap tmap_x;  // codes [M, reduction], box 128 B x 128 rows
@@ -71,19 +79,44 @@ struct BlockParams {  // 64-byte aligned through its CUtensorMap members
 
 // Instruction descriptor of kind::f8f6f4: fp32 accumulator (bit 4), E4M3 operands, B read along its
 // rows (bit 16) for the gradient, N / 8 at [17, 23), M / 16 at [24, 29).
-__device__ __forceinline__ uint32_t block_idesc(bool dgrad) {
-  return (1u << 4) | ((dgrad ? 1u : 0u) << 16) | ((uint32_t)(kBTileCols >> 3) << 17) |
-         ((uint32_t)(kBTileRows >> 4) << 24);
+__device__ __forceinline__ uint32_t block_idesc(bool dgrad, int rows) {
+  return (1u << 4) | ((dgrad ? 1u : 0u) << 16) | ((uint32_t)(kBTileCols >> 3) << 17) | ((uint32_t)(rows >> 4) << 24);
 }
 
-__device__ __forceinline__ void tc_mma_pair_f8(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
-                                               uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
-      : "memory");
+template <int G>
+__device__ __forceinline__ void tc_mma_f8(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                          uint32_t accumulate) {
+  if (G == 2)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// Arrive on `bar` of every CTA of the tile when the MMAs issued so far completed.
+template <int G>
+__device__ __forceinline__ void tc_commit_all(uint32_t bar) {
+  if (G == 2) tc_commit_pair_mc(bar, 0x3);
+  else tc_commit(bar);
+}
+
+// acc += v * s on two neighbouring sums in one instruction (half the issue slots of two).
+__device__ __forceinline__ void fma_pair(float& a0, float& a1, float v0, float v1, float s) {
+  uint64_t a, v, s2;
+  asm("mov.b64 %0, {%1, %1};" : "=l"(s2) : "f"(s));
+  asm("mov.b64 %0, {%1, %2};" : "=l"(a) : "f"(a0), "f"(a1));
+  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(v0), "f"(v1));
+  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(a) : "l"(v), "l"(s2));
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a0), "=f"(a1) : "l"(a));
 }
 
 __device__ __forceinline__ void st_global_v8(void* p, const uint32_t (&w)[8]) {
@@ -135,20 +168,21 @@ __device__ __forceinline__ BlockTile block_tile(int64_t tile, const int32_t* bas
   return {lo, (int)(local % (uint32_t)mt_e), (int)(local / (uint32_t)mt_e)};
 }
 
-template <bool DGRAD>
-__global__ void __launch_bounds__(kBThreads, 1) gemm_block_pair_kernel(const __grid_constant__ BlockParams p) {
+template <int G, bool DGRAD>
+__global__ void __launch_bounds__(kBThreads, 1) gemm_block_kernel(const __grid_constant__ BlockParams p) {
+  constexpr int kStages = BlockGeo<G>::kStages, kStageBytes = BlockGeo<G>::kStageBytes, kRows = BlockGeo<G>::kRows;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sbase = smem_u32(smem);
   const uint32_t bar0 = sbase + kBBarOff;
   auto full_bar = [&](int s) { return bar0 + 8u * s; };
-  auto empty_bar = [&](int s) { return bar0 + 8u * (kBStages + s); };
-  auto tmem_full = [&](int b) { return bar0 + 8u * (2 * kBStages + b); };
-  auto tmem_empty = [&](int b) { return bar0 + 8u * (2 * kBStages + 2 + b); };
-  auto scale_full = [&](int b) { return bar0 + 8u * (2 * kBStages + 4 + b); };
-  auto scale_empty = [&](int b) { return bar0 + 8u * (2 * kBStages + 6 + b); };
-  const uint32_t drain_bar = bar0 + 8u * (2 * kBStages + 8);
-  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + kBBarOff + 8 * (2 * kBStages + 9));
+  auto empty_bar = [&](int s) { return bar0 + 8u * (kStages + s); };
+  auto tmem_full = [&](int b) { return bar0 + 8u * (2 * kStages + b); };
+  auto tmem_empty = [&](int b) { return bar0 + 8u * (2 * kStages + 2 + b); };
+  auto scale_full = [&](int b) { return bar0 + 8u * (2 * kStages + 4 + b); };
+  auto scale_empty = [&](int b) { return bar0 + 8u * (2 * kStages + 6 + b); };
+  const uint32_t drain_bar = bar0 + 8u * (2 * kStages + 8);
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + kBBarOff + 8 * (2 * kStages + 9));
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
   int32_t* row_begin = reinterpret_cast<int32_t*>(smem + kBTabOff);
   int32_t* row_count = row_begin + kMaxExperts + 1;
@@ -156,7 +190,7 @@ __global__ void __launch_bounds__(kBThreads, 1) gemm_block_pair_kernel(const __g
 
   const GemmBlockArgs& a = p.a;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const uint32_t rank = cluster_ctarank();
+  const uint32_t rank = G == 2 ? cluster_ctarank() : 0;
   const bool leader = rank == 0;
   const int E = a.E;
 
@@ -167,13 +201,13 @@ __global__ void __launch_bounds__(kBThreads, 1) gemm_block_pair_kernel(const __g
     row_count[e] = (int32_t)sp.rows;
   }
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kBStages; ++s) {
-      mbar_init(full_bar(s), 1);   // expect_tx arrival of the even CTA's producer
-      mbar_init(empty_bar(s), 1);  // the pair's MMA commit
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(full_bar(s), 1);   // expect_tx arrival of the even (or only) CTA's producer
+      mbar_init(empty_bar(s), 1);  // the MMA commit
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(tmem_full(b), 1);
-      mbar_init(tmem_empty(b), 2 * kBEpiWarps);  // warps of both CTAs
+      mbar_init(tmem_empty(b), G * kBEpiWarps);  // warps of every CTA of the tile
       mbar_init(scale_full(b), 2);               // the two loading warps
       mbar_init(scale_empty(b), kBEpiWarps);
     }
@@ -188,7 +222,7 @@ __global__ void __launch_bounds__(kBThreads, 1) gemm_block_pair_kernel(const __g
     int running = 0;
     for (int e0 = 0; e0 < E; e0 += 32) {
       const int e = e0 + lane;
-      const int v = e < E ? (row_count[e] + kBTileRows - 1) / kBTileRows : 0;
+      const int v = e < E ? (row_count[e] + kRows - 1) / kRows : 0;
       int incl = v;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -201,11 +235,17 @@ __global__ void __launch_bounds__(kBThreads, 1) gemm_block_pair_kernel(const __g
     if (lane == 0) tile_base[E] = running;
   }
   if (warp == 1) {
-    tmem_alloc_pair(smem_u32(tmem_holder), 2 * kBTileCols);
-    tmem_relinquish_pair();
+    if (G == 2) {
+      tmem_alloc_pair(smem_u32(tmem_holder), 2 * kBTileCols);
+      tmem_relinquish_pair();
+    } else {
+      tmem_alloc(smem_u32(tmem_holder), 2 * kBTileCols);
+      tmem_relinquish();
+    }
   }
   tc_fence_before();
-  cluster_sync();  // barriers initialised in both CTAs before any remote arrival
+  if (G == 2) cluster_sync();  // barriers initialised in both CTAs before any remote arrival
+  else __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_holder;
 
@@ -215,24 +255,24 @@ __global__ void __launch_bounds__(kBThreads, 1) gemm_block_pair_kernel(const __g
   const int RB = (red + kFp8Block - 1) / kFp8Block;
   const int NT = (cols + kBTileCols - 1) / kBTileCols;
   const int64_t total_tiles = (int64_t)tile_base[E] * NT;
-  const int64_t first_tile = cluster_index(), tile_step = cluster_count();
+  const int64_t first_tile = G == 2 ? cluster_index() : blockIdx.x, tile_step = G == 2 ? cluster_count() : gridDim.x;
 
   if (warp < kBFirstEpiWarp) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kBCtlRegs));
     if (warp == 0) {
       // ------------------------------------------------------------------ producer
-      const uint32_t lfull0 = mapa_shared(full_bar(0), 0);
+      const uint32_t lfull0 = G == 2 ? mapa_shared(full_bar(0), 0) : full_bar(0);
       int slot = 0;
       uint32_t phase = 0;
       bool ok = !a.test_stall;  // the test hook leaves every stage unfilled
       for (int64_t tile = first_tile; ok && tile < total_tiles; tile += tile_step) {
         const BlockTile bt = block_tile(tile, tile_base, E, NT);
-        const int rows_left = row_count[bt.e] - bt.mt * kBTileRows;
-        const bool peer_real = rows_left > 128;  // the odd CTA has rows in this tile
+        const int rows_left = row_count[bt.e] - bt.mt * kRows;
+        const bool peer_real = G == 2 && rows_left > 128;  // the odd CTA has rows in this tile
         const bool real = leader || peer_real;
-        const int row0 = row_begin[bt.e] + bt.mt * kBTileRows + (int)rank * 128;
+        const int row0 = row_begin[bt.e] + bt.mt * kRows + (int)rank * 128;
         const int col0 = bt.nt * kBTileCols + (int)rank * 128;
-        const uint32_t tx = (uint32_t)kBHalfBytes * (peer_real ? 4u : 3u);
+        const uint32_t tx = (uint32_t)kBHalfBytes * (peer_real ? 4u : 3u);  // of every CTA of the tile
         for (int b = 0; b < RB; ++b) {
           if (!warp_wait(empty_bar(slot), phase ^ 1u, sync, a.timeout_ns)) {
             ok = false;
@@ -240,13 +280,23 @@ __global__ void __launch_bounds__(kBThreads, 1) gemm_block_pair_kernel(const __g
           }
           if (elect_one()) {
             if (leader) mbar_arrive_expect_tx(full_bar(slot), tx);
-            const uint32_t st = sbase + (uint32_t)slot * kBStageBytes, lfull = lfull0 + 8u * slot;
-            if (DGRAD) tma_load_3d_pair(st + kBHalfBytes, &p.tmap_w, lfull, col0, b * kFp8Block, bt.e);
-            else tma_load_3d_pair(st + kBHalfBytes, &p.tmap_w, lfull, b * kFp8Block, col0, bt.e);
-            if (real) tma_load_2d_pair(st, &p.tmap_x, lfull, b * kFp8Block, row0);
+            const uint32_t st = sbase + (uint32_t)slot * kStageBytes, lfull = lfull0 + 8u * slot;
+            if (G == 2) {
+              if (DGRAD) tma_load_3d_pair(st + kBHalfBytes, &p.tmap_w, lfull, col0, b * kFp8Block, bt.e);
+              else tma_load_3d_pair(st + kBHalfBytes, &p.tmap_w, lfull, b * kFp8Block, col0, bt.e);
+              if (real) tma_load_2d_pair(st, &p.tmap_x, lfull, b * kFp8Block, row0);
+            } else {
+#pragma unroll
+              for (int h = 1; h <= 2; ++h) {
+                const int c = col0 + (h - 1) * 128;
+                if (DGRAD) tma_load_3d(st + h * kBHalfBytes, &p.tmap_w, lfull, c, b * kFp8Block, bt.e);
+                else tma_load_3d(st + h * kBHalfBytes, &p.tmap_w, lfull, b * kFp8Block, c, bt.e);
+              }
+              tma_load_2d(st, &p.tmap_x, lfull, b * kFp8Block, row0);
+            }
           }
           __syncwarp();
-          if (++slot == kBStages) {
+          if (++slot == kStages) {
             slot = 0;
             phase ^= 1u;
           }
@@ -260,12 +310,13 @@ __global__ void __launch_bounds__(kBThreads, 1) gemm_block_pair_kernel(const __g
         uint32_t phase = 0, buf = 0, acc_phase = 0;
         bool ok = true, issued = false;
         // K-major tiles: 128-byte rows, 8-row groups 1024 bytes apart, an MMA step 32 bytes along the
-        // row.  MN-major B (gradient): the same tile read along its rows, a step 32 rows (4096 bytes).
+        // row.  MN-major B (gradient): the same tiles read along their rows, 128 columns a tile (the
+        // next 128 kBHalfBytes further), a step 32 rows (4096 bytes).
         const uint64_t a_desc0 = smem_desc(sbase, 16, 1024, kLayoutSwizzle128B);
-        const uint64_t b_desc0 = smem_desc(sbase + kBHalfBytes, 16, 1024, kLayoutSwizzle128B);
-        constexpr uint64_t kSlotStep = kBStageBytes >> 4;
+        const uint64_t b_desc0 = smem_desc(sbase + kBHalfBytes, DGRAD ? kBHalfBytes : 16, 1024, kLayoutSwizzle128B);
+        constexpr uint64_t kSlotStep = kStageBytes >> 4;
         constexpr uint64_t kBStep = (DGRAD ? 4096 : 32) >> 4;
-        const uint32_t idesc = block_idesc(DGRAD);
+        const uint32_t idesc = block_idesc(DGRAD, kRows);
         for (int64_t tile = first_tile; ok && tile < total_tiles; tile += tile_step) {
           for (int b = 0; b < RB; ++b) {
             if (!warp_wait(tmem_empty(buf), acc_phase ^ 1u, sync, a.timeout_ns) ||
@@ -279,13 +330,13 @@ __global__ void __launch_bounds__(kBThreads, 1) gemm_block_pair_kernel(const __g
             if (elect_one()) {
 #pragma unroll
               for (int j = 0; j < 4; ++j)
-                tc_mma_pair_f8(d, a_desc0 + so + 2 * j, b_desc0 + so + kBStep * j, idesc, j > 0 ? 1u : 0u);
-              tc_commit_pair_mc(empty_bar(slot), 0x3);
-              tc_commit_pair_mc(tmem_full(buf), 0x3);
+                tc_mma_f8<G>(d, a_desc0 + so + 2 * j, b_desc0 + so + kBStep * j, idesc, j > 0 ? 1u : 0u);
+              tc_commit_all<G>(empty_bar(slot));
+              tc_commit_all<G>(tmem_full(buf));
             }
             __syncwarp();
             issued = true;
-            if (++slot == kBStages) {
+            if (++slot == kStages) {
               slot = 0;
               phase ^= 1u;
             }
@@ -294,8 +345,11 @@ __global__ void __launch_bounds__(kBThreads, 1) gemm_block_pair_kernel(const __g
           }
         }
         if (issued) {
-          // no MMA of the pair may still run when TMEM is freed
-          if (elect_one()) tc_commit_pair(drain_bar);
+          // no MMA may still run when TMEM is freed
+          if (elect_one()) {
+            if (G == 2) tc_commit_pair(drain_bar);
+            else tc_commit(drain_bar);
+          }
           __syncwarp();
           warp_wait(drain_bar, 0, sync, 100000000ull, true);
         }
@@ -310,7 +364,7 @@ __global__ void __launch_bounds__(kBThreads, 1) gemm_block_pair_kernel(const __g
       bool ok = true;
       for (int64_t tile = first_tile; ok && tile < total_tiles; tile += tile_step) {
         const BlockTile bt = block_tile(tile, tile_base, E, NT);
-        const int row_local = bt.mt * kBTileRows + (int)rank * 128;
+        const int row_local = bt.mt * kRows + (int)rank * 128;
         const int rows_here = min(128, row_count[bt.e] - row_local);
         const float* sx = a.x_scale + ((int64_t)row_begin[bt.e] + row_local) * RB;
         // the scale block of column half (lane >> 3): past the last column, the last one (unused)
@@ -344,14 +398,14 @@ __global__ void __launch_bounds__(kBThreads, 1) gemm_block_pair_kernel(const __g
     // ------------------------------------------------------------------ sums over blocks (both CTAs)
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kBEpiRegs));
     const int quad = warp & 3, half = (warp - kBFirstEpiWarp) >> 2;
-    const uint32_t leader_empty0 = mapa_shared(tmem_empty(0), 0);
+    const uint32_t leader_empty0 = G == 2 ? mapa_shared(tmem_empty(0), 0) : tmem_empty(0);
     const uint32_t tlane = tmem_base + ((uint32_t)(quad * 32) << 16) + (uint32_t)(half * 128);
     const float* scales = reinterpret_cast<const float*>(smem + kBScaleOff);
     uint32_t buf = 0, acc_phase = 0, sbuf = 0, sphase = 0;
     bool ok = true;
     for (int64_t tile = first_tile; ok && tile < total_tiles; tile += tile_step) {
       const BlockTile bt = block_tile(tile, tile_base, E, NT);
-      const int row_local = bt.mt * kBTileRows + (int)rank * 128 + quad * 32 + lane;
+      const int row_local = bt.mt * kRows + (int)rank * 128 + quad * 32 + lane;
       const bool valid = row_local < row_count[bt.e];
       const int col0 = bt.nt * kBTileCols + half * 128;
       const bool any = __any_sync(0xffffffffu, valid) && col0 < cols;
@@ -380,13 +434,17 @@ __global__ void __launch_bounds__(kBThreads, 1) gemm_block_pair_kernel(const __g
               float v[32];
               tc_ld_32x32b_x32(t + 32 * c, v);
               tc_wait_ld();
+              if (c == 3) {  // registers hold the block: release its accumulator before the last sums
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster_relaxed(leader_empty0 + 8u * buf);
+              }
 #pragma unroll
-              for (int i = 0; i < 32; ++i) acc[32 * c + i] = fmaf(v[i], s, acc[32 * c + i]);
+              for (int i = 0; i < 32; i += 2) fma_pair(acc[32 * c + i], acc[32 * c + i + 1], v[i], v[i + 1], s);
             }
-            tc_fence_before();
+          } else if (lane == 0) {
+            mbar_arrive_cluster_relaxed(leader_empty0 + 8u * buf);
           }
-          __syncwarp();
-          if (lane == 0) mbar_arrive_cluster_relaxed(leader_empty0 + 8u * buf);  // registers hold the block
           buf ^= 1u;
           if (buf == 0) acc_phase ^= 1u;
         }
@@ -466,18 +524,23 @@ __global__ void __launch_bounds__(kBThreads, 1) gemm_block_pair_kernel(const __g
   }
 
   tc_fence_before();
-  cluster_sync();  // both CTAs done with the pair's TMEM
-  // After an abort in either CTA, loads that were issued but never waited for may still be landing
-  // in this CTA's shared memory or on the even CTA's barriers: give them time before leaving.
-  const uint32_t peer_abort = ld_shared_cluster_u32(mapa_shared(smem_u32((const void*)abort_flag), rank ^ 1u));
-  if (*abort_flag || peer_abort) {
+  if (G == 2) cluster_sync();  // both CTAs done with the pair's TMEM
+  else __syncthreads();
+  // After an abort, loads that were issued but never waited for may still be landing in this CTA's
+  // shared memory or on the even CTA's barriers: give them time before leaving.
+  uint32_t aborted = *abort_flag;
+  if (G == 2) aborted |= ld_shared_cluster_u32(mapa_shared(smem_u32((const void*)abort_flag), rank ^ 1u));
+  if (aborted) {
     const uint64_t t0 = clock64();
     while (clock64() - t0 < 2000000ull) {
     }
   }
-  cluster_sync();
+  if (G == 2) cluster_sync();
   tc_fence_after();
-  if (warp == 1) tmem_dealloc_pair(tmem_base, 2 * kBTileCols);
+  if (warp == 1) {
+    if (G == 2) tmem_dealloc_pair(tmem_base, 2 * kBTileCols);
+    else tmem_dealloc(tmem_base, 2 * kBTileCols);
+  }
 }
 
 // ---------------------------------------------------------------------- host side
@@ -491,15 +554,15 @@ bool encode_codes(CUtensorMap* m, const uint8_t* base, int rank, const cuuint64_
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <bool DGRAD>
-cudaError_t launch_pair(const GemmBlockArgs& a, cudaStream_t s) {
+template <int G, bool DGRAD>
+cudaError_t launch_tiles(const GemmBlockArgs& a, cudaStream_t s) {
   static std::atomic<int> ready[64];  // per device: the kernel's shared-memory limit is set
   int dev = 0;
   cudaError_t err = cudaGetDevice(&dev);
   if (err != cudaSuccess) return err;
   if (dev >= 64) return cudaErrorInvalidDevice;
   if (!ready[dev].load(std::memory_order_acquire)) {
-    err = cudaFuncSetAttribute(gemm_block_pair_kernel<DGRAD>, cudaFuncAttributeMaxDynamicSharedMemorySize, kBSmemBytes);
+    err = cudaFuncSetAttribute(gemm_block_kernel<G, DGRAD>, cudaFuncAttributeMaxDynamicSharedMemorySize, kBSmemBytes);
     if (err != cudaSuccess) return err;
     ready[dev].store(1, std::memory_order_release);
   }
@@ -514,28 +577,33 @@ cudaError_t launch_pair(const GemmBlockArgs& a, cudaStream_t s) {
   const int64_t cols = DGRAD ? a.K : a.N;
   p.out_vec = reinterpret_cast<uintptr_t>(a.out) % 32 == 0 && (cols * dtype_bytes(a.out_dtype)) % 32 == 0;
   // every group adds at most one partial row tile
-  const int64_t mtiles = (a.M + kBTileRows - 1) / kBTileRows + a.E - 1;
+  const int64_t mtiles = (a.M + BlockGeo<G>::kRows - 1) / BlockGeo<G>::kRows + a.E - 1;
   const int64_t tiles = mtiles * ((cols + kBTileCols - 1) / kBTileCols);
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.x = G;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
-  cfg.gridDim = dim3((unsigned)(2 * std::min<int64_t>(tiles, a.num_sms / 2)));
+  cfg.gridDim = dim3((unsigned)(G * std::min<int64_t>(tiles, a.num_sms / G)));
   cfg.blockDim = dim3(kBThreads);
   cfg.dynamicSmemBytes = kBSmemBytes;
   cfg.stream = s;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, gemm_block_pair_kernel<DGRAD>, p);
+  cfg.numAttrs = G == 2 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, gemm_block_kernel<G, DGRAD>, p);
 }
 
 }  // namespace
 
+// up to this many rows per group on average, tiles on single CTAs (see the header)
+constexpr int64_t kSingleMaxRowsPerGroup = 128;
+
 cudaError_t launch_gemm_block(const GemmBlockArgs& a, cudaStream_t s) {
   if (a.M == 0) return cudaSuccess;
-  return a.dgrad ? launch_pair<true>(a, s) : launch_pair<false>(a, s);
+  if (a.M <= kSingleMaxRowsPerGroup * (int64_t)a.E)
+    return a.dgrad ? launch_tiles<1, true>(a, s) : launch_tiles<1, false>(a, s);
+  return a.dgrad ? launch_tiles<2, true>(a, s) : launch_tiles<2, false>(a, s);
 }
 
 }  // namespace moe
