@@ -144,11 +144,13 @@ def _check(status: int, where: str):
 
 
 def _stream(stream):
+    """The stream's handle; None: the current stream (torch.cuda.current_stream() builds a Stream
+    object, 3 us a call; the raw handle costs 0.1)."""
     if stream is None:
-        return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     if isinstance(stream, torch.cuda.Stream):
-        return ctypes.c_void_p(stream.cuda_stream)
-    return ctypes.c_void_p(int(stream))
+        return stream.cuda_stream
+    return int(stream)
 
 
 def _p(t):
@@ -271,7 +273,7 @@ def moe_forward_ex(x, gate_logits, w1, w1_scale, w2, w2_scale, out, E, k, worksp
                     w1=w1.data_ptr(), w1_scale=w1_scale.data_ptr(), w2=w2.data_ptr(), w2_scale=w2_scale.data_ptr(),
                     out=out.data_ptr(), T=T, H=H, I=w2.shape[-1] * 2, E=int(E), k=int(k),
                     workspace=workspace.data_ptr(), workspace_bytes=workspace.numel() * workspace.element_size(),
-                    stream=_stream(stream).value, schedule=int(schedule))
+                    stream=_stream(stream), schedule=int(schedule))
     _check(lib().moe_forward_ex(ctypes.byref(a)), "moe_forward_ex")
 
 
@@ -360,150 +362,165 @@ def workspace_views(workspace, T, H, I, E, k, fmt=MOE_ACT_MXFP8):
 
 
 # ---------------------------------------------------------------- expert rows and FP8 experts
-# The C entry points see only pointers, so these bindings check what a pointer cannot tell:
-# element types, shapes and strides (MOE_ERR_INVALID_ARG naming the tensor).
+# The C entry points see only pointers, so these bindings check what a pointer cannot tell: element
+# types, shapes, strides and the device (MOE_ERR_INVALID_ARG naming the tensor).  A decode step is a
+# few microseconds on the GPU, so each binding makes one plain test of everything first; only when
+# it fails do the _want / _matrix / _table checks run, which say what is wrong.
+_F32, _I32, _I64, _U8 = torch.float32, torch.int32, torch.int64, torch.uint8
+
 
 def _want(ok: bool, where: str, what: str):
     if not ok:
         raise MoeError(1, f"{where}: {what}")
 
 
-def _on_gpu(where, *tensors):
-    for t in tensors:
-        if t is not None and not t.is_cuda:
-            raise MoeError(1, f"{where}: every tensor must be on the GPU")
-
-
-def _rows_of(t, where, name):
-    """(row stride, columns) of a row-major matrix with unit column stride."""
-    _want(t.dim() == 2 and (t.stride(1) == 1 or t.shape[1] <= 1), where, f"{name} must be [rows, columns] with unit column stride")
-    return (t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])), t.shape[1]
+def _matrix(t, where, name, shape, dtypes=None):
+    """A row-major matrix on the GPU with unit column stride; None in ``shape``: any size."""
+    _want(t is not None and t.dim() == 2, where, f"{name} must be a matrix")
+    _want(all(n is None or n == m for n, m in zip(shape, t.shape)), where,
+          f"{name} has shape {list(t.shape)}, expected {list(shape)}")
+    _want(t.stride(1) == 1 or t.shape[1] <= 1, where, f"{name} must have unit column stride")
+    _want(dtypes is None or t.dtype in dtypes, where, f"{name} has the unsupported type {t.dtype}")
+    _want(t.is_cuda, where, f"{name} must be on the GPU")
 
 
 def _table(t, dtype, shape, where, name):
-    _want(t.dtype == dtype and tuple(t.shape) == tuple(shape) and t.is_contiguous(), where,
-          f"{name} must be a contiguous {dtype} tensor of shape {list(shape)}")
+    _want(t is not None and t.dtype == dtype, where, f"{name} must be {dtype}")
+    _want(len(t.shape) == len(shape) and all(n is None or n == m for n, m in zip(shape, t.shape)), where,
+          f"{name} has shape {list(t.shape)}, expected {list(shape)}")
+    _want(t.is_contiguous(), where, f"{name} must be contiguous")
+    _want(t.is_cuda, where, f"{name} must be on the GPU")
 
 
-def _inv(inv, where):
-    _want(inv.dtype == torch.int32 and inv.dim() == 2 and inv.is_contiguous(), where,
-          "inv must be a contiguous int32 tensor [T, k]")
-    return inv.shape
+def _plain(t, dtype):
+    """Whether a matrix plainly passes _matrix (unit column stride, rows that do not overlap)."""
+    return t.dtype is dtype and t.is_cuda and t.dim() == 2 and t.stride(1) == 1
+
+
+def _stride(t):
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+
+
+def _fixed(t, dtype):
+    return t.dtype is dtype and t.is_cuda and t.is_contiguous()
+
+
+_ROWS = (torch.bfloat16, torch.float16, torch.float32)
 
 
 def moe_permute(x, inv, rows, stream=None):
     """rows[inv[t, j]] = x[t]: x [T, H], inv int32 [T, k] (outside [0, R): dropped) -> rows [R, H]."""
-    fn = "moe_permute"
-    T, k = _inv(inv, fn)
-    xs, H = _rows_of(x, fn, "x")
-    rs, Hr = _rows_of(rows, fn, "rows")
-    _want(x.shape[0] == T and Hr == H, fn, "x must be [T, H] and rows [R, H]")
-    _want(x.dtype == rows.dtype and x.dtype in _DTYPES, fn, "x and rows must share a type (bf16, f16, f32, u8)")
-    _on_gpu(fn, x, inv, rows)
-    _check(lib().moe_permute(x.data_ptr(), xs, _DTYPES[x.dtype], inv.data_ptr(), T, H, k, rows.data_ptr(), rs,
-                             rows.shape[0], _stream(stream)), fn)
-
-
-def _gather(fn, rows, inv, topk_w, out, stream):
-    T, k = _inv(inv, fn)
-    rs, H = _rows_of(rows, fn, "the expert rows")
-    os_, Ho = _rows_of(out, fn, "the token rows")
-    _want(out.shape[0] == T and Ho == H, fn, "token rows must be [T, H] and expert rows [R, H]")
-    _want(rows.dtype == out.dtype and rows.dtype in _DTYPES, fn, "both row matrices must share a type (bf16, f16, f32)")
-    if topk_w is not None:
-        _table(topk_w, torch.float32, (T, k), fn, "topk_w")
-    _on_gpu(fn, rows, inv, topk_w, out)
-    L = lib()
-    if topk_w is None:
-        st = L.moe_permute_backward(rows.data_ptr(), rs, rows.shape[0], _DTYPES[rows.dtype], inv.data_ptr(), T, H, k,
-                                    out.data_ptr(), os_, _stream(stream))
-    else:
-        st = L.moe_unpermute(rows.data_ptr(), rs, rows.shape[0], _DTYPES[rows.dtype], inv.data_ptr(),
-                             topk_w.data_ptr(), T, H, k, out.data_ptr(), os_, _stream(stream))
-    _check(st, fn)
+    dt = x.dtype
+    if not (dt in _DTYPES and _plain(x, dt) and _plain(rows, dt) and _fixed(inv, _I32) and inv.dim() == 2 and
+            inv.shape[0] == x.shape[0] and rows.shape[1] == x.shape[1]):
+        fn = "moe_permute"
+        _table(inv, _I32, (None, None), fn, "inv")
+        _matrix(x, fn, "x", (inv.shape[0], None), _DTYPES)
+        _matrix(rows, fn, "rows", (None, x.shape[1]), (dt,))
+    T, H = x.shape
+    _check(lib().moe_permute(x.data_ptr(), _stride(x), _DTYPES[dt], inv.data_ptr(), T, H, inv.shape[1],
+                             rows.data_ptr(), _stride(rows), rows.shape[0], _stream(stream)), "moe_permute")
 
 
 def moe_permute_backward(d_rows, inv, d_x, stream=None):
     """Gradient of moe_permute: d_x[t] = sum_j d_rows[inv[t, j]]."""
-    _gather("moe_permute_backward", d_rows, inv, None, d_x, stream)
+    dt = d_rows.dtype
+    if not (dt in _ROWS and _plain(d_rows, dt) and _plain(d_x, dt) and _fixed(inv, _I32) and inv.dim() == 2 and
+            inv.shape[0] == d_x.shape[0] and d_rows.shape[1] == d_x.shape[1]):
+        fn = "moe_permute_backward"
+        _table(inv, _I32, (None, None), fn, "inv")
+        _matrix(d_rows, fn, "d_rows", (None, None), _ROWS)
+        _matrix(d_x, fn, "d_x", (inv.shape[0], d_rows.shape[1]), (dt,))
+    T, H = d_x.shape
+    _check(lib().moe_permute_backward(d_rows.data_ptr(), _stride(d_rows), d_rows.shape[0], _DTYPES[dt], inv.data_ptr(),
+                                      T, H, inv.shape[1], d_x.data_ptr(), _stride(d_x), _stream(stream)),
+           "moe_permute_backward")
 
 
 def moe_unpermute(rows, inv, topk_w, out, stream=None):
     """out[t] = sum_j topk_w[t, j] rows[inv[t, j]]: rows [R, H], topk_w fp32 [T, k] -> out [T, H]."""
-    _want(topk_w is not None, "moe_unpermute", "topk_w is required")
-    _gather("moe_unpermute", rows, inv, topk_w, out, stream)
+    dt = rows.dtype
+    if not (topk_w is not None and dt in _ROWS and _plain(rows, dt) and _plain(out, dt) and _fixed(inv, _I32) and
+            _fixed(topk_w, _F32) and inv.dim() == 2 and inv.shape == topk_w.shape and
+            inv.shape[0] == out.shape[0] and rows.shape[1] == out.shape[1]):
+        fn = "moe_unpermute"
+        _table(inv, _I32, (None, None), fn, "inv")
+        _matrix(rows, fn, "rows", (None, None), _ROWS)
+        _matrix(out, fn, "out", (inv.shape[0], rows.shape[1]), (dt,))
+        _table(topk_w, _F32, inv.shape, fn, "topk_w")
+    T, H = out.shape
+    _check(lib().moe_unpermute(rows.data_ptr(), _stride(rows), rows.shape[0], _DTYPES[dt], inv.data_ptr(),
+                               topk_w.data_ptr(), T, H, inv.shape[1], out.data_ptr(), _stride(out), _stream(stream)),
+           "moe_unpermute")
 
 
 def moe_unpermute_backward(d_out, rows, inv, topk_w, d_rows, d_topk_w, stream=None):
     """Gradients of moe_unpermute: d_rows[inv[t, j]] = topk_w[t, j] d_out[t] and d_topk_w[t, j] =
     <d_out[t], rows[inv[t, j]]>.  Either result may be None; rows may be None without d_topk_w."""
     fn = "moe_unpermute_backward"
-    T, k = _inv(inv, fn)
-    ds, H = _rows_of(d_out, fn, "d_out")
-    _want(d_out.shape[0] == T and d_out.dtype in _DTYPES, fn, "d_out must be [T, H] of bf16, f16 or f32")
-    _table(topk_w, torch.float32, (T, k), fn, "topk_w")
-    _want(d_topk_w is None or rows is not None, fn, "d_topk_w needs rows")
-    R, strides = 0, []
-    for name, t in (("rows", rows if d_topk_w is not None else None), ("d_rows", d_rows)):
-        if t is None:
-            strides.append(0)
-            continue
-        st, Ht = _rows_of(t, fn, name)
-        _want(Ht == H and t.dtype == d_out.dtype, fn, f"{name} must be [R, H] of d_out's type")
-        _want(not strides or not strides[0] or t.shape[0] == R, fn, "rows and d_rows must have the same rows")
-        R = t.shape[0]
-        strides.append(st)
+    _table(inv, _I32, (None, None), fn, "inv")
+    T, k = inv.shape
+    _matrix(d_out, fn, "d_out", (T, None), _ROWS)
+    dt, H = d_out.dtype, d_out.shape[1]
+    _table(topk_w, _F32, (T, k), fn, "topk_w")
+    R = rp = rs = dp = ds = 0
+    if d_rows is not None:
+        _matrix(d_rows, fn, "d_rows", (None, H), (dt,))
+        R, dp, ds = d_rows.shape[0], d_rows.data_ptr(), _stride(d_rows)
     if d_topk_w is not None:
-        _table(d_topk_w, torch.float32, (T, k), fn, "d_topk_w")
-    _on_gpu(fn, d_out, rows, inv, topk_w, d_rows, d_topk_w)
-    ptr = lambda t: None if t is None else t.data_ptr()  # noqa: E731
-    _check(lib().moe_unpermute_backward(d_out.data_ptr(), ds, ptr(rows if d_topk_w is not None else None), strides[0],
-                                        R, _DTYPES[d_out.dtype], inv.data_ptr(), topk_w.data_ptr(), T, H, k,
-                                        ptr(d_rows), strides[1], ptr(d_topk_w), _stream(stream)), fn)
+        _table(d_topk_w, _F32, (T, k), fn, "d_topk_w")
+        _matrix(rows, fn, "rows", (None if d_rows is None else R, H), (dt,))
+        R, rp, rs = rows.shape[0], rows.data_ptr(), _stride(rows)
+    _check(lib().moe_unpermute_backward(d_out.data_ptr(), _stride(d_out), rp, rs, R, _DTYPES[dt], inv.data_ptr(),
+                                        topk_w.data_ptr(), T, H, k, dp, ds,
+                                        None if d_topk_w is None else d_topk_w.data_ptr(), _stream(stream)), fn)
 
 
 def moe_topk_route_backward(topk_ids, topk_w, d_topk_w, d_logits, stream=None):
     """Gradient of moe_topk_route's weights: ids int32, topk_w and d_topk_w fp32 [T, k] -> d_logits fp32 [T, E]."""
-    fn = "moe_topk_route_backward"
-    _want(d_logits.dim() == 2 and topk_ids.dim() == 2, fn, "topk_ids must be [T, k] and d_logits [T, E]")
+    if not (_fixed(topk_ids, _I32) and _fixed(topk_w, _F32) and _fixed(d_topk_w, _F32) and _fixed(d_logits, _F32) and
+            topk_ids.dim() == 2 and d_logits.dim() == 2 and topk_ids.shape == topk_w.shape == d_topk_w.shape and
+            topk_ids.shape[0] == d_logits.shape[0]):
+        fn = "moe_topk_route_backward"
+        _table(topk_ids, _I32, (None, None), fn, "topk_ids")
+        _table(topk_w, _F32, topk_ids.shape, fn, "topk_w")
+        _table(d_topk_w, _F32, topk_ids.shape, fn, "d_topk_w")
+        _table(d_logits, _F32, (topk_ids.shape[0], None), fn, "d_logits")
     T, E = d_logits.shape
-    shape = (T, topk_ids.shape[1])
-    _table(topk_ids, torch.int32, shape, fn, "topk_ids")
-    _table(topk_w, torch.float32, shape, fn, "topk_w")
-    _table(d_topk_w, torch.float32, shape, fn, "d_topk_w")
-    _table(d_logits, torch.float32, (T, E), fn, "d_logits")
-    _on_gpu(fn, topk_ids, topk_w, d_topk_w, d_logits)
-    _check(lib().moe_topk_route_backward(topk_ids.data_ptr(), topk_w.data_ptr(), d_topk_w.data_ptr(), T, E, shape[1],
-                                         d_logits.data_ptr(), _stream(stream)), fn)
+    _check(lib().moe_topk_route_backward(topk_ids.data_ptr(), topk_w.data_ptr(), d_topk_w.data_ptr(), T, E,
+                                         topk_ids.shape[1], d_logits.data_ptr(), _stream(stream)),
+           "moe_topk_route_backward")
 
 
 def moe_quantize_fp8_block(x, codes, scales, block_rows=1, stream=None):
     """x [rows, K] -> E4M3 codes u8 [rows, K] and fp32 scales [ceil(rows / block_rows), ceil(K / 128)],
     block_rows = 1 or 128."""
     fn = "moe_quantize_fp8_block"
-    xs, K = _rows_of(x, fn, "x")
-    rows = x.shape[0]
-    _want(x.dtype in _DTYPES, fn, "x must be bf16, f16 or f32")
     _want(block_rows in (1, 128), fn, "block_rows must be 1 or 128")
-    _table(codes, torch.uint8, (rows, K), fn, "codes")
-    _table(scales, torch.float32, (-(-rows // block_rows), -(-K // 128)), fn, "scales")
-    _on_gpu(fn, x, codes, scales)
-    _check(lib().moe_quantize_fp8_block(x.data_ptr(), xs, _DTYPES[x.dtype], rows, K, block_rows, codes.data_ptr(),
-                                        scales.data_ptr(), _stream(stream)), fn)
+    _matrix(x, fn, "x", (None, None), _ROWS)
+    rows, K = x.shape
+    _table(codes, _U8, (rows, K), fn, "codes")
+    _table(scales, _F32, (-(-rows // block_rows), -(-K // 128)), fn, "scales")
+    _check(lib().moe_quantize_fp8_block(x.data_ptr(), _stride(x), _DTYPES[x.dtype], rows, K, block_rows,
+                                        codes.data_ptr(), scales.data_ptr(), _stream(stream)), fn)
 
 
 def moe_permute_quantize_fp8_block(x, inv, codes, scales, stream=None):
     """moe_permute and moe_quantize_fp8_block in one pass: codes u8 [R, K], scales fp32 [R, ceil(K / 128)]."""
-    fn = "moe_permute_quantize_fp8_block"
-    T, k = _inv(inv, fn)
-    xs, K = _rows_of(x, fn, "x")
-    _want(x.shape[0] == T and x.dtype in _DTYPES, fn, "x must be [T, K] of bf16, f16 or f32")
-    R = codes.shape[0]
-    _table(codes, torch.uint8, (R, K), fn, "codes")
-    _table(scales, torch.float32, (R, -(-K // 128)), fn, "scales")
-    _on_gpu(fn, x, inv, codes, scales)
-    _check(lib().moe_permute_quantize_fp8_block(x.data_ptr(), xs, _DTYPES[x.dtype], inv.data_ptr(), T, K, k,
-                                                codes.data_ptr(), scales.data_ptr(), R, _stream(stream)), fn)
+    dt = x.dtype
+    if not (dt in _ROWS and _plain(x, dt) and _fixed(inv, _I32) and _fixed(codes, _U8) and _fixed(scales, _F32) and
+            inv.dim() == 2 and codes.dim() == 2 and scales.dim() == 2 and inv.shape[0] == x.shape[0] and
+            codes.shape[1] == x.shape[1] and scales.shape[0] == codes.shape[0] and
+            scales.shape[1] == (x.shape[1] + 127) // 128):
+        fn = "moe_permute_quantize_fp8_block"
+        _table(inv, _I32, (None, None), fn, "inv")
+        _matrix(x, fn, "x", (inv.shape[0], None), _ROWS)
+        _table(codes, _U8, (None, x.shape[1]), fn, "codes")
+        _table(scales, _F32, (codes.shape[0], (x.shape[1] + 127) // 128), fn, "scales")
+    T, K = x.shape
+    _check(lib().moe_permute_quantize_fp8_block(x.data_ptr(), _stride(x), _DTYPES[dt], inv.data_ptr(), T, K,
+                                                inv.shape[1], codes.data_ptr(), scales.data_ptr(), codes.shape[0],
+                                                _stream(stream)), "moe_permute_quantize_fp8_block")
 
 
 def moe_gemm_fp8_block_workspace_bytes(M, N, K, E) -> int:
@@ -511,21 +528,28 @@ def moe_gemm_fp8_block_workspace_bytes(M, N, K, E) -> int:
 
 
 def _gemm_block(fn, dgrad, x, x_scale, w, w_scale, out, workspace, offsets, stream):
-    _want(w.dim() == 3 and w.dtype == torch.uint8 and w.is_contiguous(), fn, "w must be a contiguous uint8 tensor [E, N, K]")
+    if w.dim() != 3:
+        _table(w, _U8, (None, None, None), fn, "w")
     E, N, K = w.shape
     inner, outer = (N, K) if dgrad else (K, N)
-    M = x.shape[0]
-    _table(x, torch.uint8, (M, inner), fn, "the codes")
-    _table(x_scale, torch.float32, (M, -(-inner // 128)), fn, "the codes' scales")
-    _table(w_scale, torch.float32, (E, -(-N // 128), -(-K // 128)), fn, "w_scale")
-    _want(out.dtype in _DTYPES, fn, "the output must be bf16, f16 or f32")
-    _table(out, out.dtype, (M, outer), fn, "the output")
-    if offsets is not None:
-        _table(offsets, torch.int64, (E + 1,), fn, "offsets")
-    _on_gpu(fn, x, x_scale, w, w_scale, out, workspace, offsets)
+    M, dt = x.shape[0], out.dtype
+    if not (_fixed(w, _U8) and _fixed(x, _U8) and _fixed(x_scale, _F32) and _fixed(w_scale, _F32) and dt in _ROWS and
+            _fixed(out, dt) and workspace.is_cuda and x.shape == (M, inner) and out.shape == (M, outer) and
+            x_scale.shape == (M, (inner + 127) // 128) and
+            w_scale.shape == (E, (N + 127) // 128, (K + 127) // 128) and
+            (offsets is None or _fixed(offsets, _I64) and offsets.shape == (E + 1,))):
+        _table(w, _U8, (None, None, None), fn, "w")
+        _table(w_scale, _F32, (E, (N + 127) // 128, (K + 127) // 128), fn, "w_scale")
+        _table(x, _U8, (M, inner), fn, "the codes")
+        _table(x_scale, _F32, (M, (inner + 127) // 128), fn, "the codes' scales")
+        _want(dt in _ROWS, fn, "the output must be bf16, f16 or f32")
+        _table(out, dt, (M, outer), fn, "the output")
+        if offsets is not None:
+            _table(offsets, _I64, (E + 1,), fn, "offsets")
+        _want(workspace.is_cuda, fn, "the workspace must be on the GPU")
     _check(getattr(lib(), fn)(x.data_ptr(), x_scale.data_ptr(), w.data_ptr(), w_scale.data_ptr(),
                               None if offsets is None else offsets.data_ptr(), M, N, K, E, out.data_ptr(),
-                              _DTYPES[out.dtype], workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                              _DTYPES[dt], workspace.data_ptr(), workspace.numel() * workspace.element_size(),
                               _stream(stream)), fn)
 
 

@@ -78,5 +78,8 @@ struct GemmBlockArgs {
   int test_stall;
 };
 cudaError_t launch_gemm_block(const GemmBlockArgs& a, cudaStream_t s);
+// gemv_block.cu: the forward product of a few rows, and whether a product is one.
+bool use_gemv(const GemmBlockArgs& a);
+cudaError_t launch_gemv_block(const GemmBlockArgs& a, cudaStream_t s);
 
 }  // namespace moe

@@ -49,6 +49,7 @@ constexpr int kBTileCols = 256;                     // output columns of a tile
 constexpr int kBHalfBytes = 128 * 128;              // 128 rows of x, or 128 of the tile's weight rows
 constexpr int kBRingBytes = 6 * 2 * kBHalfBytes;    // 192 KiB: 6 stages of a pair's CTA, 4 of a single CTA
 constexpr int kBMaxStages = 6;
+constexpr int kBMaxSplit = 8;
 constexpr int kBOutOff = kBRingBytes;   // per-warp staging of unaligned output rows
 constexpr int kBOutBytes = 32 * 32;                 // 32 rows x 32 bytes
 constexpr int kBScaleBlocks = 8;                    // reduction blocks of one scale chunk
@@ -70,11 +71,15 @@ struct BlockGeo {
   static constexpr int kStages = kBRingBytes / kStageBytes;
 };
 
+// Up to this many rows per group on average, tiles run on single CTAs.
+constexpr int64_t kSingleMaxRowsPerGroup = 128;
+
 struct BlockParams {  // 64-byte aligned through its CUtensorMap members
   CUtensorMap tmap_x;  // codes [M, reduction], box 128 B x 128 rows
   CUtensorMap tmap_w;  // codes [E, N, K], box 128 B x 128 rows x 1
   GemmBlockArgs a;
   int out_vec;         // output rows start on 32-byte boundaries
+  int split;           // SPLIT: CTAs that share the reduction of a tile
 };
 
 // Instruction descriptor of kind::f8f6f4: fp32 accumulator (bit 4), E4M3 operands, B read along its
@@ -168,8 +173,9 @@ __device__ __forceinline__ BlockTile block_tile(int64_t tile, const int32_t* bas
   return {lo, (int)(local % (uint32_t)mt_e), (int)(local / (uint32_t)mt_e)};
 }
 
-template <int G, bool DGRAD>
+template <int G, bool DGRAD, bool SPLIT>
 __global__ void __launch_bounds__(kBThreads, 1) gemm_block_kernel(const __grid_constant__ BlockParams p) {
+  static_assert(G == 1 || !SPLIT, "split tiles run on single CTAs");
   constexpr int kStages = BlockGeo<G>::kStages, kStageBytes = BlockGeo<G>::kStageBytes, kRows = BlockGeo<G>::kRows;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -254,8 +260,13 @@ __global__ void __launch_bounds__(kBThreads, 1) gemm_block_kernel(const __grid_c
   const int KB = (a.K + kFp8Block - 1) / kFp8Block, NB = (a.N + kFp8Block - 1) / kFp8Block;
   const int RB = (red + kFp8Block - 1) / kFp8Block;
   const int NT = (cols + kBTileCols - 1) / kBTileCols;
-  const int64_t total_tiles = (int64_t)tile_base[E] * NT;
-  const int64_t first_tile = G == 2 ? cluster_index() : blockIdx.x, tile_step = G == 2 ? cluster_count() : gridDim.x;
+  int64_t total_tiles = (int64_t)tile_base[E] * NT;
+  if (SPLIT) total_tiles = min(total_tiles, (int64_t)cluster_count());  // one tile a cluster
+  constexpr bool kCluster = G == 2 || SPLIT;  // a cluster works on a tile
+  const int64_t first_tile = kCluster ? cluster_index() : blockIdx.x, tile_step = kCluster ? cluster_count() : gridDim.x;
+  // this CTA's blocks of the reduction (SPLIT: CTA i of the S of its cluster takes the i-th part)
+  const uint32_t part = SPLIT ? cluster_ctarank() : 0, parts = SPLIT ? (uint32_t)p.split : 1;
+  const int b_lo = (int)((uint32_t)RB * part / parts), b_hi = (int)((uint32_t)RB * (part + 1) / parts);
 
   if (warp < kBFirstEpiWarp) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kBCtlRegs));
@@ -273,7 +284,7 @@ __global__ void __launch_bounds__(kBThreads, 1) gemm_block_kernel(const __grid_c
         const int row0 = row_begin[bt.e] + bt.mt * kRows + (int)rank * 128;
         const int col0 = bt.nt * kBTileCols + (int)rank * 128;
         const uint32_t tx = (uint32_t)kBHalfBytes * (peer_real ? 4u : 3u);  // of every CTA of the tile
-        for (int b = 0; b < RB; ++b) {
+        for (int b = b_lo; b < b_hi; ++b) {
           if (!warp_wait(empty_bar(slot), phase ^ 1u, sync, a.timeout_ns)) {
             ok = false;
             break;
@@ -318,7 +329,7 @@ __global__ void __launch_bounds__(kBThreads, 1) gemm_block_kernel(const __grid_c
         constexpr uint64_t kBStep = (DGRAD ? 4096 : 32) >> 4;
         const uint32_t idesc = block_idesc(DGRAD, kRows);
         for (int64_t tile = first_tile; ok && tile < total_tiles; tile += tile_step) {
-          for (int b = 0; b < RB; ++b) {
+          for (int b = b_lo; b < b_hi; ++b) {
             if (!warp_wait(tmem_empty(buf), acc_phase ^ 1u, sync, a.timeout_ns) ||
                 !warp_wait(full_bar(slot), phase, sync, a.timeout_ns)) {
               ok = false;
@@ -370,8 +381,8 @@ __global__ void __launch_bounds__(kBThreads, 1) gemm_block_kernel(const __grid_c
         // the scale block of column half (lane >> 3): past the last column, the last one (unused)
         const int cb = min(bt.nt * 2 + ((lane >> 3) & 1), (DGRAD ? KB : NB) - 1);
         const float* sw = a.w_scale + (int64_t)bt.e * NB * KB + (DGRAD ? cb : cb * KB);
-        for (int b0 = 0; b0 < RB; b0 += kBScaleBlocks) {
-          const bool in = b0 + j < RB;
+        for (int b0 = b_lo; b0 < b_hi; b0 += kBScaleBlocks) {
+          const bool in = b0 + j < b_hi;
           float v[16], wv = 0.0f;
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
@@ -413,13 +424,13 @@ __global__ void __launch_bounds__(kBThreads, 1) gemm_block_kernel(const __grid_c
       float acc[128];
 #pragma unroll
       for (int i = 0; i < 128; ++i) acc[i] = 0.0f;
-      for (int b0 = 0; ok && b0 < RB; b0 += kBScaleBlocks) {
+      for (int b0 = b_lo; ok && b0 < b_hi; b0 += kBScaleBlocks) {
         if (!sums_wait(scale_full(sbuf), sphase, sync)) {
           ok = false;
           break;
         }
         const float* sc = scales + sbuf * (kBScaleBytes / 4);
-        const int nb = min(kBScaleBlocks, RB - b0);
+        const int nb = min(kBScaleBlocks, b_hi - b0);
         for (int b = 0; b < nb; ++b) {
           const float s = sc[b * kBScaleRows + quad * 32 + lane] * sc[b * kBScaleRows + 128 + half];
           if (!sums_wait(tmem_full(buf), acc_phase, sync)) {
@@ -455,7 +466,17 @@ __global__ void __launch_bounds__(kBThreads, 1) gemm_block_kernel(const __grid_c
       }
       if (!ok || !any) continue;
       const int dt = a.out_dtype;
-      if (p.out_vec && col0 + 128 <= cols) {
+      if (SPLIT) {
+        // this CTA's partial sums, [row][column] in the ring (every stage has been consumed: the last
+        // accumulator is complete), 16-byte chunks of a row swizzled by the row
+        if (valid) {
+          float* prow = reinterpret_cast<float*>(smem) + (quad * 32 + lane) * kBTileCols;
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            *reinterpret_cast<float4*>(prow + (((half * 32 + i) ^ (lane & 7)) << 2)) =
+                make_float4(acc[4 * i], acc[4 * i + 1], acc[4 * i + 2], acc[4 * i + 3]);
+        }
+      } else if (p.out_vec && col0 + 128 <= cols) {
         // 32-byte stores: every lane fills whole sectors of its own row
         if (valid) {
           if (dt == kDtF32) {
@@ -524,8 +545,31 @@ __global__ void __launch_bounds__(kBThreads, 1) gemm_block_kernel(const __grid_c
   }
 
   tc_fence_before();
-  if (G == 2) cluster_sync();  // both CTAs done with the pair's TMEM
+  if (kCluster) cluster_sync();  // both CTAs done with the pair's TMEM; every part's sums are in place
   else __syncthreads();
+  if (SPLIT && first_tile < total_tiles) {
+    // CTA i sums columns [256 i / S, 256 (i + 1) / S) of the tile over the parts, in part order
+    const BlockTile bt = block_tile(first_tile, tile_base, E, NT);
+    const int rows_here = min(kRows, row_count[bt.e] - bt.mt * kRows);
+    const int width = kBTileCols / (int)parts, c0 = (int)part * width;
+    const int64_t row0 = (int64_t)row_begin[bt.e] + bt.mt * kRows;
+    uint32_t src[kBMaxSplit];
+#pragma unroll
+    for (int q = 0; q < kBMaxSplit; ++q) src[q] = mapa_shared(sbase, (uint32_t)q < parts ? q : 0);
+    for (int i = threadIdx.x; i < rows_here * width; i += kBThreads) {
+      const int r = i / width, c = c0 + i % width, col = bt.nt * kBTileCols + c;
+      if (col >= cols) continue;
+      const uint32_t at = (uint32_t)(r * kBTileCols + ((((c >> 2) ^ (r & 7)) << 2) | (c & 3))) * 4u;
+      float v[kBMaxSplit], sum = 0.0f;
+#pragma unroll
+      for (int q = 0; q < kBMaxSplit; ++q) v[q] = (uint32_t)q < parts ? __uint_as_float(ld_shared_cluster_u32(src[q] + at)) : 0.0f;
+#pragma unroll
+      for (int q = 0; q < kBMaxSplit; ++q) sum += v[q];
+      const int64_t o = (row0 + r) * cols + col;
+      if (a.out_dtype == kDtF32) static_cast<float*>(a.out)[o] = sum;
+      else static_cast<uint16_t*>(a.out)[o] = (uint16_t)out_pair(sum, 0.0f, a.out_dtype);
+    }
+  }
   // After an abort, loads that were issued but never waited for may still be landing in this CTA's
   // shared memory or on the even CTA's barriers: give them time before leaving.
   uint32_t aborted = *abort_flag;
@@ -535,7 +579,7 @@ __global__ void __launch_bounds__(kBThreads, 1) gemm_block_kernel(const __grid_c
     while (clock64() - t0 < 2000000ull) {
     }
   }
-  if (G == 2) cluster_sync();
+  if (kCluster) cluster_sync();
   tc_fence_after();
   if (warp == 1) {
     if (G == 2) tmem_dealloc_pair(tmem_base, 2 * kBTileCols);
@@ -554,15 +598,22 @@ bool encode_codes(CUtensorMap* m, const uint8_t* base, int rank, const cuuint64_
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int G, bool DGRAD>
-cudaError_t launch_tiles(const GemmBlockArgs& a, cudaStream_t s) {
+// Row tiles of 128 G rows: every group adds at most one partial tile.
+int64_t max_row_tiles(const GemmBlockArgs& a, int rows) {
+  const int64_t groups = std::min<int64_t>(a.E, a.M);
+  return (a.M + (int64_t)(rows - 1) * groups) / rows;
+}
+
+template <int G, bool DGRAD, bool SPLIT>
+cudaError_t launch_tiles(const GemmBlockArgs& a, int64_t tiles, int split, cudaStream_t s) {
   static std::atomic<int> ready[64];  // per device: the kernel's shared-memory limit is set
   int dev = 0;
   cudaError_t err = cudaGetDevice(&dev);
   if (err != cudaSuccess) return err;
   if (dev >= 64) return cudaErrorInvalidDevice;
   if (!ready[dev].load(std::memory_order_acquire)) {
-    err = cudaFuncSetAttribute(gemm_block_kernel<G, DGRAD>, cudaFuncAttributeMaxDynamicSharedMemorySize, kBSmemBytes);
+    err = cudaFuncSetAttribute(gemm_block_kernel<G, DGRAD, SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               kBSmemBytes);
     if (err != cudaSuccess) return err;
     ready[dev].store(1, std::memory_order_release);
   }
@@ -576,34 +627,84 @@ cudaError_t launch_tiles(const GemmBlockArgs& a, cudaStream_t s) {
   p.a = a;
   const int64_t cols = DGRAD ? a.K : a.N;
   p.out_vec = reinterpret_cast<uintptr_t>(a.out) % 32 == 0 && (cols * dtype_bytes(a.out_dtype)) % 32 == 0;
-  // every group adds at most one partial row tile
-  const int64_t mtiles = (a.M + BlockGeo<G>::kRows - 1) / BlockGeo<G>::kRows + a.E - 1;
-  const int64_t tiles = mtiles * ((cols + kBTileCols - 1) / kBTileCols);
+  p.split = split;
+  const int ctas = SPLIT ? split : G;  // of a tile
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = G;
+  attr[0].val.clusterDim.x = (unsigned)ctas;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
-  cfg.gridDim = dim3((unsigned)(G * std::min<int64_t>(tiles, a.num_sms / G)));
+  // split tiles: a cluster each; otherwise as many as fit, each walking the tiles
+  cfg.gridDim = dim3((unsigned)(ctas * (SPLIT ? tiles : std::min<int64_t>(tiles, a.num_sms / G))));
   cfg.blockDim = dim3(kBThreads);
   cfg.dynamicSmemBytes = kBSmemBytes;
   cfg.stream = s;
   cfg.attrs = attr;
-  cfg.numAttrs = G == 2 ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, gemm_block_kernel<G, DGRAD>, p);
+  cfg.numAttrs = ctas > 1 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, gemm_block_kernel<G, DGRAD, SPLIT>, p);
+}
+
+// Clusters of `split` CTAs of the split kernel that the device runs at once (a cluster's CTAs share a
+// GPC, so this is less than SMs / split); cached per device.
+template <bool DGRAD>
+cudaError_t split_clusters(int split, int* clusters) {
+  static std::atomic<int> cache[64][4];
+  int dev = 0;
+  cudaError_t err = cudaGetDevice(&dev);
+  if (err != cudaSuccess) return err;
+  if (dev >= 64) return cudaErrorInvalidDevice;
+  std::atomic<int>& c = cache[dev][split == 8 ? 3 : split == 4 ? 2 : 1];
+  int n = c.load(std::memory_order_acquire);
+  if (n == 0) {
+    err = cudaFuncSetAttribute(gemm_block_kernel<1, DGRAD, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               kBSmemBytes);
+    if (err != cudaSuccess) return err;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)split;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.gridDim = dim3((unsigned)split);
+    cfg.blockDim = dim3(kBThreads);
+    cfg.dynamicSmemBytes = kBSmemBytes;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    err = cudaOccupancyMaxActiveClusters(&n, gemm_block_kernel<1, DGRAD, true>, &cfg);
+    if (err != cudaSuccess) return err;
+    c.store(n > 0 ? n : -1, std::memory_order_release);
+  }
+  *clusters = n;
+  return cudaSuccess;
+}
+
+template <bool DGRAD>
+cudaError_t launch_direction(const GemmBlockArgs& a, cudaStream_t s) {
+  const int red = DGRAD ? a.N : a.K, cols = DGRAD ? a.K : a.N;
+  const int64_t col_tiles = (cols + kBTileCols - 1) / kBTileCols;
+  const int64_t singles = max_row_tiles(a, BlockGeo<1>::kRows) * col_tiles;
+  const int RB = (red + kFp8Block - 1) / kFp8Block;
+  // Tiles that would leave most SMs idle: as many CTAs a tile as run at once, two blocks each at least
+  int split = kBMaxSplit;
+  for (; split > 1; split /= 2) {
+    if (singles * split > a.num_sms || RB < 2 * split) continue;
+    int clusters = 0;
+    const cudaError_t err = split_clusters<DGRAD>(split, &clusters);
+    if (err != cudaSuccess) return err;
+    if (singles <= clusters) break;
+  }
+  if (split > 1) return launch_tiles<1, DGRAD, true>(a, singles, split, s);
+  if (a.M <= kSingleMaxRowsPerGroup * (int64_t)a.E) return launch_tiles<1, DGRAD, false>(a, singles, 1, s);
+  return launch_tiles<2, DGRAD, false>(a, max_row_tiles(a, BlockGeo<2>::kRows) * col_tiles, 1, s);
 }
 
 }  // namespace
 
-// up to this many rows per group on average, tiles on single CTAs (see the header)
-constexpr int64_t kSingleMaxRowsPerGroup = 128;
-
 cudaError_t launch_gemm_block(const GemmBlockArgs& a, cudaStream_t s) {
   if (a.M == 0) return cudaSuccess;
-  if (a.M <= kSingleMaxRowsPerGroup * (int64_t)a.E)
-    return a.dgrad ? launch_tiles<1, true>(a, s) : launch_tiles<1, false>(a, s);
-  return a.dgrad ? launch_tiles<2, true>(a, s) : launch_tiles<2, false>(a, s);
+  if (use_gemv(a)) return launch_gemv_block(a, s);
+  return a.dgrad ? launch_direction<true>(a, s) : launch_direction<false>(a, s);
 }
 
 }  // namespace moe
