@@ -12,8 +12,8 @@
 // on the tie, so the codes are those of the exact quotient at a fifth of an IEEE division's
 // instructions.  For fp32 x a quotient within 2^-20 of a tie may take either neighbour.
 //
-// HBM-bound: 16 lanes form a block of 128 columns, 8 columns each (one 16-byte load of 16-bit x),
-// agree on m with four shuffles, and write 8 codes a lane to each of the row's destinations.
+// HBM-bound: 8 lanes form a block of 128 columns, 16 columns each (two 16-byte loads of 16-bit x),
+// agree on m with three shuffles, and write 16 codes a lane to each of the row's destinations.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -45,12 +45,12 @@ __device__ __forceinline__ float finite_abs(float v) {
   return a <= 3.402823466e38f ? a : 0.0f;  // false for NaN and infinities
 }
 
-// Eight values -> eight E4M3 bytes, element 0 in the lowest byte.  The conversion saturates, so an
+// 16 values -> 16 E4M3 bytes, element 0 in the lowest byte.  The conversion saturates, so an
 // infinity is turned into a NaN first (inf - inf) and NaN stays NaN.
-__device__ __forceinline__ uint2 encode8(const float (&v)[8], float mult) {
-  uint32_t w[4];
+__device__ __forceinline__ uint4 encode16(const float (&v)[16], float mult) {
+  uint32_t w[8];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < 8; ++i) {
     float q[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -60,7 +60,7 @@ __device__ __forceinline__ uint2 encode8(const float (&v)[8], float mult) {
     }
     w[i] = (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(q[0], q[1]), __NV_SATFINITE, __NV_E4M3);
   }
-  return make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
+  return make_uint4(w[0] | (w[1] << 16), w[2] | (w[3] << 16), w[4] | (w[5] << 16), w[6] | (w[7] << 16));
 }
 
 template <int DT>
@@ -70,55 +70,58 @@ __device__ __forceinline__ float load1(const void* p, int64_t i) {
   return static_cast<const float*>(p)[i];
 }
 
-// Columns [c, c + 8) of a row of n columns starting at element `base`; columns past n read as 0.
-// VEC: the row start is 16-byte aligned and n a multiple of 8.
+// Columns [c, c + 16) of a row of n columns starting at element `base`; columns past n read as 0.
+// VEC: the row start is 16-byte aligned and n a multiple of 16.
 template <int DT, bool VEC>
-__device__ __forceinline__ void load8(const void* x, int64_t base, int c, int n, float (&v)[8]) {
+__device__ __forceinline__ void load16(const void* x, int64_t base, int c, int n, float (&v)[16]) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = 0.0f;
+  for (int i = 0; i < 16; ++i) v[i] = 0.0f;
   if (c >= n) return;
-  if (VEC) {
-    if (DT == kDtF32) {
-      const float4* src = reinterpret_cast<const float4*>(static_cast<const float*>(x) + base + c);
-      const float4 a = src[0], b = src[1];
-      v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-    } else {
-      const uint4 r = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(x) + base + c);
-      const uint32_t u[4] = {r.x, r.y, r.z, r.w};
+  if (VEC && DT == kDtF32) {
+    const float4* src = reinterpret_cast<const float4*>(static_cast<const float*>(x) + base + c);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (DT == kDtBf16) {
-          v[2 * i] = __uint_as_float(u[i] << 16);
-          v[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
-        } else {
-          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&u[i]));
-          v[2 * i] = f.x, v[2 * i + 1] = f.y;
-        }
+    for (int i = 0; i < 4; ++i) {
+      const float4 f = src[i];
+      v[4 * i] = f.x, v[4 * i + 1] = f.y, v[4 * i + 2] = f.z, v[4 * i + 3] = f.w;
+    }
+  } else if (VEC) {
+    const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(x) + base + c);
+    const uint4 r0 = src[0], r1 = src[1];
+    const uint32_t u[8] = {r0.x, r0.y, r0.z, r0.w, r1.x, r1.y, r1.z, r1.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (DT == kDtBf16) {
+        v[2 * i] = __uint_as_float(u[i] << 16);
+        v[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
+      } else {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&u[i]));
+        v[2 * i] = f.x, v[2 * i + 1] = f.y;
       }
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
+    for (int i = 0; i < 16; ++i)
       if (c + i < n) v[i] = load1<DT>(x, base + c + i);
   }
 }
 
 template <bool VEC>
-__device__ __forceinline__ void store8(uint8_t* row, int c, int n, uint2 q) {
+__device__ __forceinline__ void store16(uint8_t* row, int c, int n, uint4 q) {
   if (c >= n) return;
   if (VEC) {
-    *reinterpret_cast<uint2*>(row + c) = q;
+    *reinterpret_cast<uint4*>(row + c) = q;
   } else {
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (c + i < n) row[c + i] = (uint8_t)((i < 4 ? q.x : q.y) >> (8 * (i & 3)));
+    for (int i = 0; i < 16; ++i)
+      if (c + i < n) row[c + i] = (uint8_t)(w[i >> 2] >> (8 * (i & 3)));
   }
 }
 
 struct QuantRowsParams {
   QuantBlockArgs a;
-  int groups;  // 8-column groups of a row, padded to whole blocks
-  int lg;      // log2 of the threads a row gets (at least 16)
+  int groups;  // 16-column groups of a row, padded to whole blocks
+  int lg;      // log2 of the threads a row gets (at least 8)
 };
 
 // 1x128 blocks.  A row gets 2^lg threads of a block; thread i owns column groups i, i + 2^lg, ...
@@ -131,9 +134,9 @@ __global__ void __launch_bounds__(kQbThreads) quant_rows_block_kernel(const __gr
   const int g0 = blockIdx.y * (tpr * U) + (threadIdx.x & (tpr - 1));
   const bool on = row < a.rows;
   const int KB = (K + kFp8Block - 1) / kFp8Block;
-  float v[U][8];
+  float v[U][16];
 #pragma unroll
-  for (int u = 0; u < U; ++u) load8<DT, VEC>(a.x, row * a.x_stride, on ? (g0 + u * tpr) * 8 : K, K, v[u]);
+  for (int u = 0; u < U; ++u) load16<DT, VEC>(a.x, row * a.x_stride, on ? (g0 + u * tpr) * 16 : K, K, v[u]);
   int64_t dst[kMaxTopK];
   const int n = a.inv != nullptr ? a.k : 1;
 #pragma unroll
@@ -149,38 +152,38 @@ __global__ void __launch_bounds__(kQbThreads) quant_rows_block_kernel(const __gr
     const int g = g0 + u * tpr;
     float m = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) m = fmaxf(m, finite_abs(v[u][i]));
+    for (int i = 0; i < 16; ++i) m = fmaxf(m, finite_abs(v[u][i]));
 #pragma unroll
-    for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));  // the block's 16 lanes
+    for (int o = 4; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));  // the block's 8 lanes
     const BlockScale sc = block_scale(m);
-    const uint2 q = encode8(v[u], sc.mult);
+    const uint4 q = encode16(v[u], sc.mult);
 #pragma unroll
     for (int j = 0; j < kMaxTopK; ++j) {
       if (dst[j] < 0) continue;
-      store8<VEC>(a.codes + dst[j] * K, g * 8, K, q);
-      if ((g & 15) == 0 && g * 8 < K) a.scales[dst[j] * KB + g / 16] = sc.scale;
+      store16<VEC>(a.codes + dst[j] * K, g * 16, K, q);
+      if ((g & 7) == 0 && g * 16 < K) a.scales[dst[j] * KB + g / 8] = sc.scale;
     }
   }
 }
 
-// 128x128 blocks: one CTA per block, 16 rows at a time, values kept in registers.
+// 128x128 blocks: one CTA per block, 32 rows at a time, values kept in registers.
 template <int DT, bool VEC>
 __global__ void __launch_bounds__(kQbThreads) quant_tiles_kernel(QuantBlockArgs a) {
   __shared__ float part[kQbThreads / 32];
   const int64_t rb = blockIdx.x;
   const int cb = blockIdx.y, KB = gridDim.y;
-  const int c = cb * kFp8Block + (threadIdx.x & 15) * 8;
-  const int64_t r0 = rb * kFp8Block + (threadIdx.x >> 4);
-  float v[8][8], m = 0.0f;
+  const int c = cb * kFp8Block + (threadIdx.x & 7) * 16;
+  const int64_t r0 = rb * kFp8Block + (threadIdx.x >> 3);
+  float v[4][16], m = 0.0f;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int64_t r = r0 + 16 * i;
-    load8<DT, VEC>(a.x, r * a.x_stride, r < a.rows ? c : a.K, a.K, v[i]);
+  for (int i = 0; i < 4; ++i) {
+    const int64_t r = r0 + 32 * i;
+    load16<DT, VEC>(a.x, r * a.x_stride, r < a.rows ? c : a.K, a.K, v[i]);
   }
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
+  for (int i = 0; i < 4; ++i)
 #pragma unroll
-    for (int h = 0; h < 8; ++h) m = fmaxf(m, finite_abs(v[i][h]));
+    for (int h = 0; h < 16; ++h) m = fmaxf(m, finite_abs(v[i][h]));
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
   if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = m;
@@ -190,10 +193,25 @@ __global__ void __launch_bounds__(kQbThreads) quant_tiles_kernel(QuantBlockArgs 
   const BlockScale sc = block_scale(m);
   if (threadIdx.x == 0) a.scales[rb * KB + cb] = sc.scale;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int64_t r = r0 + 16 * i;
-    if (r < a.rows) store8<VEC>(a.codes + r * a.K, c, a.K, encode8(v[i], sc.mult));
+  for (int i = 0; i < 4; ++i) {
+    const int64_t r = r0 + 32 * i;
+    if (r < a.rows) store16<VEC>(a.codes + r * a.K, c, a.K, encode16(v[i], sc.mult));
   }
+}
+
+// Two column groups a thread keep more loads in flight (T = 8192, K = 7168, k = 6: 82.3 against 84.5
+// us, 0.86 of the copy rate); below four blocks of single groups an SM, spreading them over more SMs
+// counts more (T = 64, K = 5120: 3.8 against 3.0 us).
+constexpr int64_t kSpreadGroups = 152 * 4 * kQbThreads;
+
+template <int DT, bool VEC, int U>
+cudaError_t launch_rows_u(const QuantBlockArgs& a, int groups, cudaStream_t s) {
+  QuantRowsParams p{a, groups, 3};
+  while (p.lg < 8 && (U << p.lg) < p.groups) ++p.lg;
+  const int64_t per = kQbThreads >> p.lg;
+  const dim3 grid((unsigned)((a.rows + per - 1) / per), (unsigned)((p.groups + (U << p.lg) - 1) / (U << p.lg)));
+  quant_rows_block_kernel<DT, VEC, U><<<grid, kQbThreads, 0, s>>>(p);
+  return cudaGetLastError();
 }
 
 template <int DT, bool VEC>
@@ -203,13 +221,8 @@ cudaError_t launch_typed(const QuantBlockArgs& a, cudaStream_t s) {
     quant_tiles_kernel<DT, VEC><<<grid, kQbThreads, 0, s>>>(a);
     return cudaGetLastError();
   }
-  constexpr int U = 2;
-  QuantRowsParams p{a, (a.K + kFp8Block - 1) / kFp8Block * (kFp8Block / 8), 4};
-  while (p.lg < 8 && (U << p.lg) < p.groups) ++p.lg;
-  const int64_t per = kQbThreads >> p.lg;
-  const dim3 grid((unsigned)((a.rows + per - 1) / per), (unsigned)((p.groups + (U << p.lg) - 1) / (U << p.lg)));
-  quant_rows_block_kernel<DT, VEC, U><<<grid, kQbThreads, 0, s>>>(p);
-  return cudaGetLastError();
+  const int groups = (a.K + kFp8Block - 1) / kFp8Block * (kFp8Block / 16);
+  return a.rows * groups < kSpreadGroups ? launch_rows_u<DT, VEC, 1>(a, groups, s) : launch_rows_u<DT, VEC, 2>(a, groups, s);
 }
 
 }  // namespace
@@ -217,8 +230,8 @@ cudaError_t launch_typed(const QuantBlockArgs& a, cudaStream_t s) {
 cudaError_t launch_quant_block(const QuantBlockArgs& a, cudaStream_t s) {
   if (a.rows == 0 || (a.inv != nullptr && a.R == 0)) return cudaSuccess;
   const int es = dtype_bytes(a.dtype);
-  const bool vec = reinterpret_cast<uintptr_t>(a.x) % 16 == 0 && (a.x_stride * es) % 16 == 0 && a.K % 8 == 0 &&
-                   reinterpret_cast<uintptr_t>(a.codes) % 8 == 0;
+  const bool vec = reinterpret_cast<uintptr_t>(a.x) % 16 == 0 && (a.x_stride * es) % 16 == 0 && a.K % 16 == 0 &&
+                   reinterpret_cast<uintptr_t>(a.codes) % 16 == 0;
   if (a.dtype == kDtBf16) return vec ? launch_typed<kDtBf16, true>(a, s) : launch_typed<kDtBf16, false>(a, s);
   if (a.dtype == kDtF16) return vec ? launch_typed<kDtF16, true>(a, s) : launch_typed<kDtF16, false>(a, s);
   return vec ? launch_typed<kDtF32, true>(a, s) : launch_typed<kDtF32, false>(a, s);
