@@ -24,6 +24,7 @@ namespace moe {
 namespace {
 
 constexpr int kRowThreads = 256;
+constexpr int64_t kFewTokens = 152;  // a row's threads are then spread wider: latency counts
 
 template <int VB>
 struct Raw;
@@ -140,7 +141,7 @@ __global__ void __launch_bounds__(kRowThreads) unpermute_kernel(const __grid_con
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int c = c0 + u * tpr;
-      if (c < p.chunks) v[u][j].raw = reinterpret_cast<const typename Raw<VB>::T*>(src)[c];
+      if (c < p.chunks) v[u][j].raw = __ldcs(reinterpret_cast<const typename Raw<VB>::T*>(src) + c);
     }
   }
   uint8_t* dst = static_cast<uint8_t*>(a.tokens_out) + t * a.token_stride * p.elem;
@@ -161,17 +162,18 @@ __global__ void __launch_bounds__(kRowThreads) unpermute_kernel(const __grid_con
   }
 }
 
-// The threads of a token walk its row: every chunk of dout is read once, scaled into the k rows of
-// drows and multiplied into the k dot products, which are then summed over the threads (warp
-// shuffles, then shared memory in warp order: the same bits on every call).
-template <int DT, int VB, int LG>
-__global__ void __launch_bounds__(kRowThreads) unpermute_backward_kernel(const __grid_constant__ RowsParams p) {
+// The 2^LG threads of a token walk its row, U chunks at a time: every chunk of dout is read once,
+// scaled into the k rows of drows and multiplied into the k dot products, which are then summed over
+// the threads (warp shuffles, then shared memory in warp order: the same bits on every call).
+template <int DT, int VB, int LG, int U>
+__global__ void __launch_bounds__(LG > 8 ? 1 << LG : kRowThreads)
+    unpermute_backward_kernel(const __grid_constant__ RowsParams p) {
   using C = Chunk<DT, VB>;
   using V = typename Raw<VB>::T;
-  constexpr int kTpr = 1 << LG;
+  constexpr int kTpr = 1 << LG, kThreads = LG > 8 ? kTpr : kRowThreads;
   const RowsArgs& a = p.a;
-  __shared__ float part[kRowThreads / 32][kMaxTopK];
-  const int64_t t = (int64_t)blockIdx.x * (kRowThreads >> LG) + (threadIdx.x >> LG);
+  __shared__ float part[kThreads / 32][kMaxTopK];
+  const int64_t t = (int64_t)blockIdx.x * (kThreads >> LG) + (threadIdx.x >> LG);
   const bool on = t < a.T;
   int r[kMaxTopK];
   float w[kMaxTopK], dot[kMaxTopK];
@@ -184,25 +186,35 @@ __global__ void __launch_bounds__(kRowThreads) unpermute_backward_kernel(const _
       for (int j = 0; j < kMaxTopK; ++j)
         if (j < a.k) w[j] = a.w[t * a.k + j];
     }
-    const uint8_t* src = static_cast<const uint8_t*>(a.tokens_in) + t * a.token_stride * p.elem;
-    for (int c = threadIdx.x & (kTpr - 1); c < p.chunks; c += kTpr) {
-      C d, v[kMaxTopK];
-      d.raw = reinterpret_cast<const V*>(src)[c];
+    const V* src = reinterpret_cast<const V*>(static_cast<const uint8_t*>(a.tokens_in) + t * a.token_stride * p.elem);
+    for (int c0 = threadIdx.x & (kTpr - 1); c0 < p.chunks; c0 += kTpr * U) {
+      C d[U], v[U][kMaxTopK];
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        d[u].raw = U == 1 || c0 + u * kTpr < p.chunks ? src[c0 + u * kTpr] : V{};
       if (a.dw != nullptr) {
 #pragma unroll
-        for (int j = 0; j < kMaxTopK; ++j)
-          if (r[j] >= 0)
-            v[j].raw = reinterpret_cast<const V*>(static_cast<const uint8_t*>(a.rows_in) +
-                                                  (int64_t)r[j] * a.rows_in_stride * p.elem)[c];
+        for (int j = 0; j < kMaxTopK; ++j) {
+          if (r[j] < 0) continue;
+          const V* row = reinterpret_cast<const V*>(static_cast<const uint8_t*>(a.rows_in) +
+                                                    (int64_t)r[j] * a.rows_in_stride * p.elem);
+#pragma unroll
+          for (int u = 0; u < U; ++u)
+            v[u][j].raw = U == 1 || c0 + u * kTpr < p.chunks ? row[c0 + u * kTpr] : V{};
+        }
       }
       if (a.rows_out != nullptr) {
 #pragma unroll
         for (int j = 0; j < kMaxTopK; ++j) {
           if (r[j] < 0) continue;
-          C o;
+          V* row = reinterpret_cast<V*>(static_cast<uint8_t*>(a.rows_out) + (int64_t)r[j] * a.rows_out_stride * p.elem);
 #pragma unroll
-          for (int i = 0; i < C::kN; ++i) o.e[i] = Elem<DT>::from(w[j] * Elem<DT>::to(d.e[i]));
-          reinterpret_cast<V*>(static_cast<uint8_t*>(a.rows_out) + (int64_t)r[j] * a.rows_out_stride * p.elem)[c] = o.raw;
+          for (int u = 0; u < U; ++u) {
+            C o;
+#pragma unroll
+            for (int i = 0; i < C::kN; ++i) o.e[i] = Elem<DT>::from(w[j] * Elem<DT>::to(d[u].e[i]));
+            if (U == 1 || c0 + u * kTpr < p.chunks) row[c0 + u * kTpr] = o.raw;
+          }
         }
       }
       if (a.dw != nullptr) {
@@ -210,7 +222,9 @@ __global__ void __launch_bounds__(kRowThreads) unpermute_backward_kernel(const _
         for (int j = 0; j < kMaxTopK; ++j) {
           if (r[j] < 0) continue;
 #pragma unroll
-          for (int i = 0; i < C::kN; ++i) dot[j] = fmaf(Elem<DT>::to(d.e[i]), Elem<DT>::to(v[j].e[i]), dot[j]);
+          for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int i = 0; i < C::kN; ++i) dot[j] = fmaf(Elem<DT>::to(d[u].e[i]), Elem<DT>::to(v[u][j].e[i]), dot[j]);
         }
       }
     }
@@ -238,7 +252,7 @@ __global__ void __launch_bounds__(kRowThreads) unpermute_backward_kernel(const _
   if (on && threadIdx.x < a.k) {
     float sum = 0.0f;
 #pragma unroll
-    for (int i = 0; i < kRowThreads / 32; ++i) sum += part[i][threadIdx.x];
+    for (int i = 0; i < kThreads / 32; ++i) sum += part[i][threadIdx.x];
     a.dw[t * a.k + threadIdx.x] = sum;
   }
 }
@@ -326,12 +340,15 @@ cudaError_t unpermute_vb(const RowsArgs& a, cudaStream_t s) {
 
 template <int DT, int VB>
 cudaError_t backward_vb(const RowsArgs& a, cudaStream_t s) {
+  constexpr int U = VB >= 8 ? 1 : 4;
   RowsParams p{a, a.H * dtype_bytes(a.dtype) / VB, 0, dtype_bytes(a.dtype)};
-  if (p.chunks <= 64) {  // short rows: a warp each
+  if (p.chunks <= 64 * U) {  // short rows: a warp each
     const unsigned blocks = (unsigned)((a.T + kRowThreads / 32 - 1) / (kRowThreads / 32));
-    unpermute_backward_kernel<DT, VB, 5><<<blocks, kRowThreads, 0, s>>>(p);
+    unpermute_backward_kernel<DT, VB, 5, U><<<blocks, kRowThreads, 0, s>>>(p);
+  } else if (p.chunks > 256 * U && a.T <= kFewTokens) {  // few long rows: a block of 1024 threads each
+    unpermute_backward_kernel<DT, VB, 10, U><<<(unsigned)a.T, 1024, 0, s>>>(p);
   } else {
-    unpermute_backward_kernel<DT, VB, 8><<<(unsigned)a.T, kRowThreads, 0, s>>>(p);
+    unpermute_backward_kernel<DT, VB, 8, U><<<(unsigned)a.T, kRowThreads, 0, s>>>(p);
   }
   return cudaGetLastError();
 }
