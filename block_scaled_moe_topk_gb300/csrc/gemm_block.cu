@@ -51,14 +51,14 @@ constexpr int kBRingBytes = 6 * 2 * kBHalfBytes;    // 192 KiB: 6 stages of a pa
 constexpr int kBMaxStages = 6;
 constexpr int kBMaxSplit = 8;
 constexpr int kBOutOff = kBRingBytes;   // per-warp staging of unaligned output rows
-constexpr int kBOutBytes = 32 * 32;                 // 32 rows x 32 bytes
+constexpr int kBOutBytes = 32 * 64;                 // 32 rows x 64 bytes
 constexpr int kBScaleBlocks = 8;                    // reduction blocks of one scale chunk
 constexpr int kBScaleRows = 130;                    // 128 rows of x, then the weights' two column halves
 constexpr int kBScaleOff = kBOutOff + kBEpiWarps * kBOutBytes;  // two chunks [block][row], fp32
 constexpr int kBScaleBytes = kBScaleBlocks * kBScaleRows * 4;
 constexpr int kBBarOff = kBScaleOff + 2 * kBScaleBytes;
-constexpr int kBTabOff = kBBarOff + 256;            // per expert: first row, rows, first tile
-constexpr int kBSmemBytes = kBTabOff + 3 * 4 * (kMaxExperts + 1) + 1024;
+constexpr int kBTabOff = kBBarOff + 256;            // per expert: first row, first tile
+constexpr int kBSmemBytes = kBTabOff + 2 * 4 * (kMaxExperts + 1) + 1024;
 static_assert(kBSmemBytes <= 232448, "block GEMM shared memory");
 static_assert(kBBarOff % 8 == 0 && 8 * (2 * kBMaxStages + 9) + 8 <= 256, "block GEMM barriers");
 
@@ -70,9 +70,6 @@ struct BlockGeo {
   static constexpr int kStageBytes = (1 + 2 / G) * kBHalfBytes;
   static constexpr int kStages = kBRingBytes / kStageBytes;
 };
-
-// Up to this many rows per group on average, tiles run on single CTAs.
-constexpr int64_t kSingleMaxRowsPerGroup = 128;
 
 struct BlockParams {  // 64-byte aligned through its CUtensorMap members
   CUtensorMap tmap_x;  // codes [M, reduction], box 128 B x 128 rows
@@ -191,8 +188,8 @@ __global__ void __launch_bounds__(kBThreads, 1) gemm_block_kernel(const __grid_c
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + kBBarOff + 8 * (2 * kStages + 9));
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
   int32_t* row_begin = reinterpret_cast<int32_t*>(smem + kBTabOff);
-  int32_t* row_count = row_begin + kMaxExperts + 1;
-  int32_t* tile_base = row_count + kMaxExperts + 1;
+  int32_t* tile_base = row_begin + kMaxExperts + 1;
+  auto group_size = [&](int e) { return max(row_begin[e + 1] - row_begin[e], 0); };
 
   const GemmBlockArgs& a = p.a;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -201,11 +198,7 @@ __global__ void __launch_bounds__(kBThreads, 1) gemm_block_kernel(const __grid_c
   const int E = a.E;
 
   if (blockIdx.x == 0 && threadIdx.x < 8) a.status[threadIdx.x] = 0;
-  for (int e = threadIdx.x; e < E; e += kBThreads) {
-    const RowSpan sp = group_rows(a.offsets, e, a.M);
-    row_begin[e] = (int32_t)sp.begin;
-    row_count[e] = (int32_t)sp.rows;
-  }
+  for (int e = threadIdx.x; e <= E; e += kBThreads) row_begin[e] = (int32_t)group_start(a.offsets, e, a.M);
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
       mbar_init(full_bar(s), 1);   // expect_tx arrival of the even (or only) CTA's producer
@@ -228,7 +221,7 @@ __global__ void __launch_bounds__(kBThreads, 1) gemm_block_kernel(const __grid_c
     int running = 0;
     for (int e0 = 0; e0 < E; e0 += 32) {
       const int e = e0 + lane;
-      const int v = e < E ? (row_count[e] + kRows - 1) / kRows : 0;
+      const int v = e < E ? (group_size(e) + kRows - 1) / kRows : 0;
       int incl = v;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -278,7 +271,7 @@ __global__ void __launch_bounds__(kBThreads, 1) gemm_block_kernel(const __grid_c
       bool ok = !a.test_stall;  // the test hook leaves every stage unfilled
       for (int64_t tile = first_tile; ok && tile < total_tiles; tile += tile_step) {
         const BlockTile bt = block_tile(tile, tile_base, E, NT);
-        const int rows_left = row_count[bt.e] - bt.mt * kRows;
+        const int rows_left = group_size(bt.e) - bt.mt * kRows;
         const bool peer_real = G == 2 && rows_left > 128;  // the odd CTA has rows in this tile
         const bool real = leader || peer_real;
         const int row0 = row_begin[bt.e] + bt.mt * kRows + (int)rank * 128;
@@ -376,7 +369,7 @@ __global__ void __launch_bounds__(kBThreads, 1) gemm_block_kernel(const __grid_c
       for (int64_t tile = first_tile; ok && tile < total_tiles; tile += tile_step) {
         const BlockTile bt = block_tile(tile, tile_base, E, NT);
         const int row_local = bt.mt * kRows + (int)rank * 128;
-        const int rows_here = min(128, row_count[bt.e] - row_local);
+        const int rows_here = min(128, group_size(bt.e) - row_local);
         const float* sx = a.x_scale + ((int64_t)row_begin[bt.e] + row_local) * RB;
         // the scale block of column half (lane >> 3): past the last column, the last one (unused)
         const int cb = min(bt.nt * 2 + ((lane >> 3) & 1), (DGRAD ? KB : NB) - 1);
@@ -417,7 +410,7 @@ __global__ void __launch_bounds__(kBThreads, 1) gemm_block_kernel(const __grid_c
     for (int64_t tile = first_tile; ok && tile < total_tiles; tile += tile_step) {
       const BlockTile bt = block_tile(tile, tile_base, E, NT);
       const int row_local = bt.mt * kRows + (int)rank * 128 + quad * 32 + lane;
-      const bool valid = row_local < row_count[bt.e];
+      const bool valid = row_local < group_size(bt.e);
       const int col0 = bt.nt * kBTileCols + half * 128;
       const bool any = __any_sync(0xffffffffu, valid) && col0 < cols;
       const int64_t row = (int64_t)row_begin[bt.e] + row_local;
@@ -500,44 +493,44 @@ __global__ void __launch_bounds__(kBThreads, 1) gemm_block_kernel(const __grid_c
           }
         }
       } else {
-        // Any alignment and the last columns: 32 bytes of every row at a time through the warp's
-        // staging buffer (words swizzled: conflict-free both ways), then consecutive elements of a
-        // row by consecutive lanes
+        // Any alignment and the last columns: 64 bytes of every row at a time through the warp's
+        // staging buffer (words swizzled by the row: conflict-free both ways), then consecutive
+        // elements of a row by consecutive lanes
         uint32_t* stage = reinterpret_cast<uint32_t*>(smem + kBOutOff + (warp - kBFirstEpiWarp) * kBOutBytes);
-        const int rows_here = min(32, row_count[bt.e] - (row_local - lane));
+        const int rows_here = min(32, group_size(bt.e) - (row_local - lane));
         const int64_t row0 = row - lane;
+        const int swz = (lane >> 1) & 15;
         if (dt == kDtF32) {
-#pragma unroll
-          for (int c = 0; c < 128; c += 8) {
-            if (col0 + c >= cols) break;
-            __syncwarp();
-#pragma unroll
-            for (int i = 0; i < 8; ++i) stage[lane * 8 + (i ^ (lane >> 2))] = __float_as_uint(acc[c + i]);
-            __syncwarp();
-            const int col = col0 + c + (lane & 7);
-            for (int r4 = 0; r4 < 8; ++r4) {
-              const int r = 4 * r4 + (lane >> 3);
-              if (r < rows_here && col < cols)
-                static_cast<uint32_t*>(a.out)[(row0 + r) * cols + col] = stage[r * 8 + ((lane & 7) ^ r4)];
-            }
-          }
-        } else {
 #pragma unroll
           for (int c = 0; c < 128; c += 16) {
             if (col0 + c >= cols) break;
             __syncwarp();
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-              stage[lane * 8 + (i ^ (lane >> 2))] = out_pair(acc[c + 2 * i], acc[c + 2 * i + 1], dt);
+            for (int i = 0; i < 16; ++i) stage[lane * 16 + (i ^ swz)] = __float_as_uint(acc[c + i]);
             __syncwarp();
-            const int col = col0 + c + (lane & 15);
-            for (int r2 = 0; r2 < 16; ++r2) {
-              const int r = 2 * r2 + (lane >> 4);
+            const int col = col0 + c + (lane & 15), r0 = lane >> 4;
+            uint32_t* dst = static_cast<uint32_t*>(a.out) + (row0 + r0) * cols + col;
+#pragma unroll 8
+            for (int i = 0; i < 16; ++i, dst += 2 * cols)
+              if (2 * i + r0 < rows_here && col < cols) *dst = stage[(2 * i + r0) * 16 + ((lane & 15) ^ i)];
+          }
+        } else {
+#pragma unroll
+          for (int c = 0; c < 128; c += 32) {
+            if (col0 + c >= cols) break;
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              stage[lane * 16 + (i ^ swz)] = out_pair(acc[c + 2 * i], acc[c + 2 * i + 1], dt);
+            __syncwarp();
+            const int col = col0 + c + lane;
+            uint16_t* dst = static_cast<uint16_t*>(a.out) + row0 * cols + col;
+#pragma unroll 8
+            for (int r = 0; r < 32; ++r, dst += cols)
               if (r < rows_here && col < cols) {
-                const uint32_t w = stage[r * 8 + (((lane & 15) >> 1) ^ (r >> 2))];
-                static_cast<uint16_t*>(a.out)[(row0 + r) * cols + col] = (uint16_t)(lane & 1 ? w >> 16 : w);
+                const uint32_t w = stage[r * 16 + ((lane >> 1) ^ (r >> 1))];
+                *dst = (uint16_t)(lane & 1 ? w >> 16 : w);
               }
-            }
           }
         }
       }
@@ -548,26 +541,52 @@ __global__ void __launch_bounds__(kBThreads, 1) gemm_block_kernel(const __grid_c
   if (kCluster) cluster_sync();  // both CTAs done with the pair's TMEM; every part's sums are in place
   else __syncthreads();
   if (SPLIT && first_tile < total_tiles) {
-    // CTA i sums columns [256 i / S, 256 (i + 1) / S) of the tile over the parts, in part order
+    // CTA i sums columns [256 i / S, 256 (i + 1) / S) of the tile over the parts, its own first (so that
+    // the CTAs do not all read one part at a time; a column's order of sums is always the same)
     const BlockTile bt = block_tile(first_tile, tile_base, E, NT);
-    const int rows_here = min(kRows, row_count[bt.e] - bt.mt * kRows);
+    const int rows_here = min(kRows, group_size(bt.e) - bt.mt * kRows);
     const int width = kBTileCols / (int)parts, c0 = (int)part * width;
     const int64_t row0 = (int64_t)row_begin[bt.e] + bt.mt * kRows;
     uint32_t src[kBMaxSplit];
 #pragma unroll
-    for (int q = 0; q < kBMaxSplit; ++q) src[q] = mapa_shared(sbase, (uint32_t)q < parts ? q : 0);
-    for (int i = threadIdx.x; i < rows_here * width; i += kBThreads) {
-      const int r = i / width, c = c0 + i % width, col = bt.nt * kBTileCols + c;
-      if (col >= cols) continue;
-      const uint32_t at = (uint32_t)(r * kBTileCols + ((((c >> 2) ^ (r & 7)) << 2) | (c & 3))) * 4u;
-      float v[kBMaxSplit], sum = 0.0f;
+    for (int q = 0; q < kBMaxSplit; ++q) src[q] = mapa_shared(sbase, (part + (uint32_t)q) & (parts - 1));
+    const int lgq = 29 - __clz(width);  // log2 of the 4-column groups of a row
+    const int n = rows_here << lgq;
+    for (int i0 = threadIdx.x; i0 < n; i0 += 2 * kBThreads) {
+      float4 v[2][kBMaxSplit];
 #pragma unroll
-      for (int q = 0; q < kBMaxSplit; ++q) v[q] = (uint32_t)q < parts ? __uint_as_float(ld_shared_cluster_u32(src[q] + at)) : 0.0f;
+      for (int u = 0; u < 2; ++u) {
+        const int i = i0 + u * kBThreads, r = i >> lgq, q4 = (c0 >> 2) + (i & ((1 << lgq) - 1));
+        const uint32_t at = (uint32_t)(r * kBTileCols + ((q4 ^ (r & 7)) << 2)) * 4u;
 #pragma unroll
-      for (int q = 0; q < kBMaxSplit; ++q) sum += v[q];
-      const int64_t o = (row0 + r) * cols + col;
-      if (a.out_dtype == kDtF32) static_cast<float*>(a.out)[o] = sum;
-      else static_cast<uint16_t*>(a.out)[o] = (uint16_t)out_pair(sum, 0.0f, a.out_dtype);
+        for (int q = 0; q < kBMaxSplit; ++q)
+          if ((uint32_t)q < parts && i < n) v[u][q] = ld_shared_cluster_v4(src[q] + at);
+      }
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int i = i0 + u * kBThreads, r = i >> lgq, q4 = (c0 >> 2) + (i & ((1 << lgq) - 1));
+        if (i >= n) break;
+        float sum[4] = {};
+#pragma unroll
+        for (int q = 0; q < kBMaxSplit; ++q)
+          if ((uint32_t)q < parts) sum[0] += v[u][q].x, sum[1] += v[u][q].y, sum[2] += v[u][q].z, sum[3] += v[u][q].w;
+        const int col = bt.nt * kBTileCols + 4 * q4;
+        const int64_t o = (row0 + r) * cols + col;
+        if (p.out_vec && col + 4 <= cols) {
+          if (a.out_dtype == kDtF32)
+            *reinterpret_cast<float4*>(static_cast<float*>(a.out) + o) = make_float4(sum[0], sum[1], sum[2], sum[3]);
+          else
+            *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + o) =
+                make_uint2(out_pair(sum[0], sum[1], a.out_dtype), out_pair(sum[2], sum[3], a.out_dtype));
+          continue;
+        }
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {
+          if (col + h >= cols) break;
+          if (a.out_dtype == kDtF32) static_cast<float*>(a.out)[o + h] = sum[h];
+          else static_cast<uint16_t*>(a.out)[o + h] = (uint16_t)out_pair(sum[h], 0.0f, a.out_dtype);
+        }
+      }
     }
   }
   // After an abort, loads that were issued but never waited for may still be landing in this CTA's
@@ -679,23 +698,42 @@ cudaError_t split_clusters(int split, int* clusters) {
   return cudaSuccess;
 }
 
+// How a product's tiles run; device times of both sides, N = 6144, K = 7168 unless stated.
+//
+// Split reduction (SPLIT), when the tiles leave SMs idle: a tile costs about 0.44 us a block of the
+// reduction; S CTAs on it save (S - 1) / S of that and cost 2.7 us (cluster barriers, the partial
+// sums' way through shared memory) and 0.04 us a row of the tile.  One expert, N = 2304, K = 5120, S = 8
+// against 1: 8 rows 10.1 against 22.7 us, 64 rows 11.6 against 23.7, 128 rows 14.2 against 24.7; K = 512:
+// 8 rows 8.3 against 6.6, 128 rows 13.4 against 8.2 (not split).
+//
+// Single CTAs or pairs: a group's last tile wastes half a tile on average, 64 rows against 128, but a
+// single CTA reads 48 KiB of operands a stage where a pair's CTA reads 32.
+//   at most 128 rows a group  the weight stream bounds both and singles hold more of it in flight: 48
+//                             experts x 64 rows 343 against 440 us, x 128 469 against 469
+//   129 to 224                one pair tile against two singles: x 192 rows 484 against 519 us
+//   225 to 736                a second pair tile is often nearly empty: x 256 692 against 586 us, x 512
+//                             1070 against 1057
+//   more                      x 1024 1950 against 1960 us; one expert x 8192 309 against 331 us
 template <bool DGRAD>
 cudaError_t launch_direction(const GemmBlockArgs& a, cudaStream_t s) {
   const int red = DGRAD ? a.N : a.K, cols = DGRAD ? a.K : a.N;
   const int64_t col_tiles = (cols + kBTileCols - 1) / kBTileCols;
   const int64_t singles = max_row_tiles(a, BlockGeo<1>::kRows) * col_tiles;
   const int RB = (red + kFp8Block - 1) / kFp8Block;
-  // Tiles that would leave most SMs idle: as many CTAs a tile as run at once, two blocks each at least
+  // Rows of an average group's first row tile
+  const int64_t groups = std::min<int64_t>(a.E, a.M), avg = (a.M + groups - 1) / groups;
+  const int rows = (int)std::min<int64_t>(avg, BlockGeo<1>::kRows);
   int split = kBMaxSplit;
   for (; split > 1; split /= 2) {
-    if (singles * split > a.num_sms || RB < 2 * split) continue;
+    if (singles * split > a.num_sms || 44 * RB * (split - 1) <= split * (270 + 4 * rows)) continue;
     int clusters = 0;
     const cudaError_t err = split_clusters<DGRAD>(split, &clusters);
     if (err != cudaSuccess) return err;
     if (singles <= clusters) break;
   }
   if (split > 1) return launch_tiles<1, DGRAD, true>(a, singles, split, s);
-  if (a.M <= kSingleMaxRowsPerGroup * (int64_t)a.E) return launch_tiles<1, DGRAD, false>(a, singles, 1, s);
+  const bool single = singles <= a.num_sms || avg <= 128 || (groups > 1 && avg > 224 && avg <= 736);
+  if (single) return launch_tiles<1, DGRAD, false>(a, singles, 1, s);
   return launch_tiles<2, DGRAD, false>(a, max_row_tiles(a, BlockGeo<2>::kRows) * col_tiles, 1, s);
 }
 

@@ -19,16 +19,12 @@ __device__ __forceinline__ uint32_t out_pair(float lo, float hi, int dtype) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// Rows [begin, begin + rows) of group e, inside [0, M) whatever the offsets hold.
-struct RowSpan {
-  int64_t begin, rows;
-};
-__device__ __forceinline__ RowSpan group_rows(const int64_t* offsets, int e, int64_t M) {
-  if (offsets == nullptr) return {0, M};
-  const int64_t a = offsets[e], b = offsets[e + 1];
-  const int64_t begin = a < 0 ? 0 : (a > M ? M : a);
-  const int64_t end = b < begin ? begin : (b > M ? M : b);
-  return {begin, end - begin};
+// First row of group e (e = E: the end of the last), inside [0, M] whatever the offsets hold.
+// Group e has the rows from group_start(e) up to group_start(e + 1), none if that is less.
+__device__ __forceinline__ int64_t group_start(const int64_t* offsets, int e, int64_t M) {
+  if (offsets == nullptr) return e == 0 ? 0 : M;
+  const int64_t v = offsets[e];
+  return v < 0 ? 0 : (v > M ? M : v);
 }
 
 }  // namespace

@@ -49,10 +49,8 @@ __global__ void __launch_bounds__(kGvThreads) gemv_block_kernel(GemmBlockArgs a)
     __shared__ int group;
     if (threadIdx.x == 0) group = -1;
     __syncthreads();
-    for (int i = threadIdx.x; i < a.E; i += kGvThreads) {
-      const RowSpan sp = group_rows(a.offsets, i, a.M);
-      if (r0 >= sp.begin && r0 < sp.begin + sp.rows) group = i;
-    }
+    for (int i = threadIdx.x; i < a.E; i += kGvThreads)
+      if (r0 >= group_start(a.offsets, i, a.M) && r0 < group_start(a.offsets, i + 1, a.M)) group = i;
     __syncthreads();
     e = group;
   }

@@ -218,6 +218,14 @@ __device__ __forceinline__ uint32_t ld_shared_cluster_u32(uint32_t caddr) {
   asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(caddr) : "memory");
   return v;
 }
+__device__ __forceinline__ float4 ld_shared_cluster_v4(uint32_t caddr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(caddr)
+               : "memory");
+  return v;
+}
 // Arrive on an mbarrier given by its shared::cluster address (this CTA's or the peer's),
 // without ordering this thread's earlier memory accesses (relaxed): for hand-offs whose data
 // needs no such ordering (e.g. TMEM already read into registers).
