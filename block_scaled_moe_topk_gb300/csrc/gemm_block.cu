@@ -509,10 +509,17 @@ __global__ void __launch_bounds__(kBThreads, 1) gemm_block_kernel(const __grid_c
             for (int i = 0; i < 16; ++i) stage[lane * 16 + (i ^ swz)] = __float_as_uint(acc[c + i]);
             __syncwarp();
             const int col = col0 + c + (lane & 15), r0 = lane >> 4;
+            const int nr = col < cols ? rows_here - r0 : 0;
             uint32_t* dst = static_cast<uint32_t*>(a.out) + (row0 + r0) * cols + col;
-#pragma unroll 8
-            for (int i = 0; i < 16; ++i, dst += 2 * cols)
-              if (2 * i + r0 < rows_here && col < cols) *dst = stage[(2 * i + r0) * 16 + ((lane & 15) ^ i)];
+#pragma unroll 1
+            for (int i0 = 0; i0 < 16; i0 += 8) {
+              uint32_t w[8];
+#pragma unroll
+              for (int i = 0; i < 8; ++i) w[i] = stage[(2 * (i0 + i) + r0) * 16 + ((lane & 15) ^ (i0 + i))];
+#pragma unroll
+              for (int i = 0; i < 8; ++i, dst += 2 * cols)
+                if (2 * (i0 + i) < nr) *dst = w[i];
+            }
           }
         } else {
 #pragma unroll
@@ -524,13 +531,17 @@ __global__ void __launch_bounds__(kBThreads, 1) gemm_block_kernel(const __grid_c
               stage[lane * 16 + (i ^ swz)] = out_pair(acc[c + 2 * i], acc[c + 2 * i + 1], dt);
             __syncwarp();
             const int col = col0 + c + lane;
+            const int nr = col < cols ? rows_here : 0;
             uint16_t* dst = static_cast<uint16_t*>(a.out) + row0 * cols + col;
-#pragma unroll 8
-            for (int r = 0; r < 32; ++r, dst += cols)
-              if (r < rows_here && col < cols) {
-                const uint32_t w = stage[r * 16 + ((lane >> 1) ^ (r >> 1))];
-                *dst = (uint16_t)(lane & 1 ? w >> 16 : w);
-              }
+#pragma unroll 1
+            for (int r0 = 0; r0 < 32; r0 += 8) {  // eight reads, then eight stores
+              uint32_t w[8];
+#pragma unroll
+              for (int i = 0; i < 8; ++i) w[i] = stage[(r0 + i) * 16 + ((lane >> 1) ^ ((r0 + i) >> 1))];
+#pragma unroll
+              for (int i = 0; i < 8; ++i, dst += cols)
+                if (r0 + i < nr) *dst = (uint16_t)(lane & 1 ? w[i] >> 16 : w[i]);
+            }
           }
         }
       }
