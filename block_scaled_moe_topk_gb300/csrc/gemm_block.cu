@@ -73,6 +73,7 @@ struct BlockGeo {
 
 struct BlockParams {  // 64-byte aligned through its CUtensorMap members
   CUtensorMap tmap_x;  // codes [M, reduction], box 128 B x 128 rows
+  CUtensorMap tmap_x32;  // the same, 32 rows
   CUtensorMap tmap_w;  // codes [E, N, K], box 128 B x 128 rows x 1
   GemmBlockArgs a;
   int out_vec;         // output rows start on 32-byte boundaries
@@ -170,6 +171,26 @@ __device__ __forceinline__ BlockTile block_tile(int64_t tile, const int32_t* bas
   return {lo, (int)(local % (uint32_t)mt_e), (int)(local / (uint32_t)mt_e)};
 }
 
+// 128 rows of x, of which the first `rows` are the tile's: whole 32-row boxes past them are read past
+// the last row of x instead, where TMA writes zeros without reading memory.  The MMA then multiplies
+// zeros there, not the next group's rows: less to fetch, and less power, which bounds long products.
+template <int G>
+__device__ __forceinline__ void load_rows_x(const BlockParams& p, uint32_t dst, uint32_t bar, int c, int row0, int rows) {
+  const int past = (int)p.a.M;
+  if (rows >= 128 || rows <= 0) {
+    const int r = rows > 0 ? row0 : past;
+    if (G == 2) tma_load_2d_pair(dst, &p.tmap_x, bar, c, r);
+    else tma_load_2d(dst, &p.tmap_x, bar, c, r);
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = 32 * i < rows ? row0 + 32 * i : past;
+    if (G == 2) tma_load_2d_pair(dst + i * 4096, &p.tmap_x32, bar, c, r);
+    else tma_load_2d(dst + i * 4096, &p.tmap_x32, bar, c, r);
+  }
+}
+
 template <int G, bool DGRAD, bool SPLIT>
 __global__ void __launch_bounds__(kBThreads, 1) gemm_block_kernel(const __grid_constant__ BlockParams p) {
   static_assert(G == 1 || !SPLIT, "split tiles run on single CTAs");
@@ -214,6 +235,7 @@ __global__ void __launch_bounds__(kBThreads, 1) gemm_block_kernel(const __grid_c
     *abort_flag = 0;
     fence_mbar_init();
     prefetch_tensormap(&p.tmap_x);
+    prefetch_tensormap(&p.tmap_x32);
     prefetch_tensormap(&p.tmap_w);
   }
   __syncthreads();
@@ -272,11 +294,10 @@ __global__ void __launch_bounds__(kBThreads, 1) gemm_block_kernel(const __grid_c
       for (int64_t tile = first_tile; ok && tile < total_tiles; tile += tile_step) {
         const BlockTile bt = block_tile(tile, tile_base, E, NT);
         const int rows_left = group_size(bt.e) - bt.mt * kRows;
-        const bool peer_real = G == 2 && rows_left > 128;  // the odd CTA has rows in this tile
-        const bool real = leader || peer_real;
+        const int rows_mine = rows_left - (int)rank * 128;
         const int row0 = row_begin[bt.e] + bt.mt * kRows + (int)rank * 128;
         const int col0 = bt.nt * kBTileCols + (int)rank * 128;
-        const uint32_t tx = (uint32_t)kBHalfBytes * (peer_real ? 4u : 3u);  // of every CTA of the tile
+        const uint32_t tx = (uint32_t)kBHalfBytes * (G == 2 ? 4u : 3u);  // of every CTA of the tile
         for (int b = b_lo; b < b_hi; ++b) {
           if (!warp_wait(empty_bar(slot), phase ^ 1u, sync, a.timeout_ns)) {
             ok = false;
@@ -288,7 +309,6 @@ __global__ void __launch_bounds__(kBThreads, 1) gemm_block_kernel(const __grid_c
             if (G == 2) {
               if (DGRAD) tma_load_3d_pair(st + kBHalfBytes, &p.tmap_w, lfull, col0, b * kFp8Block, bt.e);
               else tma_load_3d_pair(st + kBHalfBytes, &p.tmap_w, lfull, b * kFp8Block, col0, bt.e);
-              if (real) tma_load_2d_pair(st, &p.tmap_x, lfull, b * kFp8Block, row0);
             } else {
 #pragma unroll
               for (int h = 1; h <= 2; ++h) {
@@ -296,8 +316,8 @@ __global__ void __launch_bounds__(kBThreads, 1) gemm_block_kernel(const __grid_c
                 if (DGRAD) tma_load_3d(st + h * kBHalfBytes, &p.tmap_w, lfull, c, b * kFp8Block, bt.e);
                 else tma_load_3d(st + h * kBHalfBytes, &p.tmap_w, lfull, b * kFp8Block, c, bt.e);
               }
-              tma_load_2d(st, &p.tmap_x, lfull, b * kFp8Block, row0);
             }
+            load_rows_x<G>(p, st, lfull, b * kFp8Block, row0, rows_mine);
           }
           __syncwarp();
           if (++slot == kStages) {
@@ -618,10 +638,11 @@ __global__ void __launch_bounds__(kBThreads, 1) gemm_block_kernel(const __grid_c
 }
 
 // ---------------------------------------------------------------------- host side
-bool encode_codes(CUtensorMap* m, const uint8_t* base, int rank, const cuuint64_t* dims, const cuuint64_t* strides) {
+bool encode_codes(CUtensorMap* m, const uint8_t* base, int rank, const cuuint64_t* dims, const cuuint64_t* strides,
+                  cuuint32_t rows) {
   EncodeTiledFn encode = get_encode_fn();
   if (!encode) return false;
-  const cuuint32_t box[3] = {128, 128, 1};
+  const cuuint32_t box[3] = {128, rows, 1};
   const cuuint32_t es[3] = {1, 1, 1};
   return encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, (cuuint32_t)rank, const_cast<uint8_t*>(base), dims, strides, box, es,
                 CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -652,7 +673,8 @@ cudaError_t launch_tiles(const GemmBlockArgs& a, int64_t tiles, int split, cudaS
   const cuuint64_t xd[2] = {red, (cuuint64_t)a.M}, xst[1] = {red};
   const cuuint64_t wd[3] = {(cuuint64_t)a.K, (cuuint64_t)a.N, (cuuint64_t)a.E};
   const cuuint64_t wst[2] = {(cuuint64_t)a.K, (cuuint64_t)a.K * (cuuint64_t)a.N};
-  if (!encode_codes(&p.tmap_x, a.x, 2, xd, xst) || !encode_codes(&p.tmap_w, a.w, 3, wd, wst))
+  if (!encode_codes(&p.tmap_x, a.x, 2, xd, xst, 128) || !encode_codes(&p.tmap_x32, a.x, 2, xd, xst, 32) ||
+      !encode_codes(&p.tmap_w, a.w, 3, wd, wst, 128))
     return cudaErrorInvalidValue;
   p.a = a;
   const int64_t cols = DGRAD ? a.K : a.N;
