@@ -21,11 +21,22 @@
 //   warps 2, 3 scales: chunks of 8 blocks' scales of the tile's rows into shared memory, eight lanes
 //              a row.  A thread of the summing warps loading its own row's scale instead touches 32
 //              lines an instruction, in competition with the operands for the shared-memory pipe
-//              (the 49152-row product below: 2.51 ms against XXXX)
+//              (49152 rows over 48 experts, N = 6144, K = 7168: 2.51 against 2.16 ms)
 //   warps 4-11 sums: a thread owns one row and 128 of the 256 columns (one scale block) in 128 fp32
 //              registers; warps whose 32 rows are past the group's end read nothing.  The two
-//              warpgroups take 224 registers a thread, the first warpgroup keeps 56 (setmaxnreg;
-//              128 x 56 + 256 x 224 = 384 x 168, what the block is launched with)
+//              warpgroups take 216 (200) registers a thread of the control warps' (setmaxnreg)
+// Groups of few rows run the same kernel on single CTAs (G = 1: 128 x 256 tiles, 48 KiB stages), and
+// tiles too few for the SMs share their reduction over a cluster (SPLIT); launch_direction has the rules.
+//
+// What bounds it (one GB300, device times): with few rows the weight stream (64 tokens x 6 over 384
+// experts of N = 1280, K = 5120: 245 us, 0.96 of the copy rate; gradient of 12288 rows over 128 experts of N =
+// 2304, K = 5120: 262 us, 0.93).  With many, the round trip of an accumulator (MMAs, read, release) and,
+// in long runs, the 1400 W power limit: 8192 x 6144 x 7168 291 us = 2.48 PFLOP/s, 49152 rows over 48
+// experts 1.82 ms in short runs, 1.98 ms (2.2 PFLOP/s) power-capped; without reading and adding the
+// accumulators the MMAs and the operand stream alone reach 2.97 PFLOP/s.  Measured and not taken: 16
+// summing warps of 64 columns (2.60 against 2.16 ms then: their polling and spills), 128-column pair
+// tiles with four accumulators (2.15 against 1.89: 1.5 times the operand bytes from L2), polling with
+// test_wait (+4 %).
 // Tiles run expert by expert, row tiles fastest, so the pairs running side by side share weight
 // tiles in L2.  Every wait is bounded as in gemm_pair.cu: on expiry the status word records
 // MOE_ERR_DEVICE_TIMEOUT and both CTAs drain before TMEM is freed.
@@ -42,8 +53,6 @@ namespace {
 
 constexpr int kBThreads = 384;   // 168 registers a thread at launch
 constexpr int kBFirstEpiWarp = 4;
-constexpr int kBCtlRegs = 104, kBEpiRegs = 200;
-static_assert(128 * kBCtlRegs + 256 * kBEpiRegs <= 384 * 168, "register split");
 constexpr int kBEpiWarps = 8;
 constexpr int kBTileCols = 256;                     // output columns of a tile
 constexpr int kBHalfBytes = 128 * 128;              // 128 rows of x, or 128 of the tile's weight rows
@@ -60,7 +69,7 @@ constexpr int kBBarOff = kBScaleOff + 2 * kBScaleBytes;
 constexpr int kBTabOff = kBBarOff + 256;            // per expert: first row, first tile
 constexpr int kBSmemBytes = kBTabOff + 2 * 4 * (kMaxExperts + 1) + 1024;
 static_assert(kBSmemBytes <= 232448, "block GEMM shared memory");
-static_assert(kBBarOff % 8 == 0 && 8 * (2 * kBMaxStages + 9) + 8 <= 256, "block GEMM barriers");
+static_assert(kBBarOff % 8 == 0 && 8 * (2 * kBMaxStages + 13) + 8 <= 256, "block GEMM barriers");
 
 // One CTA (G = 1) or a pair (G = 2) works on a tile of 128 G rows by 256 columns; a CTA stages its 128
 // rows of x and 256 / G of the weight rows.
@@ -69,6 +78,15 @@ struct BlockGeo {
   static constexpr int kRows = 128 * G;
   static constexpr int kStageBytes = (1 + 2 / G) * kBHalfBytes;
   static constexpr int kStages = kBRingBytes / kStageBytes;
+  // A pair runs a block's MMAs as two halves of 128 columns with accumulators of their own, so that a
+  // half's sums need not wait for the other half's MMAs; a CTA then holds 64 weight rows of each half.
+  // (A single CTA would read its x tile twice for that, and shared memory's bandwidth bounds it.)
+  static constexpr int kHalves = G;
+  static constexpr int kMmaCols = kBTileCols / kHalves;
+  static constexpr int kWRows = 128 / G;  // weight rows (gradient: columns) of a TMA box
+  // registers a thread of the control and the summing warpgroups: the block starts with 168 each
+  static constexpr int kCtlRegs = G == 2 ? 72 : 104, kSumRegs = G == 2 ? 216 : 200;
+  static_assert(128 * kCtlRegs + 256 * kSumRegs <= kBThreads * 168, "register split");
 };
 
 struct BlockParams {  // 64-byte aligned through its CUtensorMap members
@@ -82,8 +100,8 @@ struct BlockParams {  // 64-byte aligned through its CUtensorMap members
 
 // Instruction descriptor of kind::f8f6f4: fp32 accumulator (bit 4), E4M3 operands, B read along its
 // rows (bit 16) for the gradient, N / 8 at [17, 23), M / 16 at [24, 29).
-__device__ __forceinline__ uint32_t block_idesc(bool dgrad, int rows) {
-  return (1u << 4) | ((dgrad ? 1u : 0u) << 16) | ((uint32_t)(kBTileCols >> 3) << 17) | ((uint32_t)(rows >> 4) << 24);
+__device__ __forceinline__ uint32_t block_idesc(bool dgrad, int rows, int cols) {
+  return (1u << 4) | ((dgrad ? 1u : 0u) << 16) | ((uint32_t)(cols >> 3) << 17) | ((uint32_t)(rows >> 4) << 24);
 }
 
 template <int G>
@@ -195,18 +213,19 @@ template <int G, bool DGRAD, bool SPLIT>
 __global__ void __launch_bounds__(kBThreads, 1) gemm_block_kernel(const __grid_constant__ BlockParams p) {
   static_assert(G == 1 || !SPLIT, "split tiles run on single CTAs");
   constexpr int kStages = BlockGeo<G>::kStages, kStageBytes = BlockGeo<G>::kStageBytes, kRows = BlockGeo<G>::kRows;
+  constexpr int kHalves = BlockGeo<G>::kHalves, kWRows = BlockGeo<G>::kWRows;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sbase = smem_u32(smem);
   const uint32_t bar0 = sbase + kBBarOff;
   auto full_bar = [&](int s) { return bar0 + 8u * s; };
   auto empty_bar = [&](int s) { return bar0 + 8u * (kStages + s); };
-  auto tmem_full = [&](int b) { return bar0 + 8u * (2 * kStages + b); };
-  auto tmem_empty = [&](int b) { return bar0 + 8u * (2 * kStages + 2 + b); };
-  auto scale_full = [&](int b) { return bar0 + 8u * (2 * kStages + 4 + b); };
-  auto scale_empty = [&](int b) { return bar0 + 8u * (2 * kStages + 6 + b); };
-  const uint32_t drain_bar = bar0 + 8u * (2 * kStages + 8);
-  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + kBBarOff + 8 * (2 * kStages + 9));
+  auto tmem_full = [&](int b) { return bar0 + 8u * (2 * kStages + b); };   // b: buffer * kHalves + half
+  auto tmem_empty = [&](int b) { return bar0 + 8u * (2 * kStages + 2 * kHalves + b); };
+  auto scale_full = [&](int b) { return bar0 + 8u * (2 * kStages + 4 * kHalves + b); };
+  auto scale_empty = [&](int b) { return bar0 + 8u * (2 * kStages + 4 * kHalves + 2 + b); };
+  const uint32_t drain_bar = bar0 + 8u * (2 * kStages + 4 * kHalves + 4);
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + kBBarOff + 8 * (2 * kStages + 4 * kHalves + 5));
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
   int32_t* row_begin = reinterpret_cast<int32_t*>(smem + kBTabOff);
   int32_t* tile_base = row_begin + kMaxExperts + 1;
@@ -225,9 +244,11 @@ __global__ void __launch_bounds__(kBThreads, 1) gemm_block_kernel(const __grid_c
       mbar_init(full_bar(s), 1);   // expect_tx arrival of the even (or only) CTA's producer
       mbar_init(empty_bar(s), 1);  // the MMA commit
     }
-    for (int b = 0; b < 2; ++b) {
+    for (int b = 0; b < 2 * kHalves; ++b) {
       mbar_init(tmem_full(b), 1);
-      mbar_init(tmem_empty(b), G * kBEpiWarps);  // warps of every CTA of the tile
+      mbar_init(tmem_empty(b), G * kBEpiWarps / kHalves);  // the half's warps of every CTA of the tile
+    }
+    for (int b = 0; b < 2; ++b) {
       mbar_init(scale_full(b), 2);               // the two loading warps
       mbar_init(scale_empty(b), kBEpiWarps);
     }
@@ -284,7 +305,7 @@ __global__ void __launch_bounds__(kBThreads, 1) gemm_block_kernel(const __grid_c
   const int b_lo = (int)((uint32_t)RB * part / parts), b_hi = (int)((uint32_t)RB * (part + 1) / parts);
 
   if (warp < kBFirstEpiWarp) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kBCtlRegs));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(BlockGeo<G>::kCtlRegs));
     if (warp == 0) {
       // ------------------------------------------------------------------ producer
       const uint32_t lfull0 = G == 2 ? mapa_shared(full_bar(0), 0) : full_bar(0);
@@ -296,7 +317,7 @@ __global__ void __launch_bounds__(kBThreads, 1) gemm_block_kernel(const __grid_c
         const int rows_left = group_size(bt.e) - bt.mt * kRows;
         const int rows_mine = rows_left - (int)rank * 128;
         const int row0 = row_begin[bt.e] + bt.mt * kRows + (int)rank * 128;
-        const int col0 = bt.nt * kBTileCols + (int)rank * 128;
+        const int col0 = bt.nt * kBTileCols + (int)rank * kWRows;
         const uint32_t tx = (uint32_t)kBHalfBytes * (G == 2 ? 4u : 3u);  // of every CTA of the tile
         for (int b = b_lo; b < b_hi; ++b) {
           if (!warp_wait(empty_bar(slot), phase ^ 1u, sync, a.timeout_ns)) {
@@ -306,16 +327,13 @@ __global__ void __launch_bounds__(kBThreads, 1) gemm_block_kernel(const __grid_c
           if (elect_one()) {
             if (leader) mbar_arrive_expect_tx(full_bar(slot), tx);
             const uint32_t st = sbase + (uint32_t)slot * kStageBytes, lfull = lfull0 + 8u * slot;
-            if (G == 2) {
-              if (DGRAD) tma_load_3d_pair(st + kBHalfBytes, &p.tmap_w, lfull, col0, b * kFp8Block, bt.e);
-              else tma_load_3d_pair(st + kBHalfBytes, &p.tmap_w, lfull, b * kFp8Block, col0, bt.e);
-            } else {
 #pragma unroll
-              for (int h = 1; h <= 2; ++h) {
-                const int c = col0 + (h - 1) * 128;
-                if (DGRAD) tma_load_3d(st + h * kBHalfBytes, &p.tmap_w, lfull, c, b * kFp8Block, bt.e);
-                else tma_load_3d(st + h * kBHalfBytes, &p.tmap_w, lfull, b * kFp8Block, c, bt.e);
-              }
+            for (int h = 0; h < 2; ++h) {  // 128 columns each, kWRows of them in this CTA
+              const int c = col0 + h * 128;
+              const uint32_t dst = st + kBHalfBytes + (uint32_t)(h * kWRows * 128);
+              const int x = DGRAD ? c : b * kFp8Block, y = DGRAD ? b * kFp8Block : c;
+              if (G == 2) tma_load_3d_pair(dst, &p.tmap_w, lfull, x, y, bt.e);
+              else tma_load_3d(dst, &p.tmap_w, lfull, x, y, bt.e);
             }
             load_rows_x<G>(p, st, lfull, b * kFp8Block, row0, rows_mine);
           }
@@ -335,15 +353,16 @@ __global__ void __launch_bounds__(kBThreads, 1) gemm_block_kernel(const __grid_c
         bool ok = true, issued = false;
         // K-major tiles: 128-byte rows, 8-row groups 1024 bytes apart, an MMA step 32 bytes along the
         // row.  MN-major B (gradient): the same tiles read along their rows, 128 columns a tile (the
-        // next 128 kBHalfBytes further), a step 32 rows (4096 bytes).
+        // next 128 kBHalfBytes further; a pair's 64 columns of a half are 64-byte rows), a step 32 rows.
         const uint64_t a_desc0 = smem_desc(sbase, 16, 1024, kLayoutSwizzle128B);
-        const uint64_t b_desc0 = smem_desc(sbase + kBHalfBytes, DGRAD ? kBHalfBytes : 16, 1024, kLayoutSwizzle128B);
+        const uint64_t b_desc0 = smem_desc(sbase + kBHalfBytes, DGRAD ? kBHalfBytes : 16, DGRAD ? 8 * kWRows : 1024,
+                                           DGRAD && kWRows == 64 ? kLayoutSwizzle64B : kLayoutSwizzle128B);
         constexpr uint64_t kSlotStep = kStageBytes >> 4;
-        constexpr uint64_t kBStep = (DGRAD ? 4096 : 32) >> 4;
-        const uint32_t idesc = block_idesc(DGRAD, kRows);
+        constexpr uint64_t kBStep = (DGRAD ? 32 * kWRows : 32) >> 4, kHalfStep = (kWRows * 128) >> 4;
+        const uint32_t idesc = block_idesc(DGRAD, kRows, BlockGeo<G>::kMmaCols);
         for (int64_t tile = first_tile; ok && tile < total_tiles; tile += tile_step) {
           for (int b = b_lo; b < b_hi; ++b) {
-            if (!warp_wait(tmem_empty(buf), acc_phase ^ 1u, sync, a.timeout_ns) ||
+            if (!warp_wait(tmem_empty(buf * kHalves), acc_phase ^ 1u, sync, a.timeout_ns) ||
                 !warp_wait(full_bar(slot), phase, sync, a.timeout_ns)) {
               ok = false;
               break;
@@ -355,10 +374,27 @@ __global__ void __launch_bounds__(kBThreads, 1) gemm_block_kernel(const __grid_c
 #pragma unroll
               for (int j = 0; j < 4; ++j)
                 tc_mma_f8<G>(d, a_desc0 + so + 2 * j, b_desc0 + so + kBStep * j, idesc, j > 0 ? 1u : 0u);
-              tc_commit_all<G>(empty_bar(slot));
-              tc_commit_all<G>(tmem_full(buf));
+              if (kHalves == 1) tc_commit_all<G>(empty_bar(slot));
+              tc_commit_all<G>(tmem_full(buf * kHalves));
             }
             __syncwarp();
+            if (kHalves == 2) {
+              issued = true;
+              if (!warp_wait(tmem_empty(buf * 2 + 1), acc_phase ^ 1u, sync, a.timeout_ns)) {
+                ok = false;
+                break;
+              }
+              tc_fence_after();
+              if (elect_one()) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                  tc_mma_f8<G>(d + 128, a_desc0 + so + 2 * j, b_desc0 + so + kHalfStep + kBStep * j, idesc,
+                               j > 0 ? 1u : 0u);
+                tc_commit_all<G>(empty_bar(slot));
+                tc_commit_all<G>(tmem_full(buf * 2 + 1));
+              }
+              __syncwarp();
+            }
             issued = true;
             if (++slot == kStages) {
               slot = 0;
@@ -420,9 +456,10 @@ __global__ void __launch_bounds__(kBThreads, 1) gemm_block_kernel(const __grid_c
     }
   } else {
     // ------------------------------------------------------------------ sums over blocks (both CTAs)
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kBEpiRegs));
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(BlockGeo<G>::kSumRegs));
     const int quad = warp & 3, half = (warp - kBFirstEpiWarp) >> 2;
-    const uint32_t leader_empty0 = G == 2 ? mapa_shared(tmem_empty(0), 0) : tmem_empty(0);
+    const int mine = kHalves == 2 ? half : 0;  // which accumulators these warps read
+    const uint32_t leader_empty0 = G == 2 ? mapa_shared(tmem_empty(mine), 0) : tmem_empty(mine);
     const uint32_t tlane = tmem_base + ((uint32_t)(quad * 32) << 16) + (uint32_t)(half * 128);
     const float* scales = reinterpret_cast<const float*>(smem + kBScaleOff);
     uint32_t buf = 0, acc_phase = 0, sbuf = 0, sphase = 0;
@@ -446,28 +483,50 @@ __global__ void __launch_bounds__(kBThreads, 1) gemm_block_kernel(const __grid_c
         const int nb = min(kBScaleBlocks, b_hi - b0);
         for (int b = 0; b < nb; ++b) {
           const float s = sc[b * kBScaleRows + quad * 32 + lane] * sc[b * kBScaleRows + 128 + half];
-          if (!sums_wait(tmem_full(buf), acc_phase, sync)) {
+          if (!sums_wait(tmem_full(buf * kHalves + mine), acc_phase, sync)) {
             ok = false;
             break;
           }
           tc_fence_after();
           if (any) {
             const uint32_t t = tlane + buf * kBTileCols;
+            // The accumulator is released once the registers hold the block, before the last sums.  A
+            // pair's warps also read the next 32 columns under the sums of the last 32 (-5 % at 192 rows a
+            // group, N = 6144, K = 7168; single CTAs, bound by HBM, were 2 % slower that way).
+            auto release = [&] {
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive_cluster_relaxed(leader_empty0 + 8u * kHalves * buf);
+            };
+            auto add = [&](float* sums, const float* v) {
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              float v[32];
-              tc_ld_32x32b_x32(t + 32 * c, v);
+              for (int i = 0; i < 32; i += 2) fma_pair(sums[i], sums[i + 1], v[i], v[i + 1], s);
+            };
+            if (G == 2) {
+              float v0[32], v1[32];
+              tc_ld_32x32b_x32(t, v0);
+              tc_ld_32x32b_x32(t + 32, v1);
               tc_wait_ld();
-              if (c == 3) {  // registers hold the block: release its accumulator before the last sums
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive_cluster_relaxed(leader_empty0 + 8u * buf);
-              }
+              add(acc, v0);
+              tc_ld_32x32b_x32(t + 64, v0);
+              add(acc + 32, v1);
+              tc_ld_32x32b_x32(t + 96, v1);
+              tc_wait_ld();
+              release();
+              add(acc + 64, v0);
+              add(acc + 96, v1);
+            } else {
 #pragma unroll
-              for (int i = 0; i < 32; i += 2) fma_pair(acc[32 * c + i], acc[32 * c + i + 1], v[i], v[i + 1], s);
+              for (int c = 0; c < 4; ++c) {
+                float v[32];
+                tc_ld_32x32b_x32(t + 32 * c, v);
+                tc_wait_ld();
+                if (c == 3) release();
+                add(acc + 32 * c, v);
+              }
             }
           } else if (lane == 0) {
-            mbar_arrive_cluster_relaxed(leader_empty0 + 8u * buf);
+            mbar_arrive_cluster_relaxed(leader_empty0 + 8u * kHalves * buf);
           }
           buf ^= 1u;
           if (buf == 0) acc_phase ^= 1u;
@@ -639,13 +698,14 @@ __global__ void __launch_bounds__(kBThreads, 1) gemm_block_kernel(const __grid_c
 
 // ---------------------------------------------------------------------- host side
 bool encode_codes(CUtensorMap* m, const uint8_t* base, int rank, const cuuint64_t* dims, const cuuint64_t* strides,
-                  cuuint32_t rows) {
+                  cuuint32_t bytes, cuuint32_t rows) {
   EncodeTiledFn encode = get_encode_fn();
   if (!encode) return false;
-  const cuuint32_t box[3] = {128, rows, 1};
+  const cuuint32_t box[3] = {bytes, rows, 1};
   const cuuint32_t es[3] = {1, 1, 1};
   return encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, (cuuint32_t)rank, const_cast<uint8_t*>(base), dims, strides, box, es,
-                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, bytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+                CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -673,8 +733,9 @@ cudaError_t launch_tiles(const GemmBlockArgs& a, int64_t tiles, int split, cudaS
   const cuuint64_t xd[2] = {red, (cuuint64_t)a.M}, xst[1] = {red};
   const cuuint64_t wd[3] = {(cuuint64_t)a.K, (cuuint64_t)a.N, (cuuint64_t)a.E};
   const cuuint64_t wst[2] = {(cuuint64_t)a.K, (cuuint64_t)a.K * (cuuint64_t)a.N};
-  if (!encode_codes(&p.tmap_x, a.x, 2, xd, xst, 128) || !encode_codes(&p.tmap_x32, a.x, 2, xd, xst, 32) ||
-      !encode_codes(&p.tmap_w, a.w, 3, wd, wst, 128))
+  constexpr int kWRows = BlockGeo<G>::kWRows;
+  if (!encode_codes(&p.tmap_x, a.x, 2, xd, xst, 128, 128) || !encode_codes(&p.tmap_x32, a.x, 2, xd, xst, 128, 32) ||
+      !encode_codes(&p.tmap_w, a.w, 3, wd, wst, DGRAD ? kWRows : 128, DGRAD ? 128 : kWRows))
     return cudaErrorInvalidValue;
   p.a = a;
   const int64_t cols = DGRAD ? a.K : a.N;

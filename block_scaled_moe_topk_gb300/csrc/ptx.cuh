@@ -305,7 +305,7 @@ __device__ __forceinline__ void tc_mma_pair_mxf4(uint32_t d, uint64_t adesc, uin
 
 // Shared-memory matrix descriptor (tcgen05 format): start address, leading and
 // stride byte offsets (all >> 4), descriptor version 1, layout type in [61,64).
-enum : uint32_t { kLayoutNone = 0, kLayoutSwizzle128B = 2 };
+enum : uint32_t { kLayoutNone = 0, kLayoutSwizzle128B = 2, kLayoutSwizzle64B = 4 };
 __device__ __forceinline__ uint64_t smem_desc(uint32_t saddr, uint32_t lbo_bytes, uint32_t sbo_bytes, uint32_t layout) {
   uint64_t d = 0;
   d |= (uint64_t)((saddr >> 4) & 0x3FFF);
