@@ -392,135 +392,153 @@ def _table(t, dtype, shape, where, name):
     _want(t.is_cuda, where, f"{name} must be on the GPU")
 
 
-def _plain(t, dtype):
-    """Whether a matrix plainly passes _matrix (unit column stride, rows that do not overlap)."""
-    return t.dtype is dtype and t.is_cuda and t.dim() == 2 and t.stride(1) == 1
-
-
-def _stride(t):
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+_ROWS = {d: c for d, c in _DTYPES.items() if d is not torch.uint8}
 
 
 def _fixed(t, dtype):
     return t.dtype is dtype and t.is_cuda and t.is_contiguous()
 
 
-_ROWS = (torch.bfloat16, torch.float16, torch.float32)
+def _row_stride(t, shape):
+    """Elements between rows, or 0 unless the matrix plainly has unit column stride and is on the GPU."""
+    st = t.stride()
+    if len(shape) != 2 or st[1] != 1 or not t.is_cuda:
+        return 0
+    return st[0] if shape[0] > 1 else max(st[0], shape[1])
+
+
+def _stride(t):
+    """Elements between rows of a matrix; overlapping rows are left for the library to refuse."""
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
 
 
 def moe_permute(x, inv, rows, stream=None):
     """rows[inv[t, j]] = x[t]: x [T, H], inv int32 [T, k] (outside [0, R): dropped) -> rows [R, H]."""
-    dt = x.dtype
-    if not (dt in _DTYPES and _plain(x, dt) and _plain(rows, dt) and _fixed(inv, _I32) and inv.dim() == 2 and
-            inv.shape[0] == x.shape[0] and rows.shape[1] == x.shape[1]):
+    dt, sx, si, sr = x.dtype, x.shape, inv.shape, rows.shape
+    tx, tr = _row_stride(x, sx), _row_stride(rows, sr)
+    if not (tx and tr and dt in _DTYPES and rows.dtype is dt and _fixed(inv, _I32) and len(si) == 2 and
+            si[0] == sx[0] and sr[1] == sx[1]):
         fn = "moe_permute"
         _table(inv, _I32, (None, None), fn, "inv")
-        _matrix(x, fn, "x", (inv.shape[0], None), _DTYPES)
-        _matrix(rows, fn, "rows", (None, x.shape[1]), (dt,))
-    T, H = x.shape
-    _check(lib().moe_permute(x.data_ptr(), _stride(x), _DTYPES[dt], inv.data_ptr(), T, H, inv.shape[1],
-                             rows.data_ptr(), _stride(rows), rows.shape[0], _stream(stream)), "moe_permute")
+        _matrix(x, fn, "x", (si[0], None), _DTYPES)
+        _matrix(rows, fn, "rows", (None, sx[1]), (dt,))
+        tx, tr = _stride(x), _stride(rows)
+    _check(lib().moe_permute(x.data_ptr(), tx, _DTYPES[dt], inv.data_ptr(), sx[0], sx[1], si[1], rows.data_ptr(), tr,
+                             sr[0], _stream(stream)), "moe_permute")
 
 
 def moe_permute_backward(d_rows, inv, d_x, stream=None):
     """Gradient of moe_permute: d_x[t] = sum_j d_rows[inv[t, j]]."""
-    dt = d_rows.dtype
-    if not (dt in _ROWS and _plain(d_rows, dt) and _plain(d_x, dt) and _fixed(inv, _I32) and inv.dim() == 2 and
-            inv.shape[0] == d_x.shape[0] and d_rows.shape[1] == d_x.shape[1]):
+    dt, sr, si, sx = d_rows.dtype, d_rows.shape, inv.shape, d_x.shape
+    tr, tx = _row_stride(d_rows, sr), _row_stride(d_x, sx)
+    if not (tr and tx and dt in _ROWS and d_x.dtype is dt and _fixed(inv, _I32) and len(si) == 2 and
+            si[0] == sx[0] and sr[1] == sx[1]):
         fn = "moe_permute_backward"
         _table(inv, _I32, (None, None), fn, "inv")
         _matrix(d_rows, fn, "d_rows", (None, None), _ROWS)
-        _matrix(d_x, fn, "d_x", (inv.shape[0], d_rows.shape[1]), (dt,))
-    T, H = d_x.shape
-    _check(lib().moe_permute_backward(d_rows.data_ptr(), _stride(d_rows), d_rows.shape[0], _DTYPES[dt], inv.data_ptr(),
-                                      T, H, inv.shape[1], d_x.data_ptr(), _stride(d_x), _stream(stream)),
-           "moe_permute_backward")
+        _matrix(d_x, fn, "d_x", (si[0], sr[1]), (dt,))
+        tr, tx = _stride(d_rows), _stride(d_x)
+    _check(lib().moe_permute_backward(d_rows.data_ptr(), tr, sr[0], _DTYPES[dt], inv.data_ptr(), sx[0], sx[1], si[1],
+                                      d_x.data_ptr(), tx, _stream(stream)), "moe_permute_backward")
 
 
 def moe_unpermute(rows, inv, topk_w, out, stream=None):
     """out[t] = sum_j topk_w[t, j] rows[inv[t, j]]: rows [R, H], topk_w fp32 [T, k] -> out [T, H]."""
-    dt = rows.dtype
-    if not (topk_w is not None and dt in _ROWS and _plain(rows, dt) and _plain(out, dt) and _fixed(inv, _I32) and
-            _fixed(topk_w, _F32) and inv.dim() == 2 and inv.shape == topk_w.shape and
-            inv.shape[0] == out.shape[0] and rows.shape[1] == out.shape[1]):
+    dt, sr, si, so = rows.dtype, rows.shape, inv.shape, out.shape
+    tr, to = _row_stride(rows, sr), _row_stride(out, so)
+    if not (tr and to and dt in _ROWS and out.dtype is dt and _fixed(inv, _I32) and len(si) == 2 and
+            topk_w is not None and _fixed(topk_w, _F32) and topk_w.shape == si and si[0] == so[0] and sr[1] == so[1]):
         fn = "moe_unpermute"
         _table(inv, _I32, (None, None), fn, "inv")
         _matrix(rows, fn, "rows", (None, None), _ROWS)
-        _matrix(out, fn, "out", (inv.shape[0], rows.shape[1]), (dt,))
-        _table(topk_w, _F32, inv.shape, fn, "topk_w")
-    T, H = out.shape
-    _check(lib().moe_unpermute(rows.data_ptr(), _stride(rows), rows.shape[0], _DTYPES[dt], inv.data_ptr(),
-                               topk_w.data_ptr(), T, H, inv.shape[1], out.data_ptr(), _stride(out), _stream(stream)),
-           "moe_unpermute")
+        _matrix(out, fn, "out", (si[0], sr[1]), (dt,))
+        _table(topk_w, _F32, si, fn, "topk_w")
+        tr, to = _stride(rows), _stride(out)
+    _check(lib().moe_unpermute(rows.data_ptr(), tr, sr[0], _DTYPES[dt], inv.data_ptr(), topk_w.data_ptr(), so[0],
+                               so[1], si[1], out.data_ptr(), to, _stream(stream)), "moe_unpermute")
 
 
 def moe_unpermute_backward(d_out, rows, inv, topk_w, d_rows, d_topk_w, stream=None):
     """Gradients of moe_unpermute: d_rows[inv[t, j]] = topk_w[t, j] d_out[t] and d_topk_w[t, j] =
     <d_out[t], rows[inv[t, j]]>.  Either result may be None; rows may be None without d_topk_w."""
     fn = "moe_unpermute_backward"
-    _table(inv, _I32, (None, None), fn, "inv")
-    T, k = inv.shape
-    _matrix(d_out, fn, "d_out", (T, None), _ROWS)
-    dt, H = d_out.dtype, d_out.shape[1]
-    _table(topk_w, _F32, (T, k), fn, "topk_w")
-    R = rp = rs = dp = ds = 0
+    dt, so, si = d_out.dtype, d_out.shape, inv.shape
+    to = _row_stride(d_out, so)
+    if not (to and dt in _ROWS and _fixed(inv, _I32) and len(si) == 2 and si[0] == so[0] and
+            topk_w is not None and _fixed(topk_w, _F32) and topk_w.shape == si):
+        _table(inv, _I32, (None, None), fn, "inv")
+        _matrix(d_out, fn, "d_out", (si[0], None), _ROWS)
+        _table(topk_w, _F32, si, fn, "topk_w")
+        to = _stride(d_out)
+    R = rp = tr = dp = td = 0
+    wp = None
     if d_rows is not None:
-        _matrix(d_rows, fn, "d_rows", (None, H), (dt,))
-        R, dp, ds = d_rows.shape[0], d_rows.data_ptr(), _stride(d_rows)
+        sd = d_rows.shape
+        td = _row_stride(d_rows, sd)
+        if not (td and d_rows.dtype is dt and sd[1] == so[1]):
+            _matrix(d_rows, fn, "d_rows", (None, so[1]), (dt,))
+            td = _stride(d_rows)
+        R, dp = sd[0], d_rows.data_ptr()
     if d_topk_w is not None:
-        _table(d_topk_w, _F32, (T, k), fn, "d_topk_w")
-        _matrix(rows, fn, "rows", (None if d_rows is None else R, H), (dt,))
-        R, rp, rs = rows.shape[0], rows.data_ptr(), _stride(rows)
-    _check(lib().moe_unpermute_backward(d_out.data_ptr(), _stride(d_out), rp, rs, R, _DTYPES[dt], inv.data_ptr(),
-                                        topk_w.data_ptr(), T, H, k, dp, ds,
-                                        None if d_topk_w is None else d_topk_w.data_ptr(), _stream(stream)), fn)
+        _want(rows is not None, fn, "d_topk_w needs rows")
+        sr = rows.shape
+        tr = _row_stride(rows, sr)
+        if not (tr and rows.dtype is dt and sr[1] == so[1] and (d_rows is None or sr[0] == R) and
+                _fixed(d_topk_w, _F32) and d_topk_w.shape == si):
+            _matrix(rows, fn, "rows", (None if d_rows is None else R, so[1]), (dt,))
+            _table(d_topk_w, _F32, si, fn, "d_topk_w")
+            tr = _stride(rows)
+        R, rp, wp = sr[0], rows.data_ptr(), d_topk_w.data_ptr()
+    _check(lib().moe_unpermute_backward(d_out.data_ptr(), to, rp, tr, R, _DTYPES[dt], inv.data_ptr(),
+                                        topk_w.data_ptr(), so[0], so[1], si[1], dp, td, wp, _stream(stream)), fn)
 
 
 def moe_topk_route_backward(topk_ids, topk_w, d_topk_w, d_logits, stream=None):
     """Gradient of moe_topk_route's weights: ids int32, topk_w and d_topk_w fp32 [T, k] -> d_logits fp32 [T, E]."""
+    si, sl = topk_ids.shape, d_logits.shape
     if not (_fixed(topk_ids, _I32) and _fixed(topk_w, _F32) and _fixed(d_topk_w, _F32) and _fixed(d_logits, _F32) and
-            topk_ids.dim() == 2 and d_logits.dim() == 2 and topk_ids.shape == topk_w.shape == d_topk_w.shape and
-            topk_ids.shape[0] == d_logits.shape[0]):
+            len(si) == 2 and len(sl) == 2 and topk_w.shape == si and d_topk_w.shape == si and si[0] == sl[0]):
         fn = "moe_topk_route_backward"
         _table(topk_ids, _I32, (None, None), fn, "topk_ids")
-        _table(topk_w, _F32, topk_ids.shape, fn, "topk_w")
-        _table(d_topk_w, _F32, topk_ids.shape, fn, "d_topk_w")
-        _table(d_logits, _F32, (topk_ids.shape[0], None), fn, "d_logits")
-    T, E = d_logits.shape
-    _check(lib().moe_topk_route_backward(topk_ids.data_ptr(), topk_w.data_ptr(), d_topk_w.data_ptr(), T, E,
-                                         topk_ids.shape[1], d_logits.data_ptr(), _stream(stream)),
-           "moe_topk_route_backward")
+        _table(topk_w, _F32, si, fn, "topk_w")
+        _table(d_topk_w, _F32, si, fn, "d_topk_w")
+        _table(d_logits, _F32, (si[0], None), fn, "d_logits")
+    _check(lib().moe_topk_route_backward(topk_ids.data_ptr(), topk_w.data_ptr(), d_topk_w.data_ptr(), sl[0], sl[1],
+                                         si[1], d_logits.data_ptr(), _stream(stream)), "moe_topk_route_backward")
 
 
 def moe_quantize_fp8_block(x, codes, scales, block_rows=1, stream=None):
     """x [rows, K] -> E4M3 codes u8 [rows, K] and fp32 scales [ceil(rows / block_rows), ceil(K / 128)],
     block_rows = 1 or 128."""
     fn = "moe_quantize_fp8_block"
-    _want(block_rows in (1, 128), fn, "block_rows must be 1 or 128")
-    _matrix(x, fn, "x", (None, None), _ROWS)
-    rows, K = x.shape
-    _table(codes, _U8, (rows, K), fn, "codes")
-    _table(scales, _F32, (-(-rows // block_rows), -(-K // 128)), fn, "scales")
-    _check(lib().moe_quantize_fp8_block(x.data_ptr(), _stride(x), _DTYPES[x.dtype], rows, K, block_rows,
-                                        codes.data_ptr(), scales.data_ptr(), _stream(stream)), fn)
+    _want(block_rows == 1 or block_rows == 128, fn, "block_rows must be 1 or 128")
+    dt, sx = x.dtype, x.shape
+    tx = _row_stride(x, sx)
+    if not (tx and dt in _ROWS and _fixed(codes, _U8) and codes.shape == sx and _fixed(scales, _F32) and
+            scales.shape == ((sx[0] + block_rows - 1) // block_rows, (sx[1] + 127) // 128)):
+        _matrix(x, fn, "x", (None, None), _ROWS)
+        _table(codes, _U8, sx, fn, "codes")
+        _table(scales, _F32, (-(-sx[0] // block_rows), -(-sx[1] // 128)), fn, "scales")
+        tx = _stride(x)
+    _check(lib().moe_quantize_fp8_block(x.data_ptr(), tx, _DTYPES[dt], sx[0], sx[1], block_rows, codes.data_ptr(),
+                                        scales.data_ptr(), _stream(stream)), fn)
 
 
 def moe_permute_quantize_fp8_block(x, inv, codes, scales, stream=None):
     """moe_permute and moe_quantize_fp8_block in one pass: codes u8 [R, K], scales fp32 [R, ceil(K / 128)]."""
-    dt = x.dtype
-    if not (dt in _ROWS and _plain(x, dt) and _fixed(inv, _I32) and _fixed(codes, _U8) and _fixed(scales, _F32) and
-            inv.dim() == 2 and codes.dim() == 2 and scales.dim() == 2 and inv.shape[0] == x.shape[0] and
-            codes.shape[1] == x.shape[1] and scales.shape[0] == codes.shape[0] and
-            scales.shape[1] == (x.shape[1] + 127) // 128):
+    dt, sx, si, sc = x.dtype, x.shape, inv.shape, codes.shape
+    tx = _row_stride(x, sx)
+    if not (tx and dt in _ROWS and _fixed(inv, _I32) and len(si) == 2 and si[0] == sx[0] and _fixed(codes, _U8) and
+            len(sc) == 2 and sc[1] == sx[1] and _fixed(scales, _F32) and scales.shape == (sc[0], (sx[1] + 127) // 128)):
         fn = "moe_permute_quantize_fp8_block"
         _table(inv, _I32, (None, None), fn, "inv")
-        _matrix(x, fn, "x", (inv.shape[0], None), _ROWS)
-        _table(codes, _U8, (None, x.shape[1]), fn, "codes")
-        _table(scales, _F32, (codes.shape[0], (x.shape[1] + 127) // 128), fn, "scales")
-    T, K = x.shape
-    _check(lib().moe_permute_quantize_fp8_block(x.data_ptr(), _stride(x), _DTYPES[dt], inv.data_ptr(), T, K,
-                                                inv.shape[1], codes.data_ptr(), scales.data_ptr(), codes.shape[0],
-                                                _stream(stream)), "moe_permute_quantize_fp8_block")
+        _matrix(x, fn, "x", (si[0], None), _ROWS)
+        _table(codes, _U8, (None, sx[1]), fn, "codes")
+        _table(scales, _F32, (sc[0], (sx[1] + 127) // 128), fn, "scales")
+        tx = _stride(x)
+    _check(lib().moe_permute_quantize_fp8_block(x.data_ptr(), tx, _DTYPES[dt], inv.data_ptr(), sx[0], sx[1], si[1],
+                                                codes.data_ptr(), scales.data_ptr(), sc[0], _stream(stream)),
+           "moe_permute_quantize_fp8_block")
 
 
 def moe_gemm_fp8_block_workspace_bytes(M, N, K, E) -> int:
@@ -528,13 +546,14 @@ def moe_gemm_fp8_block_workspace_bytes(M, N, K, E) -> int:
 
 
 def _gemm_block(fn, dgrad, x, x_scale, w, w_scale, out, workspace, offsets, stream):
-    if w.dim() != 3:
+    if len(w.shape) != 3:
         _table(w, _U8, (None, None, None), fn, "w")
     E, N, K = w.shape
+    sx, dt = x.shape, out.dtype
+    M = sx[0]
     inner, outer = (N, K) if dgrad else (K, N)
-    M, dt = x.shape[0], out.dtype
     if not (_fixed(w, _U8) and _fixed(x, _U8) and _fixed(x_scale, _F32) and _fixed(w_scale, _F32) and dt in _ROWS and
-            _fixed(out, dt) and workspace.is_cuda and x.shape == (M, inner) and out.shape == (M, outer) and
+            _fixed(out, dt) and workspace.is_cuda and sx == (M, inner) and out.shape == (M, outer) and
             x_scale.shape == (M, (inner + 127) // 128) and
             w_scale.shape == (E, (N + 127) // 128, (K + 127) // 128) and
             (offsets is None or _fixed(offsets, _I64) and offsets.shape == (E + 1,))):
@@ -547,10 +566,11 @@ def _gemm_block(fn, dgrad, x, x_scale, w, w_scale, out, workspace, offsets, stre
         if offsets is not None:
             _table(offsets, _I64, (E + 1,), fn, "offsets")
         _want(workspace.is_cuda, fn, "the workspace must be on the GPU")
-    _check(getattr(lib(), fn)(x.data_ptr(), x_scale.data_ptr(), w.data_ptr(), w_scale.data_ptr(),
-                              None if offsets is None else offsets.data_ptr(), M, N, K, E, out.data_ptr(),
-                              _DTYPES[dt], workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-                              _stream(stream)), fn)
+    L = lib()
+    _check((L.moe_gemm_fp8_block_dgrad if dgrad else L.moe_gemm_fp8_block)(
+        x.data_ptr(), x_scale.data_ptr(), w.data_ptr(), w_scale.data_ptr(),
+        None if offsets is None else offsets.data_ptr(), M, N, K, E, out.data_ptr(), _DTYPES[dt], workspace.data_ptr(),
+        workspace.nbytes, _stream(stream)), fn)
 
 
 def moe_gemm_fp8_block(x, x_scale, w, w_scale, out, workspace, offsets=None, stream=None):

@@ -216,6 +216,29 @@ def test_row_gradients_against_differences():
 
 
 @gpu
+def test_odd_strides():
+    """Rows that overlap (an expanded matrix) are refused; one column, or one row, may have any stride there."""
+    inv = torch.arange(8, dtype=torch.int32, device="cuda").view(4, 2)
+    w, rows, x = torch.ones(4, 2, device="cuda"), torch.zeros(8, 64, device="cuda"), torch.ones(4, 64, device="cuda")
+    same, wide = torch.ones(1, 64, device="cuda").expand(4, 64), torch.ones(1, 64, device="cuda").expand(8, 64)
+    codes, scales = torch.zeros(8, 64, dtype=torch.uint8, device="cuda"), torch.zeros(8, 1, device="cuda")
+    for call in (lambda: moe.moe_permute(same, inv, rows), lambda: moe.moe_unpermute(wide, inv, w, x),
+                 lambda: moe.moe_permute_backward(wide, inv, x), lambda: moe.moe_unpermute_backward(same, rows, inv, w, rows, w),
+                 lambda: moe.moe_unpermute_backward(x, wide, inv, w, None, w), lambda: moe.moe_quantize_fp8_block(wide, codes, scales),
+                 lambda: moe.moe_permute_quantize_fp8_block(same, inv, codes, scales)):
+        with pytest.raises(moe.MoeError) as ei:
+            call()
+        assert ei.value.status == 1
+    col = torch.arange(16.0, device="cuda").view(4, 4)[:, 1:2]
+    got = torch.zeros(8, 1, device="cuda")
+    moe.moe_permute(col, inv, got)
+    assert got[:, 0].tolist() == [1, 1, 5, 5, 9, 9, 13, 13]
+    one = torch.arange(64.0, device="cuda").view(1, 64).as_strided((1, 64), (1, 1))
+    moe.moe_permute(one, inv[:1], rows)
+    assert torch.equal(rows[1], one[0]) and bool((rows[2:] == 0).all())
+
+
+@gpu
 def test_other_stream_and_repeat_bits():
     T, H, k, E = 200, 1024, 6, 64
     _, inv, R = mapping(T, k, E, 18)
