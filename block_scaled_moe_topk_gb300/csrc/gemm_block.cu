@@ -17,8 +17,8 @@
 // it.  The weight tile of the gradient is the same box of the same matrix, read by the MMA with its
 // reduction along rows (MN-major descriptor): no transposed copy of the weights exists.
 //   warp 0     TMA producer (converged, copies issued by an elected lane)
-//   warp 1     TMEM owner; in the even CTA the MMA issuer for both
-//   warps 2, 3 scales: chunks of 8 blocks' scales of the tile's rows into shared memory, eight lanes
+//   warps 1, 3 warp 1 owns TMEM; in the even CTA they issue the MMAs for both, a half of the columns each
+//   warp 2     scales: chunks of 8 blocks' scales of the tile's rows into shared memory, eight lanes
 //              a row.  A thread of the summing warps loading its own row's scale instead touches 32
 //              lines an instruction, in competition with the operands for the shared-memory pipe
 //              (49152 rows over 48 experts, N = 6144, K = 7168: 2.51 against 2.16 ms)
@@ -31,8 +31,8 @@
 // What bounds it (one GB300, device times): with few rows the weight stream (64 tokens x 6 over 384
 // experts of N = 1280, K = 5120: 245 us, 0.96 of the copy rate; gradient of 12288 rows over 128 experts of N =
 // 2304, K = 5120: 262 us, 0.93).  With many, the round trip of an accumulator (MMAs, read, release) and,
-// in long runs, the 1400 W power limit: 8192 x 6144 x 7168 291 us = 2.48 PFLOP/s, 49152 rows over 48
-// experts 1.82 ms in short runs, 1.98 ms (2.2 PFLOP/s) power-capped; without reading and adding the
+// in long runs, the 1400 W power limit: 8192 x 6144 x 7168 288 us = 2.5 PFLOP/s, 49152 rows over 48
+// experts 1.79 ms in short runs, 1.97 ms (2.2 PFLOP/s) power-capped; without reading and adding the
 // accumulators the MMAs and the operand stream alone reach 2.97 PFLOP/s.  Measured and not taken: 16
 // summing warps of 64 columns (2.60 against 2.16 ms then: their polling and spills), 128-column pair
 // tiles with four accumulators (2.15 against 1.89: 1.5 times the operand bytes from L2), polling with
@@ -69,7 +69,7 @@ constexpr int kBBarOff = kBScaleOff + 2 * kBScaleBytes;
 constexpr int kBTabOff = kBBarOff + 256;            // per expert: first row, first tile
 constexpr int kBSmemBytes = kBTabOff + 2 * 4 * (kMaxExperts + 1) + 1024;
 static_assert(kBSmemBytes <= 232448, "block GEMM shared memory");
-static_assert(kBBarOff % 8 == 0 && 8 * (2 * kBMaxStages + 13) + 8 <= 256, "block GEMM barriers");
+static_assert(kBBarOff % 8 == 0 && 8 * (2 * kBMaxStages + 14) + 8 <= 256, "block GEMM barriers");
 
 // One CTA (G = 1) or a pair (G = 2) works on a tile of 128 G rows by 256 columns; a CTA stages its 128
 // rows of x and 256 / G of the weight rows.
@@ -83,6 +83,9 @@ struct BlockGeo {
   // (A single CTA would read its x tile twice for that, and shared memory's bandwidth bounds it.)
   static constexpr int kHalves = G;
   static constexpr int kMmaCols = kBTileCols / kHalves;
+  // Each half has an issuing warp (1 and 3): eight MMAs of 128 columns and their commits take one warp
+  // longer to issue than they take to run.  Warp 3 helps to load scales otherwise.
+  static constexpr int kScaleWarps = 3 - kHalves;
   static constexpr int kWRows = 128 / G;  // weight rows (gradient: columns) of a TMA box
   // registers a thread of the control and the summing warpgroups: the block starts with 168 each
   static constexpr int kCtlRegs = G == 2 ? 72 : 104, kSumRegs = G == 2 ? 216 : 200;
@@ -224,8 +227,8 @@ __global__ void __launch_bounds__(kBThreads, 1) gemm_block_kernel(const __grid_c
   auto tmem_empty = [&](int b) { return bar0 + 8u * (2 * kStages + 2 * kHalves + b); };
   auto scale_full = [&](int b) { return bar0 + 8u * (2 * kStages + 4 * kHalves + b); };
   auto scale_empty = [&](int b) { return bar0 + 8u * (2 * kStages + 4 * kHalves + 2 + b); };
-  const uint32_t drain_bar = bar0 + 8u * (2 * kStages + 4 * kHalves + 4);
-  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + kBBarOff + 8 * (2 * kStages + 4 * kHalves + 5));
+  auto drain_bar = [&](int h) { return bar0 + 8u * (2 * kStages + 4 * kHalves + 4 + h); };
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + kBBarOff + 8 * (2 * kStages + 4 * kHalves + 6));
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
   int32_t* row_begin = reinterpret_cast<int32_t*>(smem + kBTabOff);
   int32_t* tile_base = row_begin + kMaxExperts + 1;
@@ -242,17 +245,17 @@ __global__ void __launch_bounds__(kBThreads, 1) gemm_block_kernel(const __grid_c
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
       mbar_init(full_bar(s), 1);   // expect_tx arrival of the even (or only) CTA's producer
-      mbar_init(empty_bar(s), 1);  // the MMA commit
+      mbar_init(empty_bar(s), kHalves);  // a commit of each half's MMAs
     }
     for (int b = 0; b < 2 * kHalves; ++b) {
       mbar_init(tmem_full(b), 1);
       mbar_init(tmem_empty(b), G * kBEpiWarps / kHalves);  // the half's warps of every CTA of the tile
     }
     for (int b = 0; b < 2; ++b) {
-      mbar_init(scale_full(b), 2);               // the two loading warps
+      mbar_init(scale_full(b), BlockGeo<G>::kScaleWarps);
+      mbar_init(drain_bar(b), 1);
       mbar_init(scale_empty(b), kBEpiWarps);
     }
-    mbar_init(drain_bar, 1);
     *abort_flag = 0;
     fence_mbar_init();
     prefetch_tensormap(&p.tmap_x);
@@ -345,8 +348,8 @@ __global__ void __launch_bounds__(kBThreads, 1) gemm_block_kernel(const __grid_c
         }
       }
       __syncwarp();
-    } else if (warp == 1) {
-      // ------------------------------------------------------------------ MMA issuer (even CTA)
+    } else if (warp == 1 || (kHalves == 2 && warp == 3)) {
+      // ------------------------------------------------------------------ MMA issuers (even CTA)
       if (leader) {
         int slot = 0;
         uint32_t phase = 0, buf = 0, acc_phase = 0;
@@ -355,46 +358,31 @@ __global__ void __launch_bounds__(kBThreads, 1) gemm_block_kernel(const __grid_c
         // row.  MN-major B (gradient): the same tiles read along their rows, 128 columns a tile (the
         // next 128 kBHalfBytes further; a pair's 64 columns of a half are 64-byte rows), a step 32 rows.
         const uint64_t a_desc0 = smem_desc(sbase, 16, 1024, kLayoutSwizzle128B);
-        const uint64_t b_desc0 = smem_desc(sbase + kBHalfBytes, DGRAD ? kBHalfBytes : 16, DGRAD ? 8 * kWRows : 1024,
+        const int h = warp == 3 ? 1 : 0;  // this warp's half of the columns
+        const uint64_t b_desc0 = smem_desc(sbase + kBHalfBytes + h * kWRows * 128, DGRAD ? kBHalfBytes : 16,
+                                           DGRAD ? 8 * kWRows : 1024,
                                            DGRAD && kWRows == 64 ? kLayoutSwizzle64B : kLayoutSwizzle128B);
         constexpr uint64_t kSlotStep = kStageBytes >> 4;
-        constexpr uint64_t kBStep = (DGRAD ? 32 * kWRows : 32) >> 4, kHalfStep = (kWRows * 128) >> 4;
+        constexpr uint64_t kBStep = (DGRAD ? 32 * kWRows : 32) >> 4;
         const uint32_t idesc = block_idesc(DGRAD, kRows, BlockGeo<G>::kMmaCols);
         for (int64_t tile = first_tile; ok && tile < total_tiles; tile += tile_step) {
           for (int b = b_lo; b < b_hi; ++b) {
-            if (!warp_wait(tmem_empty(buf * kHalves), acc_phase ^ 1u, sync, a.timeout_ns) ||
+            if (!warp_wait(tmem_empty(buf * kHalves + h), acc_phase ^ 1u, sync, a.timeout_ns) ||
                 !warp_wait(full_bar(slot), phase, sync, a.timeout_ns)) {
               ok = false;
               break;
             }
             tc_fence_after();
             const uint64_t so = (uint64_t)slot * kSlotStep;
-            const uint32_t d = tmem_base + buf * kBTileCols;
+            const uint32_t d = tmem_base + buf * kBTileCols + h * 128;
             if (elect_one()) {
 #pragma unroll
               for (int j = 0; j < 4; ++j)
                 tc_mma_f8<G>(d, a_desc0 + so + 2 * j, b_desc0 + so + kBStep * j, idesc, j > 0 ? 1u : 0u);
-              if (kHalves == 1) tc_commit_all<G>(empty_bar(slot));
-              tc_commit_all<G>(tmem_full(buf * kHalves));
+              tc_commit_all<G>(empty_bar(slot));
+              tc_commit_all<G>(tmem_full(buf * kHalves + h));
             }
             __syncwarp();
-            if (kHalves == 2) {
-              issued = true;
-              if (!warp_wait(tmem_empty(buf * 2 + 1), acc_phase ^ 1u, sync, a.timeout_ns)) {
-                ok = false;
-                break;
-              }
-              tc_fence_after();
-              if (elect_one()) {
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                  tc_mma_f8<G>(d + 128, a_desc0 + so + 2 * j, b_desc0 + so + kHalfStep + kBStep * j, idesc,
-                               j > 0 ? 1u : 0u);
-                tc_commit_all<G>(empty_bar(slot));
-                tc_commit_all<G>(tmem_full(buf * 2 + 1));
-              }
-              __syncwarp();
-            }
             issued = true;
             if (++slot == kStages) {
               slot = 0;
@@ -407,18 +395,20 @@ __global__ void __launch_bounds__(kBThreads, 1) gemm_block_kernel(const __grid_c
         if (issued) {
           // no MMA may still run when TMEM is freed
           if (elect_one()) {
-            if (G == 2) tc_commit_pair(drain_bar);
-            else tc_commit(drain_bar);
+            if (G == 2) tc_commit_pair(drain_bar(h));
+            else tc_commit(drain_bar(h));
           }
           __syncwarp();
-          warp_wait(drain_bar, 0, sync, 100000000ull, true);
+          warp_wait(drain_bar(h), 0, sync, 100000000ull, true);
         }
       }
       __syncwarp();
     } else {
-      // ---------------------------------------------------------------- scales (warps 2 and 3)
+      // ---------------------------------------------------------------- scales (warp 2, or 2 and 3)
       float* scales = reinterpret_cast<float*>(smem + kBScaleOff);
-      const int j = lane & 7, rsub = (warp - 2) * 4 + (lane >> 3);  // this lane's block, and row mod 8
+      constexpr int kStep = 4 * BlockGeo<G>::kScaleWarps;           // rows of one load of the warps
+      constexpr int kBatch = 8 * BlockGeo<G>::kScaleWarps;          // loads of a lane in flight
+      const int j = lane & 7, rsub = (warp - 2) * 4 + (lane >> 3);  // this lane's block, and row mod kStep
       const int sw_step = DGRAD ? KB : 1;
       uint32_t sbuf = 0, sphase = 0;
       bool ok = true;
@@ -432,21 +422,26 @@ __global__ void __launch_bounds__(kBThreads, 1) gemm_block_kernel(const __grid_c
         const float* sw = a.w_scale + (int64_t)bt.e * NB * KB + (DGRAD ? cb : cb * KB);
         for (int b0 = b_lo; b0 < b_hi; b0 += kBScaleBlocks) {
           const bool in = b0 + j < b_hi;
-          float v[16], wv = 0.0f;
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const int r = i * 8 + rsub;
-            v[i] = in && r < rows_here ? sx[(int64_t)r * RB + b0 + j] : 0.0f;
-          }
-          if (warp == 2 && lane < 16 && in) wv = sw[(int64_t)(b0 + j) * sw_step];
-          if (!warp_wait(scale_empty(sbuf), sphase ^ 1u, sync, a.timeout_ns)) {
-            ok = false;
-            break;
-          }
           float* dst = scales + sbuf * (kBScaleBytes / 4) + j * kBScaleRows;
+          const float* src = sx + (int64_t)rsub * RB + b0 + j;  // this lane's next row
+#pragma unroll 1
+          for (int q = 0; q < 128; q += kBatch * kStep) {
+            float v[kBatch];
 #pragma unroll
-          for (int i = 0; i < 16; ++i) dst[i * 8 + rsub] = v[i];
-          if (warp == 2 && lane < 16) dst[128 + (lane >> 3)] = wv;
+            for (int i = 0; i < kBatch; ++i, src += (int64_t)kStep * RB)
+              v[i] = in && q + i * kStep + rsub < rows_here ? *src : 0.0f;
+            if (q == 0) {  // the first loads are on their way before the chunk's buffer is free
+              const float wv = warp == 2 && lane < 16 && in ? sw[(int64_t)(b0 + j) * sw_step] : 0.0f;
+              if (!warp_wait(scale_empty(sbuf), sphase ^ 1u, sync, a.timeout_ns)) {
+                ok = false;
+                break;
+              }
+              if (warp == 2 && lane < 16) dst[128 + (lane >> 3)] = wv;
+            }
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) dst[q + i * kStep + rsub] = v[i];
+          }
+          if (!ok) break;
           __syncwarp();
           if (lane == 0) mbar_arrive(scale_full(sbuf));
           sbuf ^= 1u;

@@ -56,7 +56,7 @@ def test_expired_wait_is_reported_and_the_context_survives(case):
     d = json.loads(r.stdout.strip().splitlines()[-1])
     words = d["words"]
     assert d["status"] == 6 and words[1] == 1  # MOE_ERR_DEVICE_TIMEOUT, an expiry was recorded
-    # the first expiry: stage 0 in the MMA warp, or the accumulator in a summing warp
-    assert (words[2], words[5]) == (0, 1) or (words[2] - acc_ready in (0, acc_ready // 12) and 4 <= words[5] <= 11), words
+    # the first expiry: stage 0 in an MMA warp (1; 3 too on pairs), or the accumulator in a summing warp
+    assert (words[2] == 0 and words[5] in (1, 3)) or (words[2] - acc_ready in (0, acc_ready // 12) and 4 <= words[5] <= 11), words
     assert words[6] >= 25000                   # it waited the limit (50 ms or more at 2 GHz or less), in us
     assert d["alive"] == 999000.0 and d["seconds"] < 60
