@@ -216,6 +216,25 @@ def test_row_gradients_against_differences():
 
 
 @gpu
+@pytest.mark.parametrize("H", [32768, 32767])
+def test_rows_past_4_gib(H):
+    """Row offsets past 2^32 bytes: the last rows of an 8.6 GiB matrix."""
+    R = 70000
+    rows = torch.empty(R, H, dtype=torch.float32, device="cuda")
+    inv = torch.tensor([[R - 1, 0], [R - 2, 1]], dtype=torch.int32, device="cuda")
+    x = rows_like(2, H, dtype=torch.float32, seed=22).cuda()
+    w = torch.tensor([[0.5, 0.25], [1.0, -1.0]], device="cuda")
+    moe.moe_permute(x, inv, rows)
+    assert torch.equal(rows[-1], x[0]) and torch.equal(rows[-2], x[1]) and torch.equal(rows[0], x[0])
+    out = torch.empty_like(x)
+    moe.moe_unpermute(rows, inv, w, out)
+    assert torch.equal(out[0], 0.75 * x[0]) and bool((out[1] == 0).all())
+    dw = torch.empty(2, 2, device="cuda")
+    moe.moe_unpermute_backward(out, rows, inv, w, rows, dw)
+    assert torch.equal(rows[-1], 0.5 * out[0]) and bool((rows[-2] == 0).all())
+
+
+@gpu
 def test_odd_strides():
     """Rows that overlap (an expanded matrix) are refused; one column, or one row, may have any stride there."""
     inv = torch.arange(8, dtype=torch.int32, device="cuda").view(4, 2)

@@ -396,6 +396,23 @@ def test_weights_past_4_gib():
         assert bool(((out - ref).abs() <= (64 + 16) * 2.0 ** -22 * size).all())
 
 
+@gpu
+@pytest.mark.parametrize("N", [32768, 32765])
+def test_output_past_4_gib(N):
+    """Output offsets past 2^32 bytes, aligned rows and not: the last rows of 70000."""
+    M, K = 70000, 128
+    w, ws = make_weights(1, N, K, 3)
+    x, xs = make_rows(64, K, 4)
+    full = torch.zeros(M, K, dtype=torch.uint8, device="cuda")
+    scale = torch.ones(M, 1, device="cuda")
+    full[-64:], scale[-64:] = x.cuda(), xs.cuda()
+    out = product(full, scale, w.cuda(), ws.cuda(), None, torch.bfloat16)
+    got = out[-64:].double().cpu()
+    ref, size = values(x, xs, 1) @ weight_values(w, ws)[0].t(), values(x, xs, 1).abs() @ weight_values(w, ws)[0].t().abs()
+    assert bool(((got - ref).abs() <= U[torch.bfloat16] * ref.abs() + 17 * 2.0 ** -22 * size).all())
+    assert bool((out[:-64] == 0).all())
+
+
 def test_refusals():
     u8, f32 = lambda *s: torch.zeros(*s, dtype=torch.uint8), torch.zeros  # noqa: E731
     ws = u8(256)
