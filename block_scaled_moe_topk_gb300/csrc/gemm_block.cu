@@ -44,6 +44,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <cmath>
 
 #include "gemm_block_common.cuh"
 #include "gemm_common.cuh"
@@ -795,14 +796,26 @@ cudaError_t split_clusters(int split, int* clusters) {
 // against 1: 8 rows 10.1 against 22.7 us, 64 rows 11.6 against 23.7, 128 rows 14.2 against 24.7; K = 512:
 // 8 rows 8.3 against 6.6, 128 rows 13.4 against 8.2 (not split).
 //
-// Single CTAs or pairs: a group's last tile wastes half a tile on average, 64 rows against 128, but a
-// single CTA reads 48 KiB of operands a stage where a pair's CTA reads 32.
-//   at most 128 rows a group  the weight stream bounds both and singles hold more of it in flight: 48
-//                             experts x 64 rows 343 against 440 us, x 128 469 against 469
-//   129 to 224                one pair tile against two singles: x 192 rows 484 against 519 us
-//   225 to 736                a second pair tile is often nearly empty: x 256 692 against 586 us, x 512
-//                             1070 against 1057
-//   more                      x 1024 1950 against 1960 us; one expert x 8192 309 against 331 us
+// Single CTAs or pairs: the smaller estimate of tile_time.  A pair's tile is cheaper a row (0.49
+// against 2 x 0.56 us a block for 256 rows), a single's wastes fewer rows in a group's last tile.  48
+// experts, N = 6144, K = 7168, rows a group: single / pair us
+//   64: 345 / 411    128: 488 / 434    192: 547 / 449    256: 619 / 668    320: 742 / 846
+//   384: 886 / 845    512: 1112 / 1027    768: 1578 / 1533    1024: 2076 / 1906
+// one expert x 1024 rows 66 / 57, x 8192 333 / 288; 8 experts, N = 2048, K = 1024 x 512 rows 17.7 / 24.6.
+//
+// Estimated time (us) of the product in row tiles of `rows` rows: a group of r rows, spread by sqrt(r)
+// when there are several, has k + 1 tiles or more with probability P(r > k rows) (a linear ramp here).
+double tile_time(const GemmBlockArgs& a, int rows, int64_t col_tiles, int RB, double block_us) {
+  const double groups = (double)std::min<int64_t>(a.E, a.M), r = (double)a.M / groups;
+  const double width = groups > 1 ? 2.5 * std::sqrt(r) : 1e-9;
+  const double whole = std::floor(std::max(0.0, r - width) / rows);
+  double tiles = whole;
+  for (double k = whole; k * rows < r + width; k += 1)
+    tiles += k == 0 ? 1.0 : std::min(1.0, std::max(0.0, (r - k * rows) / width + 0.5));
+  const double rounds = tiles * groups * (double)col_tiles / (a.num_sms * 128 / rows);
+  return (rounds < 8 ? std::ceil(rounds) : rounds + 0.5) * (RB * block_us + 2.0);
+}
+
 template <bool DGRAD>
 cudaError_t launch_direction(const GemmBlockArgs& a, cudaStream_t s) {
   const int red = DGRAD ? a.N : a.K, cols = DGRAD ? a.K : a.N;
@@ -821,8 +834,8 @@ cudaError_t launch_direction(const GemmBlockArgs& a, cudaStream_t s) {
     if (singles <= clusters) break;
   }
   if (split > 1) return launch_tiles<1, DGRAD, true>(a, singles, split, s);
-  const bool single = singles <= a.num_sms || avg <= 128 || (groups > 1 && avg > 224 && avg <= 736);
-  if (single) return launch_tiles<1, DGRAD, false>(a, singles, 1, s);
+  if (tile_time(a, 128, col_tiles, RB, 0.56) <= tile_time(a, 256, col_tiles, RB, 0.49) + 2.0)  // pairs start 2 us later
+    return launch_tiles<1, DGRAD, false>(a, singles, 1, s);
   return launch_tiles<2, DGRAD, false>(a, max_row_tiles(a, BlockGeo<2>::kRows) * col_tiles, 1, s);
 }
 
