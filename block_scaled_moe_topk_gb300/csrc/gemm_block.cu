@@ -144,12 +144,6 @@ __device__ __forceinline__ void fma_pair(float& a0, float& a1, float v0, float v
   asm("mov.b64 {%0, %1}, %2;" : "=f"(a0), "=f"(a1) : "l"(a));
 }
 
-__device__ __forceinline__ void st_global_v8(void* p, const uint32_t (&w)[8]) {
-  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
-               "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
-               : "memory");
-}
-
 // bounded_wait for the warps that hold their sums in registers: inlined, because a call would have
 // to save the 128 sums around it.  Warp-uniform; false when the CTA aborts or the limit passes.
 __device__ __forceinline__ bool sums_wait(uint32_t bar, uint32_t parity, const Sync& s) {
@@ -544,32 +538,42 @@ __global__ void __launch_bounds__(kBThreads, 1) gemm_block_kernel(const __grid_c
             *reinterpret_cast<float4*>(prow + (((half * 32 + i) ^ (lane & 7)) << 2)) =
                 make_float4(acc[4 * i], acc[4 * i + 1], acc[4 * i + 2], acc[4 * i + 3]);
         }
-      } else if (p.out_vec && col0 + 128 <= cols) {
-        // 32-byte stores: every lane fills whole sectors of its own row
-        if (valid) {
+      } else if (col0 + 128 <= cols) {
+        // Every lane stores its own row, whole 32-byte sectors but for the ends of unaligned rows (17535
+        // rows of 13 experts, K = 1136: N = 2681 101 us, 2688 90 us; by consecutive lanes through a
+        // staging buffer, as the last columns below, 107)
+        if (p.out_vec) {
+          uint8_t* dst = static_cast<uint8_t*>(a.out) + (row * cols + col0) * (dt == kDtF32 ? 4 : 2);
           if (dt == kDtF32) {
-            float* dst = static_cast<float*>(a.out) + row * cols + col0;
 #pragma unroll
             for (int i = 0; i < 128; i += 8) {
               uint32_t w[8];
 #pragma unroll
               for (int q = 0; q < 8; ++q) w[q] = __float_as_uint(acc[i + q]);
-              st_global_v8(dst + i, w);
+              if (valid) st_global_v8(dst + 4 * i, w);
             }
           } else {
-            uint16_t* dst = static_cast<uint16_t*>(a.out) + row * cols + col0;
 #pragma unroll
             for (int i = 0; i < 128; i += 16) {
               uint32_t w[8];
 #pragma unroll
               for (int q = 0; q < 8; ++q) w[q] = out_pair(acc[i + 2 * q], acc[i + 2 * q + 1], dt);
-              st_global_v8(dst + i, w);
+              if (valid) st_global_v8(dst + 2 * i, w);
             }
           }
+        } else if (dt == kDtF32) {
+          uint32_t w[128];
+#pragma unroll
+          for (int i = 0; i < 128; ++i) w[i] = __float_as_uint(acc[i]);
+          store_words<128>(static_cast<uint8_t*>(a.out) + (row * cols + col0) * 4, w, valid);
+        } else {
+          uint32_t w[64];
+#pragma unroll
+          for (int i = 0; i < 64; ++i) w[i] = out_pair(acc[2 * i], acc[2 * i + 1], dt);
+          store_halves<64>(static_cast<uint8_t*>(a.out) + (row * cols + col0) * 2, w, valid);
         }
       } else {
-        // Any alignment and the last columns: 64 bytes of every row at a time through the warp's
-        // staging buffer (words swizzled by the row: conflict-free both ways), then consecutive
+        // The last columns: 64 bytes of every row at a time through the warp's staging buffer (words swizzled by the row: conflict-free both ways), then consecutive
         // elements of a row by consecutive lanes
         uint32_t* stage = reinterpret_cast<uint32_t*>(smem + kBOutOff + (warp - kBFirstEpiWarp) * kBOutBytes);
         const int rows_here = min(32, group_size(bt.e) - (row_local - lane));
