@@ -64,8 +64,9 @@ constexpr int kBOutOff = kBRingBytes;   // per-warp staging of unaligned output 
 constexpr int kBOutBytes = 32 * 64;                 // 32 rows x 64 bytes
 constexpr int kBScaleBlocks = 8;                    // reduction blocks of one scale chunk
 constexpr int kBScaleRows = 130;                    // 128 rows of x, then the weights' two column halves
-constexpr int kBScaleOff = kBOutOff + kBEpiWarps * kBOutBytes;  // two chunks [block][row], fp32
-constexpr int kBScaleBytes = kBScaleBlocks * kBScaleRows * 4;
+constexpr int kBScaleOff = kBOutOff + kBEpiWarps * kBOutBytes;  // two chunks [block][row], fp32 (and a tile)
+constexpr int kBScaleTile = kBScaleBlocks * kBScaleRows;  // then, with a tile's first chunk, the tile itself
+constexpr int kBScaleBytes = (kBScaleTile + 4) * 4;
 constexpr int kBBarOff = kBScaleOff + 2 * kBScaleBytes;
 constexpr int kBTabOff = kBBarOff + 256;            // per expert: first row, first tile
 constexpr int kBSmemBytes = kBTabOff + 2 * 4 * (kMaxExperts + 1) + 1024;
@@ -437,6 +438,11 @@ __global__ void __launch_bounds__(kBThreads, 1) gemm_block_kernel(const __grid_c
             for (int i = 0; i < kBatch; ++i) dst[q + i * kStep + rsub] = v[i];
           }
           if (!ok) break;
+          // the summing warps learn of the tile here: the search for its expert is a chain of dependent
+          // shared-memory reads, which would stand between their tiles
+          if (warp == 2 && lane == 0 && b0 == b_lo)
+            *reinterpret_cast<int4*>(scales + sbuf * (kBScaleBytes / 4) + kBScaleTile) =
+                make_int4(row_begin[bt.e] + row_local, rows_here, bt.nt, 0);
           __syncwarp();
           if (lane == 0) mbar_arrive(scale_full(sbuf));
           sbuf ^= 1u;
@@ -455,17 +461,21 @@ __global__ void __launch_bounds__(kBThreads, 1) gemm_block_kernel(const __grid_c
     uint32_t buf = 0, acc_phase = 0, sbuf = 0, sphase = 0;
     bool ok = true;
     for (int64_t tile = first_tile; ok && tile < total_tiles; tile += tile_step) {
-      const BlockTile bt = block_tile(tile, tile_base, E, NT);
-      const int row_local = bt.mt * kRows + (int)rank * 128 + quad * 32 + lane;
-      const bool valid = row_local < group_size(bt.e);
-      const int col0 = bt.nt * kBTileCols + half * 128;
-      const bool any = __any_sync(0xffffffffu, valid) && col0 < cols;
-      const int64_t row = (int64_t)row_begin[bt.e] + row_local;
+      if (!sums_wait(scale_full(sbuf), sphase, sync)) {
+        ok = false;
+        break;
+      }
+      const int4 hd = *reinterpret_cast<const int4*>(scales + sbuf * (kBScaleBytes / 4) + kBScaleTile);
+      const int rows_here = hd.y - quad * 32;  // rows of the tile in this warp's 32 (and past them)
+      const bool valid = lane < rows_here;
+      const int64_t row = (int64_t)hd.x + quad * 32 + lane;
+      const int col0 = hd.z * kBTileCols + half * 128;
+      const bool any = rows_here > 0 && col0 < cols;
       float acc[128];
 #pragma unroll
       for (int i = 0; i < 128; ++i) acc[i] = 0.0f;
       for (int b0 = b_lo; ok && b0 < b_hi; b0 += kBScaleBlocks) {
-        if (!sums_wait(scale_full(sbuf), sphase, sync)) {
+        if (b0 > b_lo && !sums_wait(scale_full(sbuf), sphase, sync)) {
           ok = false;
           break;
         }
@@ -576,7 +586,6 @@ __global__ void __launch_bounds__(kBThreads, 1) gemm_block_kernel(const __grid_c
         // The last columns: 64 bytes of every row at a time through the warp's staging buffer (words swizzled by the row: conflict-free both ways), then consecutive
         // elements of a row by consecutive lanes
         uint32_t* stage = reinterpret_cast<uint32_t*>(smem + kBOutOff + (warp - kBFirstEpiWarp) * kBOutBytes);
-        const int rows_here = min(32, group_size(bt.e) - (row_local - lane));
         const int64_t row0 = row - lane;
         const int swz = (lane >> 1) & 15;
         if (dt == kDtF32) {
