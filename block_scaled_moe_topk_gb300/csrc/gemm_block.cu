@@ -482,7 +482,9 @@ __global__ void __launch_bounds__(kBThreads, 1) gemm_block_kernel(const __grid_c
         const float* sc = scales + sbuf * (kBScaleBytes / 4);
         const int nb = min(kBScaleBlocks, b_hi - b0);
         for (int b = 0; b < nb; ++b) {
-          const float s = sc[b * kBScaleRows + quad * 32 + lane] * sc[b * kBScaleRows + 128 + half];
+          // multiplied only behind the accumulator's first reads: beside the operands' traffic shared
+          // memory answers after ~140 cycles
+          const float sx = sc[b * kBScaleRows + quad * 32 + lane], sw = sc[b * kBScaleRows + 128 + half];
           if (!sums_wait(tmem_full(buf * kHalves + mine), acc_phase, sync)) {
             ok = false;
             break;
@@ -498,6 +500,7 @@ __global__ void __launch_bounds__(kBThreads, 1) gemm_block_kernel(const __grid_c
               __syncwarp();
               if (lane == 0) mbar_arrive_cluster_relaxed(leader_empty0 + 8u * kHalves * buf);
             };
+            const float s = sx * sw;
             auto add = [&](float* sums, const float* v) {
 #pragma unroll
               for (int i = 0; i < 32; i += 2) fma_pair(sums[i], sums[i + 1], v[i], v[i + 1], s);
@@ -583,8 +586,9 @@ __global__ void __launch_bounds__(kBThreads, 1) gemm_block_kernel(const __grid_c
           store_halves<64>(static_cast<uint8_t*>(a.out) + (row * cols + col0) * 2, w, valid);
         }
       } else {
-        // The last columns: 64 bytes of every row at a time through the warp's staging buffer (words swizzled by the row: conflict-free both ways), then consecutive
-        // elements of a row by consecutive lanes
+        // The last columns: 64 bytes of every row at a time through the warp's staging buffer (words
+        // swizzled by the row: conflict-free both ways), then consecutive elements of a row by
+        // consecutive lanes
         uint32_t* stage = reinterpret_cast<uint32_t*>(smem + kBOutOff + (warp - kBFirstEpiWarp) * kBOutBytes);
         const int64_t row0 = row - lane;
         const int swz = (lane >> 1) & 15;
