@@ -31,12 +31,15 @@
 // What bounds it (one GB300, device times): with few rows the weight stream (64 tokens x 6 over 384
 // experts of N = 1280, K = 5120: 245 us, 0.96 of the copy rate; gradient of 12288 rows over 128 experts of N =
 // 2304, K = 5120: 262 us, 0.93).  With many, the round trip of an accumulator (MMAs, read, release) and,
-// in long runs, the 1400 W power limit: 8192 x 6144 x 7168 288 us = 2.5 PFLOP/s, 49152 rows over 48
-// experts 1.79 ms in short runs, 1.97 ms (2.2 PFLOP/s) power-capped; without reading and adding the
+// in long runs, the 1400 W power limit: 8192 x 6144 x 7168 284 us = 2.5 PFLOP/s, 49152 rows over 48
+// experts 1.75 ms in short runs, 1.92-1.97 ms (2.2 PFLOP/s) power-capped; without reading and adding the
 // accumulators the MMAs and the operand stream alone reach 2.97 PFLOP/s.  Measured and not taken: 16
 // summing warps of 64 columns (2.60 against 2.16 ms then: their polling and spills), 128-column pair
 // tiles with four accumulators (2.15 against 1.89: 1.5 times the operand bytes from L2), polling with
-// test_wait (+4 %).
+// test_wait (+4 %), the groups' small remainders as single tiles of a second launch (-0.7 %, but up to
+// +22 % with a short reduction: the weights are read again), reads carried across blocks and scales read
+// a block ahead (the registers of the summing and of the control warps are used up; spills in either
+// cost 10-20 %).
 // Tiles run expert by expert, row tiles fastest, so the pairs running side by side share weight
 // tiles in L2.  Every wait is bounded as in gemm_pair.cu: on expiry the status word records
 // MOE_ERR_DEVICE_TIMEOUT and both CTAs drain before TMEM is freed.
