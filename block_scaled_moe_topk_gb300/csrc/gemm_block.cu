@@ -827,11 +827,13 @@ cudaError_t split_clusters(int split, int* clusters) {
 // when there are several, has k + 1 tiles or more with probability P(r > k rows) (a linear ramp here).
 double tile_time(const GemmBlockArgs& a, int rows, int64_t col_tiles, int RB, double block_us) {
   const double groups = (double)std::min<int64_t>(a.E, a.M), r = (double)a.M / groups;
-  const double width = groups > 1 ? 2.5 * std::sqrt(r) : 1e-9;
-  const double whole = std::floor(std::max(0.0, r - width) / rows);
-  double tiles = whole;
-  for (double k = whole; k * rows < r + width; k += 1)
-    tiles += k == 0 ? 1.0 : std::min(1.0, std::max(0.0, (r - k * rows) / width + 0.5));
+  double tiles = std::ceil(r / rows);
+  if (groups > 1) {
+    const double width = 2.5 * std::sqrt(r);
+    tiles = std::floor(std::max(0.0, r - width) / rows);
+    for (double k = tiles; k * rows < r + width; k += 1)
+      tiles += k == 0 ? 1.0 : std::min(1.0, std::max(0.0, (r - k * rows) / width + 0.5));
+  }
   const double rounds = tiles * groups * (double)col_tiles / (a.num_sms * 128 / rows);
   return (rounds < 8 ? std::ceil(rounds) : rounds + 0.5) * (RB * block_us + 2.0);
 }
