@@ -13,7 +13,8 @@
 // instructions.  For fp32 x a quotient within 2^-20 of a tie may take either neighbour.
 //
 // HBM-bound: 8 lanes form a block of 128 columns, 16 columns each (two 16-byte loads of 16-bit x),
-// agree on m with three shuffles, and write 16 codes a lane to each of the row's destinations.
+// agree on m with three shuffles, and write 16 codes a lane to each of the row's destinations, one
+// destination after the other.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -147,21 +148,27 @@ __global__ void __launch_bounds__(kQbThreads) quant_rows_block_kernel(const __gr
       if (r >= 0 && r < a.R) dst[j] = r;
     }
   }
+  uint4 q[U];
+  float scale[U];
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    const int g = g0 + u * tpr;
     float m = 0.0f;
 #pragma unroll
     for (int i = 0; i < 16; ++i) m = fmaxf(m, finite_abs(v[u][i]));
 #pragma unroll
-    for (int o = 4; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));  // the block's 8 lanes
+    for (int o = 4; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
     const BlockScale sc = block_scale(m);
-    const uint4 q = encode16(v[u], sc.mult);
+    q[u] = encode16(v[u], sc.mult);
+    scale[u] = sc.scale;
+  }
 #pragma unroll
-    for (int j = 0; j < kMaxTopK; ++j) {
-      if (dst[j] < 0) continue;
-      store16<VEC>(a.codes + dst[j] * K, g * 16, K, q);
-      if ((g & 7) == 0 && g * 16 < K) a.scales[dst[j] * KB + g / 8] = sc.scale;
+  for (int j = 0; j < kMaxTopK; ++j) {
+    if (dst[j] < 0) continue;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int g = g0 + u * tpr;
+      store16<VEC>(a.codes + dst[j] * K, g * 16, K, q[u]);
+      if ((g & 7) == 0 && g * 16 < K) a.scales[dst[j] * KB + g / 8] = scale[u];
     }
   }
 }
@@ -199,8 +206,8 @@ __global__ void __launch_bounds__(kQbThreads) quant_tiles_kernel(QuantBlockArgs 
   }
 }
 
-// Two column groups a thread keep more loads in flight (T = 8192, K = 7168, k = 6: 82.3 against 84.5
-// us, 0.86 of the copy rate); below four blocks of single groups an SM, spreading them over more SMs
+// Two column groups a thread keep more loads in flight (T = 8192, K = 7168, k = 6: 79.8 against 83.9
+// us, 0.89 of the copy rate); below four blocks of single groups an SM, spreading them over more SMs
 // counts more (T = 64, K = 5120: 3.8 against 3.0 us).
 constexpr int64_t kSpreadGroups = 152 * 4 * kQbThreads;
 
