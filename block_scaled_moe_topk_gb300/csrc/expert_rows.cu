@@ -91,9 +91,17 @@ __device__ __forceinline__ void load_rows(const RowsArgs& a, int64_t t, int (&r)
   }
 }
 
+// The first of a thread's U chunks, `step` apart: a warp's rounds are neighbours in the row, so that the
+// sectors that two rounds share are fetched and written while they are at hand (permute at H = 7166,
+// bf16, T = 8192, k = 6: 183 us with the rounds a block apart, 126 us so).
+template <int U>
+__device__ __forceinline__ int first_chunk(int in_row, int step) {
+  return (in_row & ~(step - 1)) * U + (in_row & (step - 1));
+}
+
 // A thread copies U chunks of a token's row to each of its k rows.  Blocks of a row are neighbours in
 // launch order: with the rows in the order of one slice after the other, H = 7167 took 220 against 180
-// us (T = 8192, k = 6, bf16; H = 7168: 125, 0.97 of the copy rate).
+// us (T = 8192, k = 6, bf16; with adjacent rounds 151, and H = 7168: 124, 0.98 of the copy rate).
 template <int VB, int U>
 __global__ void __launch_bounds__(kRowThreads) permute_kernel(const __grid_constant__ RowsParams p) {
   using V = typename Raw<VB>::T;
@@ -101,13 +109,13 @@ __global__ void __launch_bounds__(kRowThreads) permute_kernel(const __grid_const
   const int tpr = 1 << p.lg;
   const uint32_t group = blockIdx.x / (uint32_t)p.slices, slice = blockIdx.x - group * (uint32_t)p.slices;
   const int64_t t = (int64_t)group * (kRowThreads >> p.lg) + (threadIdx.x >> p.lg);
-  const int c0 = (int)slice * (tpr * U) + (threadIdx.x & (tpr - 1));
+  const int step = min(tpr, 32), c0 = (int)slice * (tpr * U) + first_chunk<U>(threadIdx.x & (tpr - 1), step);
   if (t >= a.T) return;
   const uint8_t* src = static_cast<const uint8_t*>(a.tokens_in) + t * a.token_stride * p.elem;
   V v[U];
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    const int c = c0 + u * tpr;
+    const int c = c0 + u * step;
     if (c < p.chunks) v[u] = reinterpret_cast<const V*>(src)[c];
   }
   int r[kMaxTopK];
@@ -118,7 +126,7 @@ __global__ void __launch_bounds__(kRowThreads) permute_kernel(const __grid_const
     V* dst = reinterpret_cast<V*>(static_cast<uint8_t*>(a.rows_out) + (int64_t)r[j] * a.rows_out_stride * p.elem);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int c = c0 + u * tpr;
+      const int c = c0 + u * step;
       if (c < p.chunks) dst[c] = v[u];
     }
   }
@@ -133,7 +141,7 @@ __global__ void __launch_bounds__(kRowThreads) unpermute_kernel(const __grid_con
   const RowsArgs& a = p.a;
   const int tpr = 1 << p.lg;
   const int64_t t = (int64_t)blockIdx.x * (kRowThreads >> p.lg) + (threadIdx.x >> p.lg);
-  const int c0 = blockIdx.y * (tpr * U) + (threadIdx.x & (tpr - 1));
+  const int step = min(tpr, 32), c0 = blockIdx.y * (tpr * U) + first_chunk<U>(threadIdx.x & (tpr - 1), step);
   if (t >= a.T) return;
   int r[KM];
   load_rows(a, t, r);
@@ -147,14 +155,14 @@ __global__ void __launch_bounds__(kRowThreads) unpermute_kernel(const __grid_con
     const uint8_t* src = static_cast<const uint8_t*>(a.rows_in) + (int64_t)r[j] * a.rows_in_stride * p.elem;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int c = c0 + u * tpr;
+      const int c = c0 + u * step;
       if (c < p.chunks) v[u][j].raw = __ldcs(reinterpret_cast<const typename Raw<VB>::T*>(src) + c);
     }
   }
   uint8_t* dst = static_cast<uint8_t*>(a.tokens_out) + t * a.token_stride * p.elem;
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    const int c = c0 + u * tpr;
+    const int c = c0 + u * step;
     if (c >= p.chunks) continue;
     C o;
 #pragma unroll
@@ -171,7 +179,9 @@ __global__ void __launch_bounds__(kRowThreads) unpermute_kernel(const __grid_con
 
 // The 2^LG threads of a token walk its row, U chunks at a time: every chunk of dout is read once,
 // scaled into the k rows of drows and multiplied into the k dot products, which are then summed over
-// the threads (warp shuffles, then shared memory in warp order: the same bits on every call).
+// the threads (warp shuffles, then shared memory in warp order: the same bits on every call).  Rounds
+// lie a block apart: adjacent ones leave a row's last warps without work (261 against 225 us at T = 8192,
+// H = 7168, k = 6, bf16).
 template <int DT, int VB, int LG, int U, int KM>
 __global__ void __launch_bounds__(LG > 8 ? 1 << LG : kRowThreads)
     unpermute_backward_kernel(const __grid_constant__ RowsParams p) {
