@@ -177,13 +177,23 @@ __global__ void __launch_bounds__(kRowThreads) unpermute_kernel(const __grid_con
   }
 }
 
+// Blocks of the kernel below that an SM is to hold: loads in flight carry it, and left alone it took up to
+// 98 registers a thread (T = 8192, k = 6, bf16, H = 7166: 276 against 258 us; T = 4096, k = 3, f32, H = 5120: 92
+// against 89).  Warps of their own (LG = 5) with more than four slots spill at four blocks: 54 against
+// 48 us with three at T = 16384, H = 512, k = 8, bf16, and 32 against 25 us at H = 124 left alone.
+constexpr int backward_blocks(int vb, int lg, int km) {
+  if (lg > 8) return 1;
+  if (lg == 5 && km > 4) return 3;
+  return km > 4 || vb == 2 ? 4 : 5;
+}
+
 // The 2^LG threads of a token walk its row, U chunks at a time: every chunk of dout is read once,
 // scaled into the k rows of drows and multiplied into the k dot products, which are then summed over
 // the threads (warp shuffles, then shared memory in warp order: the same bits on every call).  Rounds
 // lie a block apart: adjacent ones leave a row's last warps without work (261 against 225 us at T = 8192,
 // H = 7168, k = 6, bf16).
 template <int DT, int VB, int LG, int U, int KM>
-__global__ void __launch_bounds__(LG > 8 ? 1 << LG : kRowThreads)
+__global__ void __launch_bounds__(LG > 8 ? 1 << LG : kRowThreads, backward_blocks(VB, LG, KM))
     unpermute_backward_kernel(const __grid_constant__ RowsParams p) {
   using C = Chunk<DT, VB>;
   using V = typename Raw<VB>::T;
@@ -353,7 +363,7 @@ cudaError_t permute_vb(const RowsArgs& a, cudaStream_t s) {
 
 template <int DT, int VB, int KM>
 cudaError_t unpermute_vb(const RowsArgs& a, cudaStream_t s) {
-  constexpr int U = VB >= 8 ? 1 : 4;
+  constexpr int U = VB == 16 ? 1 : 4;
   unsigned blocks = 0;
   const RowsParams p = row_params<VB, U>(a, &blocks);
   const dim3 grid(blocks / (unsigned)p.slices, (unsigned)p.slices);
@@ -385,9 +395,15 @@ cudaError_t gather_vb(const RowsArgs& a, bool backward, cudaStream_t s) {
 
 template <int DT>
 cudaError_t gather_typed(const RowsArgs& a, bool backward, cudaStream_t s) {
+  // Rows on the 8-byte grid go in four 4-byte accesses a thread and not one of 8 bytes: T = 4096, H = 5118,
+  // f32, k = 6: unpermute 103 against 113 us, backward 174 against 207; T = 8192, H = 7164, bf16: unpermute 87
+  // against 93 us with k = 3 and 163 against 159 with k = 6, backward 255 against 328 with k = 6.  The backward
+  // of few slots is the exception: 146 with 8 bytes against 156 us with k = 3 (H = 116: 8.3 against 9.8).
   switch (access_bytes(a)) {
     case 16: return gather_vb<DT, 16>(a, backward, s);
-    case 8: return gather_vb<DT, 8>(a, backward, s);
+    case 8:
+      if (backward && a.k <= 4) return backward_vb<DT, 8, 4>(a, s);
+      return gather_vb<DT, 4>(a, backward, s);
     case 4: return gather_vb<DT, 4>(a, backward, s);
     default: return gather_vb<DT, (int)sizeof(typename Elem<DT>::T)>(a, backward, s);
   }
