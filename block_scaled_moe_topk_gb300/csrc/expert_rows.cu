@@ -134,9 +134,12 @@ __global__ void __launch_bounds__(kRowThreads) permute_kernel(const __grid_const
 
 // A thread sums U chunks over the k <= KM rows of a token (w null: plain sum).  Here the blocks of one
 // slice of all rows come first (row by row: 139 against 131 us at T = 8192, H = 7168, k = 6, bf16, 0.92
-// of the copy rate with streaming loads).  KM = 4 leaves registers for more threads an SM.
+// of the copy rate with streaming loads).  KM = 4 leaves registers for more threads an SM.  Narrow
+// accesses over more slots are held to three blocks' registers, which batches their loads: H = 7167 253 -> 230 us,
+// H = 7166 163 -> 156, H = 121 with T = 16384, k = 8 13.3 -> 11.8; the others are best left alone (H = 7168:
+// 131 against 145 us with three, k = 3 77 against 83 with four).
 template <int DT, int VB, int U, int KM>
-__global__ void __launch_bounds__(kRowThreads) unpermute_kernel(const __grid_constant__ RowsParams p) {
+__global__ void __launch_bounds__(kRowThreads, VB < 16 && KM > 4 ? 3 : 0) unpermute_kernel(const __grid_constant__ RowsParams p) {
   using C = Chunk<DT, VB>;
   const RowsArgs& a = p.a;
   const int tpr = 1 << p.lg;
@@ -182,7 +185,7 @@ __global__ void __launch_bounds__(kRowThreads) unpermute_kernel(const __grid_con
 // against 89).  Warps of their own (LG = 5) with more than four slots spill at four blocks: 54 against
 // 48 us with three at T = 16384, H = 512, k = 8, bf16, and 32 against 25 us at H = 124 left alone.
 constexpr int backward_blocks(int vb, int lg, int km) {
-  if (lg > 8) return 1;
+  if (lg > 8) return 0;
   if (lg == 5 && km > 4) return 3;
   return km > 4 || vb == 2 ? 4 : 5;
 }
