@@ -48,6 +48,7 @@
 #include <algorithm>
 #include <atomic>
 #include <cmath>
+#include <type_traits>
 
 #include "gemm_block_common.cuh"
 #include "gemm_common.cuh"
@@ -60,29 +61,45 @@ constexpr int kBFirstEpiWarp = 4;
 constexpr int kBEpiWarps = 8;
 constexpr int kBTileCols = 256;                     // output columns of a tile
 constexpr int kBHalfBytes = 128 * 128;              // 128 rows of x, or 128 of the tile's weight rows
-constexpr int kBRingBytes = 6 * 2 * kBHalfBytes;    // 192 KiB: 6 stages of a pair's CTA, 4 of a single CTA
-constexpr int kBMaxStages = 6;
+constexpr int kBStages = 4;                         // 48 KiB each on a single CTA, 32 KiB in a pair's
 constexpr int kBMaxSplit = 8;
-constexpr int kBOutOff = kBRingBytes;   // per-warp staging of unaligned output rows
-constexpr int kBOutBytes = 32 * 64;                 // 32 rows x 64 bytes
 constexpr int kBScaleBlocks = 8;                    // reduction blocks of one scale chunk
 constexpr int kBScaleRows = 130;                    // 128 rows of x, then the weights' two column halves
-constexpr int kBScaleOff = kBOutOff + kBEpiWarps * kBOutBytes;  // two chunks [block][row], fp32 (and a tile)
+constexpr int kBScaleOff = 208 * 1024;              // two chunks [block][row], fp32 (and a tile)
 constexpr int kBScaleTile = kBScaleBlocks * kBScaleRows;  // then, with a tile's first chunk, the tile itself
 constexpr int kBScaleBytes = (kBScaleTile + 4) * 4;
 constexpr int kBBarOff = kBScaleOff + 2 * kBScaleBytes;
 constexpr int kBTabOff = kBBarOff + 256;            // per expert: first row, first tile
 constexpr int kBSmemBytes = kBTabOff + 2 * 4 * (kMaxExperts + 1) + 1024;
 static_assert(kBSmemBytes <= 232448, "block GEMM shared memory");
-static_assert(kBBarOff % 8 == 0 && 8 * (2 * kBMaxStages + 14) + 8 <= 256, "block GEMM barriers");
+static_assert(kBBarOff % 8 == 0 && 8 * (2 * kBStages + 14) + 8 <= 256, "block GEMM barriers");
+
+struct BlockParams {  // 64-byte aligned through its CUtensorMap members
+  CUtensorMap tmap_x;  // codes [M, reduction], box 128 B x 128 rows
+  CUtensorMap tmap_x32;  // the same, 32 rows
+  CUtensorMap tmap_w;  // codes [E, N, K], box 128 B x 128 rows x 1
+  GemmBlockArgs a;
+  int out_vec;         // output rows start on 32-byte boundaries
+  int split;           // SPLIT: CTAs that share the reduction of a tile
+};
+struct PairParams : BlockParams {
+  CUtensorMap tmap_out;  // output, box 128 B x 32 rows
+  int out_tma;           // output rows start on 16-byte boundaries
+};
 
 // One CTA (G = 1) or a pair (G = 2) works on a tile of 128 G rows by 256 columns; a CTA stages its 128
 // rows of x and 256 / G of the weight rows.
 template <int G>
 struct BlockGeo {
+  using Params = std::conditional_t<G == 2, PairParams, BlockParams>;
   static constexpr int kRows = 128 * G;
   static constexpr int kStageBytes = (1 + 2 / G) * kBHalfBytes;
-  static constexpr int kStages = kBRingBytes / kStageBytes;
+  // Behind the stages, a summing warp's staging of 32 output rows: a pair's hold 256 bytes of each, in
+  // two boxes of TMA stores, a single CTA's 64 bytes, for the ends of rows.  (A pair with six
+  // stages and the smaller staging is no faster for long reductions either.)
+  static constexpr int kOutOff = kBStages * kStageBytes;
+  static constexpr int kOutPitch = G == 2 ? 256 : 64;
+  static_assert(kOutOff + kBEpiWarps * 32 * kOutPitch <= kBScaleOff, "stages and staging");
   // A pair runs a block's MMAs as two halves of 128 columns with accumulators of their own, so that a
   // half's sums need not wait for the other half's MMAs; a CTA then holds 64 weight rows of each half.
   // (A single CTA would read its x tile twice for that, and shared memory's bandwidth bounds it.)
@@ -95,15 +112,6 @@ struct BlockGeo {
   // registers a thread of the control and the summing warpgroups: the block starts with 168 each
   static constexpr int kCtlRegs = G == 2 ? 72 : 104, kSumRegs = G == 2 ? 216 : 200;
   static_assert(128 * kCtlRegs + 256 * kSumRegs <= kBThreads * 168, "register split");
-};
-
-struct BlockParams {  // 64-byte aligned through its CUtensorMap members
-  CUtensorMap tmap_x;  // codes [M, reduction], box 128 B x 128 rows
-  CUtensorMap tmap_x32;  // the same, 32 rows
-  CUtensorMap tmap_w;  // codes [E, N, K], box 128 B x 128 rows x 1
-  GemmBlockArgs a;
-  int out_vec;         // output rows start on 32-byte boundaries
-  int split;           // SPLIT: CTAs that share the reduction of a tile
 };
 
 // Instruction descriptor of kind::f8f6f4: fp32 accumulator (bit 4), E4M3 operands, B read along its
@@ -212,9 +220,10 @@ __device__ __forceinline__ void load_rows_x(const BlockParams& p, uint32_t dst, 
 }
 
 template <int G, bool DGRAD, bool SPLIT>
-__global__ void __launch_bounds__(kBThreads, 1) gemm_block_kernel(const __grid_constant__ BlockParams p) {
+__global__ void __launch_bounds__(kBThreads, 1)
+    gemm_block_kernel(const __grid_constant__ typename BlockGeo<G>::Params p) {
   static_assert(G == 1 || !SPLIT, "split tiles run on single CTAs");
-  constexpr int kStages = BlockGeo<G>::kStages, kStageBytes = BlockGeo<G>::kStageBytes, kRows = BlockGeo<G>::kRows;
+  constexpr int kStages = kBStages, kStageBytes = BlockGeo<G>::kStageBytes, kRows = BlockGeo<G>::kRows;
   constexpr int kHalves = BlockGeo<G>::kHalves, kWRows = BlockGeo<G>::kWRows;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -544,6 +553,61 @@ __global__ void __launch_bounds__(kBThreads, 1) gemm_block_kernel(const __grid_c
       }
       if (!ok || !any) continue;
       const int dt = a.out_dtype;
+      if constexpr (G == 2) {
+        if (p.out_tma && rows_here >= 32) {
+          // 128 bytes of the 32 rows at a time as a swizzled box, left to a TMA store that runs under
+          // the next tile's sums and clips the columns past the last one.  Stores by the lanes, as
+          // below, hold the warps up for ~2.4 us a tile: 49152 rows over 48 experts, N = 7168, K = 2048
+          // 697 against 627 us, N = 6144, K = 7168 1760 against 1690; a bulk copy of each lane's row 690.
+          uint8_t* out_stage = smem + BlockGeo<G>::kOutOff + (warp - kBFirstEpiWarp) * 32 * BlockGeo<G>::kOutPitch;
+          auto box = [&](int c, int slot) {  // columns c... of the warp's 128
+            uint8_t* brow = out_stage + slot * 4096 + lane * 128;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              uint4 w;
+              if (dt == kDtF32)
+                w = make_uint4(__float_as_uint(acc[(c + 4 * i) & 127]), __float_as_uint(acc[(c + 4 * i + 1) & 127]),
+                               __float_as_uint(acc[(c + 4 * i + 2) & 127]), __float_as_uint(acc[(c + 4 * i + 3) & 127]));
+              else
+                w = make_uint4(out_pair(acc[(c + 8 * i) & 127], acc[(c + 8 * i + 1) & 127], dt),
+                               out_pair(acc[(c + 8 * i + 2) & 127], acc[(c + 8 * i + 3) & 127], dt),
+                               out_pair(acc[(c + 8 * i + 4) & 127], acc[(c + 8 * i + 5) & 127], dt),
+                               out_pair(acc[(c + 8 * i + 6) & 127], acc[(c + 8 * i + 7) & 127], dt));
+              *reinterpret_cast<uint4*>(brow + ((i ^ (lane & 7)) << 4)) = w;
+            }
+          };
+          auto send = [&](int c, int width) {  // both boxes, `width` columns each
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+#pragma unroll
+              for (int q = 0; q < 2; ++q)
+                if (col0 + c + q * width < cols)
+                  tma_store_2d(&p.tmap_out, smem_u32(out_stage) + q * 4096, col0 + c + q * width, (int)row);
+              bulk_commit_group();
+            }
+          };
+          auto reuse = [&] {  // the last stores have read the staging
+            if (lane == 0) bulk_wait_read_all();
+            __syncwarp();
+          };
+          reuse();
+          if (dt == kDtF32) {
+            box(0, 0);
+            box(32, 1);
+            send(0, 32);
+            reuse();
+            box(64, 0);
+            box(96, 1);
+            send(64, 32);
+          } else {
+            box(0, 0);
+            box(64, 1);
+            send(0, 64);
+          }
+          continue;
+        }
+      }
       if (SPLIT) {
         // this CTA's partial sums, [row][column] in the ring (every stage has been consumed: the last
         // accumulator is complete), 16-byte chunks of a row swizzled by the row
@@ -592,7 +656,9 @@ __global__ void __launch_bounds__(kBThreads, 1) gemm_block_kernel(const __grid_c
         // The last columns: 64 bytes of every row at a time through the warp's staging buffer (words
         // swizzled by the row: conflict-free both ways), then consecutive elements of a row by
         // consecutive lanes
-        uint32_t* stage = reinterpret_cast<uint32_t*>(smem + kBOutOff + (warp - kBFirstEpiWarp) * kBOutBytes);
+        uint32_t* stage = reinterpret_cast<uint32_t*>(smem + BlockGeo<G>::kOutOff +
+                                                      (warp - kBFirstEpiWarp) * 32 * BlockGeo<G>::kOutPitch);
+        if (G == 2 && lane == 0) bulk_wait_read_all();
         const int64_t row0 = row - lane;
         const int swz = (lane >> 1) & 15;
         if (dt == kDtF32) {
@@ -641,6 +707,7 @@ __global__ void __launch_bounds__(kBThreads, 1) gemm_block_kernel(const __grid_c
         }
       }
     }
+    if (G == 2) bulk_wait_all();  // the staging must outlive the copies
   }
 
   tc_fence_before();
@@ -725,6 +792,22 @@ bool encode_codes(CUtensorMap* m, const uint8_t* base, int rank, const cuuint64_
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Output rows start on the powers of two that divide this.
+uint64_t out_grid(const GemmBlockArgs& a, int64_t cols) {
+  return reinterpret_cast<uintptr_t>(a.out) | (uint64_t)(cols * dtype_bytes(a.out_dtype));
+}
+
+bool encode_out(CUtensorMap* m, const GemmBlockArgs& a, int64_t cols) {
+  EncodeTiledFn encode = get_encode_fn();
+  if (!encode) return false;
+  const int es = dtype_bytes(a.out_dtype);
+  const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)a.M}, strides[1] = {(cuuint64_t)(cols * es)};
+  const cuuint32_t box[2] = {(cuuint32_t)(128 / es), 32}, steps[2] = {1, 1};
+  return encode(m, es == 4 ? CU_TENSOR_MAP_DATA_TYPE_UINT32 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, a.out, dims, strides,
+                box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // Row tiles of 128 G rows: every group adds at most one partial tile.
 int64_t max_row_tiles(const GemmBlockArgs& a, int rows) {
   const int64_t groups = std::min<int64_t>(a.E, a.M);
@@ -744,7 +827,7 @@ cudaError_t launch_tiles(const GemmBlockArgs& a, int64_t tiles, int split, cudaS
     if (err != cudaSuccess) return err;
     ready[dev].store(1, std::memory_order_release);
   }
-  BlockParams p;
+  typename BlockGeo<G>::Params p;
   const cuuint64_t red = (cuuint64_t)(DGRAD ? a.N : a.K);
   const cuuint64_t xd[2] = {red, (cuuint64_t)a.M}, xst[1] = {red};
   const cuuint64_t wd[3] = {(cuuint64_t)a.K, (cuuint64_t)a.N, (cuuint64_t)a.E};
@@ -755,7 +838,11 @@ cudaError_t launch_tiles(const GemmBlockArgs& a, int64_t tiles, int split, cudaS
     return cudaErrorInvalidValue;
   p.a = a;
   const int64_t cols = DGRAD ? a.K : a.N;
-  p.out_vec = reinterpret_cast<uintptr_t>(a.out) % 32 == 0 && (cols * dtype_bytes(a.out_dtype)) % 32 == 0;
+  p.out_vec = out_grid(a, cols) % 32 == 0;
+  if constexpr (G == 2) {
+    p.out_tma = out_grid(a, cols) % 16 == 0;
+    if (p.out_tma && !encode_out(&p.tmap_out, a, cols)) return cudaErrorInvalidValue;
+  }
   p.split = split;
   const int ctas = SPLIT ? split : G;  // of a tile
   cudaLaunchConfig_t cfg = {};
@@ -816,16 +903,18 @@ cudaError_t split_clusters(int split, int* clusters) {
 // against 1: 8 rows 10.1 against 22.7 us, 64 rows 11.6 against 23.7, 128 rows 14.2 against 24.7; K = 512:
 // 8 rows 8.3 against 6.6, 128 rows 13.4 against 8.2 (not split).
 //
-// Single CTAs or pairs: the smaller estimate of tile_time.  A pair's tile is cheaper a row (0.49
-// against 2 x 0.56 us a block for 256 rows), a single's wastes fewer rows in a group's last tile.  48
-// experts, N = 6144, K = 7168, rows a group: single / pair us
-//   64: 345 / 411    128: 488 / 434    192: 547 / 449    256: 619 / 668    320: 742 / 846
-//   384: 886 / 845    512: 1112 / 1027    768: 1578 / 1533    1024: 2076 / 1906
-// one expert x 1024 rows 66 / 57, x 8192 333 / 288; 8 experts, N = 2048, K = 1024 x 512 rows 17.7 / 24.6.
+// Single CTAs or pairs: the smaller estimate of tile_time.  A pair's tile is cheaper a row (0.47
+// against 2 x 0.54 us a block for 256 rows, and its TMA stores leave 1.6 us a tile between the last sums and
+// the next tile's against 2.6), a single's wastes fewer rows in a group's last tile.  48 experts, N =
+// 6144, K = 7168, rows a group: single / pair us
+//   64: 345 / 411    128: 483 / 429    192: 532 / 441    256: 591 / 589    320: 712 / 807
+//   384: 888 / 795    512: 1046 / 926    768: 1528 / 1441    1024: 1980 / 1760
+// 48 experts x 1024 rows, N = 7168, K = 512 344 / 243, K = 256 251 / 202; one expert x 1024 rows, N = 6144, K =
+// 7168 64 / 61; 8 experts, N = 2048, K = 1024 x 512 rows 17.6 / 22.8.
 //
 // Estimated time (us) of the product in row tiles of `rows` rows: a group of r rows, spread by sqrt(r)
 // when there are several, has k + 1 tiles or more with probability P(r > k rows) (a linear ramp here).
-double tile_time(const GemmBlockArgs& a, int rows, int64_t col_tiles, int RB, double block_us) {
+double tile_time(const GemmBlockArgs& a, int rows, int64_t col_tiles, int RB, double block_us, double rest_us) {
   const double groups = (double)std::min<int64_t>(a.E, a.M), r = (double)a.M / groups;
   double tiles = std::ceil(r / rows);
   if (groups > 1) {
@@ -835,7 +924,7 @@ double tile_time(const GemmBlockArgs& a, int rows, int64_t col_tiles, int RB, do
       tiles += k == 0 ? 1.0 : std::min(1.0, std::max(0.0, (r - k * rows) / width + 0.5));
   }
   const double rounds = tiles * groups * (double)col_tiles / (a.num_sms * 128 / rows);
-  return (rounds < 8 ? std::ceil(rounds) : rounds + 0.5) * (RB * block_us + 2.0);
+  return (rounds < 8 ? std::ceil(rounds) : rounds + 0.5) * (RB * block_us + rest_us);
 }
 
 template <bool DGRAD>
@@ -856,7 +945,9 @@ cudaError_t launch_direction(const GemmBlockArgs& a, cudaStream_t s) {
     if (singles <= clusters) break;
   }
   if (split > 1) return launch_tiles<1, DGRAD, true>(a, singles, split, s);
-  if (tile_time(a, 128, col_tiles, RB, 0.56) <= tile_time(a, 256, col_tiles, RB, 0.49) + 2.0)  // pairs start 2 us later
+  const bool tma_rows = out_grid(a, cols) % 16 == 0;
+  if (tile_time(a, 128, col_tiles, RB, 0.54, 2.6) <=
+      tile_time(a, 256, col_tiles, RB, 0.47, tma_rows ? 1.6 : 2.6) + 2.0)  // pairs start 2 us later
     return launch_tiles<1, DGRAD, false>(a, singles, 1, s);
   return launch_tiles<2, DGRAD, false>(a, max_row_tiles(a, BlockGeo<2>::kRows) * col_tiles, 1, s);
 }

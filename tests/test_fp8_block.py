@@ -268,6 +268,15 @@ def test_grouped_dgrad(counts, N, K):
 
 
 @gpu
+@pytest.mark.parametrize("N,K,dgrad", [(328, 256, False), (329, 256, False), (264, 400, False), (272, 336, True)])
+@pytest.mark.parametrize("out_dtype", DTYPES)
+def test_many_rows(N, K, dgrad, out_dtype):
+    """Full and ragged tiles of 256 rows side by side, columns past the last whole tile, rows on and off 16 bytes."""
+    counts = [9000, 0, 15, 12345, 33]
+    check_product(sum(counts) + 2, N, K, counts, out_dtype, dgrad=dgrad, seed=N)
+
+
+@gpu
 def test_no_rows():
     w, ws = make_weights(3, 64, 128, 0)
     for off in (torch.zeros(4, dtype=torch.int64), torch.tensor([0, 0, 4, 4])):
