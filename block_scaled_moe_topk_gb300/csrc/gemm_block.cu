@@ -22,7 +22,7 @@
 //              a row.  A thread of the summing warps loading its own row's scale instead touches 32
 //              lines an instruction, in competition with the operands for the shared-memory pipe
 //              (49152 rows over 48 experts, N = 6144, K = 7168: 2.51 against 2.16 ms)
-//   warps 4-11 sums: a thread owns one row and 128 of the 256 columns (one scale block) in 128 fp32
+//   warps 4-11 sums (and the output): a thread owns one row and 128 of the 256 columns (one scale block) in 128 fp32
 //              registers; warps whose 32 rows are past the group's end read nothing.  The two
 //              warpgroups take 216 (200) registers a thread of the control warps' (setmaxnreg)
 // Groups of few rows run the same kernel on single CTAs (G = 1: 128 x 256 tiles, 48 KiB stages), and
@@ -31,8 +31,8 @@
 // What bounds it (one GB300, device times): with few rows the weight stream (64 tokens x 6 over 384
 // experts of N = 1280, K = 5120: 245 us, 0.96 of the copy rate; gradient of 12288 rows over 128 experts of N =
 // 2304, K = 5120: 262 us, 0.93).  With many, the round trip of an accumulator (MMAs, read, release) and,
-// in long runs, the 1400 W power limit: 8192 x 6144 x 7168 284 us = 2.5 PFLOP/s, 49152 rows over 48
-// experts 1.75 ms in short runs, 1.92-1.97 ms (2.2 PFLOP/s) power-capped; without reading and adding the
+// in long runs, the 1400 W power limit: 8192 x 6144 x 7168 281 us = 2.57 PFLOP/s, 49152 rows over 48
+// experts 1.64-1.74 ms in short runs, 1.87-1.96 ms (2.2-2.3 PFLOP/s) power-capped; without reading and adding the
 // accumulators the MMAs and the operand stream alone reach 2.97 PFLOP/s.  Measured and not taken: 16
 // summing warps of 64 columns (2.60 against 2.16 ms then: their polling and spills), 128-column pair
 // tiles with four accumulators (2.15 against 1.89: 1.5 times the operand bytes from L2), polling with
@@ -98,8 +98,8 @@ struct BlockGeo {
   // two boxes of TMA stores, a single CTA's 64 bytes, for the ends of rows.  (A pair with six
   // stages and the smaller staging is no faster for long reductions either.)
   static constexpr int kOutOff = kBStages * kStageBytes;
-  static constexpr int kOutPitch = G == 2 ? 256 : 64;
-  static_assert(kOutOff + kBEpiWarps * 32 * kOutPitch <= kBScaleOff, "stages and staging");
+  static constexpr int kOutBytes = G == 2 ? 32 * 256 : 32 * 64;
+  static_assert(kOutOff + kBEpiWarps * kOutBytes <= kBScaleOff, "stages and staging");
   // A pair runs a block's MMAs as two halves of 128 columns with accumulators of their own, so that a
   // half's sums need not wait for the other half's MMAs; a CTA then holds 64 weight rows of each half.
   // (A single CTA would read its x tile twice for that, and shared memory's bandwidth bounds it.)
@@ -559,7 +559,7 @@ __global__ void __launch_bounds__(kBThreads, 1)
           // the next tile's sums and clips the columns past the last one.  Stores by the lanes, as
           // below, hold the warps up for ~2.4 us a tile: 49152 rows over 48 experts, N = 7168, K = 2048
           // 697 against 627 us, N = 6144, K = 7168 1760 against 1690; a bulk copy of each lane's row 690.
-          uint8_t* out_stage = smem + BlockGeo<G>::kOutOff + (warp - kBFirstEpiWarp) * 32 * BlockGeo<G>::kOutPitch;
+          uint8_t* out_stage = smem + BlockGeo<G>::kOutOff + (warp - kBFirstEpiWarp) * BlockGeo<G>::kOutBytes;
           auto box = [&](int c, int slot) {  // columns c... of the warp's 128
             uint8_t* brow = out_stage + slot * 4096 + lane * 128;
 #pragma unroll
@@ -620,8 +620,8 @@ __global__ void __launch_bounds__(kBThreads, 1)
         }
       } else if (col0 + 128 <= cols) {
         // Every lane stores its own row, whole 32-byte sectors but for the ends of unaligned rows (17535
-        // rows of 13 experts, K = 1136: N = 2681 101 us, 2688 90 us; by consecutive lanes through a
-        // staging buffer, as the last columns below, 107)
+        // rows of 13 experts, K = 1136, N = 2681: 101 us; by consecutive lanes through a staging buffer, as
+        // the last columns below, 107; N = 2688 90, and 74 by the TMA stores above)
         if (p.out_vec) {
           uint8_t* dst = static_cast<uint8_t*>(a.out) + (row * cols + col0) * (dt == kDtF32 ? 4 : 2);
           if (dt == kDtF32) {
@@ -657,7 +657,7 @@ __global__ void __launch_bounds__(kBThreads, 1)
         // swizzled by the row: conflict-free both ways), then consecutive elements of a row by
         // consecutive lanes
         uint32_t* stage = reinterpret_cast<uint32_t*>(smem + BlockGeo<G>::kOutOff +
-                                                      (warp - kBFirstEpiWarp) * 32 * BlockGeo<G>::kOutPitch);
+                                                      (warp - kBFirstEpiWarp) * BlockGeo<G>::kOutBytes);
         if (G == 2 && lane == 0) bulk_wait_read_all();
         const int64_t row0 = row - lane;
         const int swz = (lane >> 1) & 15;
