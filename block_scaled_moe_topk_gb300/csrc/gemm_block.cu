@@ -607,6 +607,69 @@ __global__ void __launch_bounds__(kBThreads, 1)
           }
           continue;
         }
+        if (!p.out_vec && col0 + 128 <= cols) {
+          // Rows off the 32-byte boundaries: 64 words of every row through the staging, then a row at a time
+          // by all lanes.  A 16-bit row at an odd element goes to the staging shifted by one, so that its
+          // words lie on memory's; the two elements at its ends are stored by themselves.  (29 experts x 910
+          // rows, N = 3311, K = 4048: 336 us, and 344 with every lane storing its own row as single CTAs do;
+          // N = 7167, K = 2048, 48 x 1024 rows: 738 and 764)
+          uint32_t* stage = reinterpret_cast<uint32_t*>(smem + BlockGeo<G>::kOutOff +
+                                                        (warp - kBFirstEpiWarp) * BlockGeo<G>::kOutBytes);
+          const int es = dt == kDtF32 ? 4 : 2, nr = min(32, rows_here);
+          const int64_t pitch = (int64_t)cols * es;
+          uint8_t* dst0 = static_cast<uint8_t*>(a.out) + (row - lane) * pitch + (int64_t)col0 * es;
+          auto put = [&](const uint32_t(&w)[64]) {
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              *reinterpret_cast<uint4*>(stage + lane * 64 + ((i ^ (lane & 7)) << 2)) =
+                  make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+            __syncwarp();
+          };
+          auto rows_out = [&](uint8_t* dst) {
+#pragma unroll 1
+            for (int r0 = 0; r0 < nr; r0 += 8) {
+              uint32_t v[8][2];
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) v[i][h] = stage[(r0 + i) * 64 + ((((lane >> 2) + 8 * h) ^ i) << 2) + (lane & 3)];
+#pragma unroll
+              for (int i = 0; i < 8; ++i, dst += pitch) {
+                if (r0 + i >= nr) break;
+                const int odd = (int)(reinterpret_cast<uintptr_t>(dst) & 2);
+                uint32_t* d = reinterpret_cast<uint32_t*>(dst + odd) + lane;
+                d[0] = v[i][0];
+                if (odd == 0 || lane < 31) d[32] = v[i][1];
+              }
+            }
+          };
+          if (lane == 0) bulk_wait_read_all();
+          uint32_t w[64];
+          if (dt == kDtF32) {
+#pragma unroll
+            for (int c = 0; c < 128; c += 64) {
+#pragma unroll
+              for (int i = 0; i < 64; ++i) w[i] = __float_as_uint(acc[c + i]);
+              put(w);
+              rows_out(dst0 + 4 * c);
+            }
+          } else {
+#pragma unroll
+            for (int i = 0; i < 64; ++i) w[i] = out_pair(acc[2 * i], acc[2 * i + 1], dt);
+            uint8_t* mine_dst = dst0 + lane * pitch;
+            const uint32_t odd = (uint32_t)(reinterpret_cast<uintptr_t>(mine_dst) & 2);
+            if (odd != 0 && valid) {
+              *reinterpret_cast<uint16_t*>(mine_dst) = (uint16_t)w[0];
+              *reinterpret_cast<uint16_t*>(mine_dst + 254) = (uint16_t)(w[63] >> 16);
+            }
+#pragma unroll
+            for (int i = 0; i < 64; ++i) w[i] = __funnelshift_r(w[i], i < 63 ? w[i + 1] : 0u, 8 * odd);
+            put(w);
+            rows_out(dst0);
+          }
+          continue;
+        }
       }
       if (SPLIT) {
         // this CTA's partial sums, [row][column] in the ring (every stage has been consumed: the last
@@ -619,9 +682,9 @@ __global__ void __launch_bounds__(kBThreads, 1)
                 make_float4(acc[4 * i], acc[4 * i + 1], acc[4 * i + 2], acc[4 * i + 3]);
         }
       } else if (col0 + 128 <= cols) {
-        // Every lane stores its own row, whole 32-byte sectors but for the ends of unaligned rows (17535
-        // rows of 13 experts, K = 1136, N = 2681: 101 us; by consecutive lanes through a staging buffer, as
-        // the last columns below, 107; N = 2688 90, and 74 by the TMA stores above)
+        // Every lane stores its own row, whole 32-byte sectors but for the ends of a single CTA's unaligned
+        // rows (17535 rows of 13 experts, N = 2681, K = 1136: 97 us; element by element through a small
+        // staging buffer, as the last columns below, took 6 % longer)
         if (p.out_vec) {
           uint8_t* dst = static_cast<uint8_t*>(a.out) + (row * cols + col0) * (dt == kDtF32 ? 4 : 2);
           if (dt == kDtF32) {
@@ -641,12 +704,12 @@ __global__ void __launch_bounds__(kBThreads, 1)
               if (valid) st_global_v8(dst + 2 * i, w);
             }
           }
-        } else if (dt == kDtF32) {
+        } else if (G == 1 && dt == kDtF32) {
           uint32_t w[128];
 #pragma unroll
           for (int i = 0; i < 128; ++i) w[i] = __float_as_uint(acc[i]);
           store_words<128>(static_cast<uint8_t*>(a.out) + (row * cols + col0) * 4, w, valid);
-        } else {
+        } else if (G == 1) {
           uint32_t w[64];
 #pragma unroll
           for (int i = 0; i < 64; ++i) w[i] = out_pair(acc[2 * i], acc[2 * i + 1], dt);
@@ -910,7 +973,9 @@ cudaError_t split_clusters(int split, int* clusters) {
 //   64: 345 / 411    128: 483 / 429    192: 532 / 441    256: 591 / 589    320: 712 / 807
 //   384: 888 / 795    512: 1046 / 926    768: 1528 / 1441    1024: 1980 / 1760
 // 48 experts x 1024 rows, N = 7168, K = 512 344 / 243, K = 256 251 / 202; one expert x 1024 rows, N = 6144, K =
-// 7168 64 / 61; 8 experts, N = 2048, K = 1024 x 512 rows 17.6 / 22.8.
+// 7168 64 / 61; 8 experts, N = 2048, K = 1024 x 512 rows 17.6 / 22.8.  Rows off the boundaries of the wide
+// stores take 3.6 and 3.1 us a tile instead: 13 experts x 1349 rows, N = 2681, K = 1136 96.6 / 91.6; 48 x 384, N =
+// 6143, K = 7168 890 / 810; 8 x 512, N = 2041, K = 1024 21.8 / 26.0; 48 x 1024, N = 7167, K = 256 316 / 323.
 //
 // Estimated time (us) of the product in row tiles of `rows` rows: a group of r rows, spread by sqrt(r)
 // when there are several, has k + 1 tiles or more with probability P(r > k rows) (a linear ramp here).
@@ -945,9 +1010,9 @@ cudaError_t launch_direction(const GemmBlockArgs& a, cudaStream_t s) {
     if (singles <= clusters) break;
   }
   if (split > 1) return launch_tiles<1, DGRAD, true>(a, singles, split, s);
-  const bool tma_rows = out_grid(a, cols) % 16 == 0;
-  if (tile_time(a, 128, col_tiles, RB, 0.54, 2.6) <=
-      tile_time(a, 256, col_tiles, RB, 0.47, tma_rows ? 1.6 : 2.6) + 2.0)  // pairs start 2 us later
+  const uint64_t grid = out_grid(a, cols);
+  if (tile_time(a, 128, col_tiles, RB, 0.54, grid % 32 == 0 ? 2.6 : 3.6) <=
+      tile_time(a, 256, col_tiles, RB, 0.47, grid % 16 == 0 ? 1.6 : 3.1) + 2.0)  // pairs start 2 us later
     return launch_tiles<1, DGRAD, false>(a, singles, 1, s);
   return launch_tiles<2, DGRAD, false>(a, max_row_tiles(a, BlockGeo<2>::kRows) * col_tiles, 1, s);
 }
