@@ -139,7 +139,8 @@ __global__ void __launch_bounds__(kRowThreads) permute_kernel(const __grid_const
 // H = 7166 163 -> 156, H = 121 with T = 16384, k = 8 13.3 -> 11.8; the others are best left alone (H = 7168:
 // 131 against 145 us with three, k = 3 77 against 83 with four).
 template <int DT, int VB, int U, int KM>
-__global__ void __launch_bounds__(kRowThreads, VB < 16 && KM > 4 ? 3 : 0) unpermute_kernel(const __grid_constant__ RowsParams p) {
+__global__ void __launch_bounds__(kRowThreads, VB < 16 && KM > 4 ? 3 : 0)
+    unpermute_kernel(const __grid_constant__ RowsParams p) {
   using C = Chunk<DT, VB>;
   const RowsArgs& a = p.a;
   const int tpr = 1 << p.lg;
