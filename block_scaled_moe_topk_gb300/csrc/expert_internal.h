@@ -78,6 +78,10 @@ struct GemmBlockArgs {
   int test_stall;
 };
 cudaError_t launch_gemm_block(const GemmBlockArgs& a, cudaStream_t s);
+// What ran is left in status word 7 (the other words start at 0): the choice between the forms is an
+// estimate, and a test or a timing that means one of them can see that it got it.
+constexpr int kFormWord = 7;
+enum : uint32_t { kFormVector = 1, kFormSingle = 2, kFormPair = 3, kFormSplit = 4 };
 // gemv_block.cu: the forward product of a few rows, and whether a product is one.
 bool use_gemv(const GemmBlockArgs& a);
 cudaError_t launch_gemv_block(const GemmBlockArgs& a, cudaStream_t s);

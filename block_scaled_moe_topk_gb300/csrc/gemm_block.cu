@@ -248,7 +248,8 @@ __global__ void __launch_bounds__(kBThreads, 1)
   const bool leader = rank == 0;
   const int E = a.E;
 
-  if (blockIdx.x == 0 && threadIdx.x < 8) a.status[threadIdx.x] = 0;
+  if (blockIdx.x == 0 && threadIdx.x < 8)
+    a.status[threadIdx.x] = threadIdx.x == kFormWord ? (G == 2 ? kFormPair : SPLIT ? kFormSplit : kFormSingle) : 0;
   for (int e = threadIdx.x; e <= E; e += kBThreads) row_begin[e] = (int32_t)group_start(a.offsets, e, a.M);
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {

@@ -516,7 +516,9 @@ moe_status_t moe_permute_quantize_fp8_block(const void* x, int64_t x_stride, moe
  *   out      [M, N] BF16, F16 or F32
  *   K % 16 == 0, E <= 1024; N and M are any
  *   workspace  device, 256-byte aligned, >= moe_gemm_fp8_block_workspace_bytes(M, N, K, E); holds the
- *            status words read by moe_read_device_status, reset by every call with M > 0
+ *            status words read by moe_read_device_status, reset by every call with M > 0; uint32 word 7
+ *            says how the product ran: 1 vector form, 2 tiles on single CTAs, 3 tiles on CTA pairs,
+ *            4 tiles with the reduction split over a cluster
  */
 size_t moe_gemm_fp8_block_workspace_bytes(int64_t M, int N, int K, int E);
 moe_status_t moe_gemm_fp8_block(const uint8_t* x, const float* x_scale, const uint8_t* w, const float* w_scale,

@@ -1,0 +1,74 @@
+"""The forms of the FP8 product (vector, single CTAs, CTA pairs, split reduction), each on the groups, widths and
+contents where it can go wrong.  The library chooses a form by an estimated time and leaves it in word 7 of
+the workspace; a test that means one form grows its problem until that form runs, or fails.
+
+Against fp64 on the GPU with the bound of test_fp8_block.py: u |ref| + (blocks + 16) 2^-22 sum |terms|.
+"""
+import pytest
+import torch
+
+import block_scaled_moe_topk_gb300 as moe
+from test_fp8_block import DTYPES, NAN_CODES, SMALLEST, U, ceil_div, make_rows, make_weights, offsets_of, workspace
+
+pytestmark = pytest.mark.gpu
+VECTOR, SINGLE, PAIR, SPLIT = 1, 2, 3, 4
+
+
+def values(codes, scales, block_rows):
+    rows, K = codes.shape
+    s = scales.double().repeat_interleave(block_rows, 0)[:rows].repeat_interleave(128, 1)[:, :K]
+    return codes.view(torch.float8_e4m3fn).double() * s
+
+
+def product(x, xs, w, ws, offsets, out_dtype, dgrad=False):
+    """The product of GPU tensors and the form that ran."""
+    E, N, K = w.shape
+    M = x.shape[0]
+    out = torch.full((M, K if dgrad else N), -77.0, dtype=out_dtype, device="cuda")
+    space = workspace(M, N, K, E)
+    call = moe.moe_gemm_fp8_block_dgrad if dgrad else moe.moe_gemm_fp8_block
+    call(x, xs, w, ws, out, space, offsets=offsets)
+    assert moe.moe_read_device_status(space) == 0
+    return out, int(space.view(torch.int32)[7])
+
+
+def problem(M, N, K, E, dgrad, seed):
+    w, ws = make_weights(E, N, K, seed)
+    x, xs = make_rows(M, N if dgrad else K, seed + 10)
+    return [t.cuda() for t in (x, xs, w, ws)]
+
+
+def check(args, out, counts, out_dtype, dgrad):
+    x, xs, w, ws = args
+    off = offsets_of(counts).tolist()
+    X, red = values(x, xs, 1), x.shape[1]
+    for e in range(len(counts)):
+        a, b = off[e], off[e + 1]
+        if a == b:
+            continue
+        W = values(w[e], ws[e], 128)
+        B = W if dgrad else W.t()
+        ref, size = X[a:b] @ B, X[a:b].abs() @ B.abs()
+        bound = U[out_dtype] * ref.abs() + (ceil_div(red, 128) + 16) * 2.0 ** -22 * size + SMALLEST[out_dtype]
+        fits = ref.abs() < (65504.0 if out_dtype == torch.float16 else float("inf")) * 0.99
+        err = (out[a:b].double() - ref).abs()
+        assert bool((err <= bound)[fits].all()), f"expert {e}: worst {float((err / bound)[fits].max()):.3g}"
+    assert bool((out[off[-1]:] == -77.0).all())
+
+
+SPLIT_GROUPS = [[3, 0, 1, 4, 0, 0, 8, 0], [0, 0, 0, 5], [0, 40, 0, 0, 1], [17, 16, 31], [0, 130, 0, 2]]
+
+
+@pytest.mark.parametrize("counts", SPLIT_GROUPS)
+@pytest.mark.parametrize("cols", [512, 272, 250])
+@pytest.mark.parametrize("dgrad", [False, True])
+def test_split_reduction_over_groups(counts, cols, dgrad):
+    """Tiles found by the search over groups, clusters beyond the last tile (empty groups), rows that no group holds."""
+    if dgrad:
+        cols = ceil_div(cols, 16) * 16
+    N, K = (4096, cols) if dgrad else (cols, 4096)
+    for extra, out_dtype in ((0, torch.bfloat16), (3, torch.float32)):
+        args = problem(sum(counts) + extra, N, K, len(counts), dgrad, len(counts))
+        out, form = product(*args, offsets_of(counts).cuda(), out_dtype, dgrad)
+        assert form == SPLIT
+        check(args, out, counts, out_dtype, dgrad)
