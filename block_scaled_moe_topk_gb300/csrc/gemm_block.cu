@@ -85,6 +85,7 @@ struct BlockParams {  // 64-byte aligned through its CUtensorMap members
 struct PairParams : BlockParams {
   CUtensorMap tmap_out;  // output, box 128 B x 32 rows
   int out_tma;           // output rows start on 16-byte boundaries
+  int out_stage;         // rows go through the staging and leave a row at a time
 };
 
 // One CTA (G = 1) or a pair (G = 2) works on a tile of 128 G rows by 256 columns; a CTA stages its 128
@@ -608,66 +609,47 @@ __global__ void __launch_bounds__(kBThreads, 1)
           }
           continue;
         }
-        if (!p.out_vec && col0 + 128 <= cols) {
-          // Rows off the 32-byte boundaries: 64 words of every row through the staging, then a row at a time
-          // by all lanes.  A 16-bit row at an odd element goes to the staging shifted by one, so that its
-          // words lie on memory's; the two elements at its ends are stored by themselves.  (29 experts x 910
-          // rows, N = 3311, K = 4048: 336 us, and 344 with every lane storing its own row as single CTAs do;
-          // N = 7167, K = 2048, 48 x 1024 rows: 738 and 764)
+        if (p.out_stage && col0 + 128 <= cols) {
+          // 16-bit rows off the 4-byte boundaries: a row's 64 words go through the staging and leave by all lanes,
+          // a row at a time; rows at an odd element are staged shifted by one, so that their words lie on
+          // memory's, and the two elements at their ends are stored by themselves.
           uint32_t* stage = reinterpret_cast<uint32_t*>(smem + BlockGeo<G>::kOutOff +
                                                         (warp - kBFirstEpiWarp) * BlockGeo<G>::kOutBytes);
-          const int es = dt == kDtF32 ? 4 : 2, nr = min(32, rows_here);
-          const int64_t pitch = (int64_t)cols * es;
-          uint8_t* dst0 = static_cast<uint8_t*>(a.out) + (row - lane) * pitch + (int64_t)col0 * es;
-          auto put = [&](const uint32_t(&w)[64]) {
-            __syncwarp();
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-              *reinterpret_cast<uint4*>(stage + lane * 64 + ((i ^ (lane & 7)) << 2)) =
-                  make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
-            __syncwarp();
-          };
-          auto rows_out = [&](uint8_t* dst) {
-#pragma unroll 1
-            for (int r0 = 0; r0 < nr; r0 += 8) {
-              uint32_t v[8][2];
-#pragma unroll
-              for (int i = 0; i < 8; ++i)
-#pragma unroll
-                for (int h = 0; h < 2; ++h) v[i][h] = stage[(r0 + i) * 64 + ((((lane >> 2) + 8 * h) ^ i) << 2) + (lane & 3)];
-#pragma unroll
-              for (int i = 0; i < 8; ++i, dst += pitch) {
-                if (r0 + i >= nr) break;
-                const int odd = (int)(reinterpret_cast<uintptr_t>(dst) & 2);
-                uint32_t* d = reinterpret_cast<uint32_t*>(dst + odd) + lane;
-                d[0] = v[i][0];
-                if (odd == 0 || lane < 31) d[32] = v[i][1];
-              }
-            }
-          };
-          if (lane == 0) bulk_wait_read_all();
+          const int nr = min(32, rows_here);
+          const int64_t pitch = (int64_t)cols * 2;
+          uint8_t* dst = static_cast<uint8_t*>(a.out) + (row - lane) * pitch + (int64_t)col0 * 2;
           uint32_t w[64];
-          if (dt == kDtF32) {
 #pragma unroll
-            for (int c = 0; c < 128; c += 64) {
+          for (int i = 0; i < 64; ++i) w[i] = out_pair(acc[2 * i], acc[2 * i + 1], dt);
+          uint8_t* mine_dst = dst + lane * pitch;
+          const uint32_t odd = (uint32_t)(reinterpret_cast<uintptr_t>(mine_dst) & 2);
+          if (odd != 0 && valid) {
+            *reinterpret_cast<uint16_t*>(mine_dst) = (uint16_t)w[0];
+            *reinterpret_cast<uint16_t*>(mine_dst + 254) = (uint16_t)(w[63] >> 16);
+          }
 #pragma unroll
-              for (int i = 0; i < 64; ++i) w[i] = __float_as_uint(acc[c + i]);
-              put(w);
-              rows_out(dst0 + 4 * c);
+          for (int i = 0; i < 64; ++i) w[i] = __funnelshift_r(w[i], i < 63 ? w[i + 1] : 0u, 8 * odd);
+          __syncwarp();  // the last tile's rows have been read
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            *reinterpret_cast<uint4*>(stage + lane * 64 + ((i ^ (lane & 7)) << 2)) =
+                make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+          __syncwarp();
+#pragma unroll 1
+          for (int r0 = 0; r0 < nr; r0 += 8) {
+            uint32_t v[8][2];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+#pragma unroll
+              for (int h = 0; h < 2; ++h) v[i][h] = stage[(r0 + i) * 64 + ((((lane >> 2) + 8 * h) ^ i) << 2) + (lane & 3)];
+#pragma unroll
+            for (int i = 0; i < 8; ++i, dst += pitch) {
+              if (r0 + i >= nr) break;
+              const int off = (int)(reinterpret_cast<uintptr_t>(dst) & 2);
+              uint32_t* d = reinterpret_cast<uint32_t*>(dst + off) + lane;
+              d[0] = v[i][0];
+              if (off == 0 || lane < 31) d[32] = v[i][1];
             }
-          } else {
-#pragma unroll
-            for (int i = 0; i < 64; ++i) w[i] = out_pair(acc[2 * i], acc[2 * i + 1], dt);
-            uint8_t* mine_dst = dst0 + lane * pitch;
-            const uint32_t odd = (uint32_t)(reinterpret_cast<uintptr_t>(mine_dst) & 2);
-            if (odd != 0 && valid) {
-              *reinterpret_cast<uint16_t*>(mine_dst) = (uint16_t)w[0];
-              *reinterpret_cast<uint16_t*>(mine_dst + 254) = (uint16_t)(w[63] >> 16);
-            }
-#pragma unroll
-            for (int i = 0; i < 64; ++i) w[i] = __funnelshift_r(w[i], i < 63 ? w[i + 1] : 0u, 8 * odd);
-            put(w);
-            rows_out(dst0);
           }
           continue;
         }
@@ -683,9 +665,9 @@ __global__ void __launch_bounds__(kBThreads, 1)
                 make_float4(acc[4 * i], acc[4 * i + 1], acc[4 * i + 2], acc[4 * i + 3]);
         }
       } else if (col0 + 128 <= cols) {
-        // Every lane stores its own row, whole 32-byte sectors but for the ends of a single CTA's unaligned
-        // rows (17535 rows of 13 experts, N = 2681, K = 1136: 97 us; element by element through a small
-        // staging buffer, as the last columns below, took 6 % longer)
+        // Every lane stores its own row, whole 32-byte sectors but for the ends of unaligned rows (17535 rows of
+        // 13 experts, N = 2681, K = 1136: 97 us; element by element through a small staging buffer, as the
+        // last columns below, took 6 % longer)
         if (p.out_vec) {
           uint8_t* dst = static_cast<uint8_t*>(a.out) + (row * cols + col0) * (dt == kDtF32 ? 4 : 2);
           if (dt == kDtF32) {
@@ -705,12 +687,12 @@ __global__ void __launch_bounds__(kBThreads, 1)
               if (valid) st_global_v8(dst + 2 * i, w);
             }
           }
-        } else if (G == 1 && dt == kDtF32) {
+        } else if (dt == kDtF32) {
           uint32_t w[128];
 #pragma unroll
           for (int i = 0; i < 128; ++i) w[i] = __float_as_uint(acc[i]);
           store_words<128>(static_cast<uint8_t*>(a.out) + (row * cols + col0) * 4, w, valid);
-        } else if (G == 1) {
+        } else {
           uint32_t w[64];
 #pragma unroll
           for (int i = 0; i < 64; ++i) w[i] = out_pair(acc[2 * i], acc[2 * i + 1], dt);
@@ -878,6 +860,14 @@ int64_t max_row_tiles(const GemmBlockArgs& a, int rows) {
   return (a.M + (int64_t)(rows - 1) * groups) / rows;
 }
 
+// A pair's rows off the 16-byte boundaries are stored by their lanes, pieces of up to 32 bytes
+// (store_words, store_halves), but 16-bit rows off the 4-byte boundaries behind a reduction longer than this by
+// the staging, a row at a time by all lanes.  Staging / lanes, us:
+//   48 experts x 1024 rows: N = 7167, K = 7168 2170 / 2206, K = 2048 739 / 767, K = 512 379 / 379; N = 7164, K = 2048
+//   749 / 740; 29 x 910, N = 3311, K = 4048 336 / 350; 32 x 1024, N = 4099: K = 1152 222 / 221, K = 256 133 / 127,
+//   N = 4100: K = 1152 222 / 210; fp32, N = 4099: K = 4096 567 / 556, K = 256 181 / 152
+constexpr cuuint64_t kStageCols = 1408;
+
 template <int G, bool DGRAD, bool SPLIT>
 cudaError_t launch_tiles(const GemmBlockArgs& a, int64_t tiles, int split, cudaStream_t s) {
   static std::atomic<int> ready[64];  // per device: the kernel's shared-memory limit is set
@@ -904,7 +894,9 @@ cudaError_t launch_tiles(const GemmBlockArgs& a, int64_t tiles, int split, cudaS
   const int64_t cols = DGRAD ? a.K : a.N;
   p.out_vec = out_grid(a, cols) % 32 == 0;
   if constexpr (G == 2) {
-    p.out_tma = out_grid(a, cols) % 16 == 0;
+    const uint64_t grid = out_grid(a, cols);
+    p.out_tma = grid % 16 == 0;
+    p.out_stage = grid % 4 != 0 && red > kStageCols;
     if (p.out_tma && !encode_out(&p.tmap_out, a, cols)) return cudaErrorInvalidValue;
   }
   p.split = split;

@@ -72,3 +72,30 @@ def test_split_reduction_over_groups(counts, cols, dgrad):
         out, form = product(*args, offsets_of(counts).cuda(), out_dtype, dgrad)
         assert form == SPLIT
         check(args, out, counts, out_dtype, dgrad)
+
+
+def on_pairs(N, K, dgrad, out_dtype, seed):
+    """Ragged groups, the smallest of a growing sequence that runs on pairs: (arguments, output, counts)."""
+    for s in (1, 2, 4, 8, 16, 32):
+        counts = [523 * s, 0, 15, 1200 * s + 7, 33]
+        args = problem(sum(counts) + 2, N, K, len(counts), dgrad, seed)
+        out, form = product(*args, offsets_of(counts).cuda(), out_dtype, dgrad)
+        if form == PAIR:
+            return args, out, counts
+    pytest.fail("no size ran on pairs")
+
+
+# Output rows on 32, 16, 8 and 4 bytes and off them, tiles' whole columns and the rest; long reductions, from which
+# 16-bit rows off the 4-byte boundaries leave through the staging, and shorter ones
+@pytest.mark.parametrize("cols", [1040, 1032, 1036, 1034, 1033])
+@pytest.mark.parametrize("red", [1040, 2064])
+@pytest.mark.parametrize("out_dtype", DTYPES)
+def test_pair_rows_on_and_off_the_boundaries(cols, red, out_dtype):
+    args, out, counts = on_pairs(cols, red, False, out_dtype, cols)
+    check(args, out, counts, out_dtype, False)
+
+
+@pytest.mark.parametrize("out_dtype", [torch.bfloat16, torch.float32])
+def test_pair_gradient(out_dtype):
+    args, out, counts = on_pairs(2064, 1040, True, out_dtype, 3)
+    check(args, out, counts, out_dtype, True)
