@@ -960,15 +960,20 @@ cudaError_t split_clusters(int split, int* clusters) {
 // 8 rows 8.3 against 6.6, 128 rows 13.4 against 8.2 (not split).
 //
 // Single CTAs or pairs: the smaller estimate of tile_time.  A pair's tile is cheaper a row (0.47
-// against 2 x 0.54 us a block for 256 rows, and its TMA stores leave 1.6 us a tile between the last sums and
-// the next tile's against 2.6), a single's wastes fewer rows in a group's last tile.  48 experts, N =
-// 6144, K = 7168, rows a group: single / pair us
-//   64: 345 / 411    128: 483 / 429    192: 532 / 441    256: 591 / 589    320: 712 / 807
-//   384: 888 / 795    512: 1046 / 926    768: 1528 / 1441    1024: 1980 / 1760
-// 48 experts x 1024 rows, N = 7168, K = 512 344 / 243, K = 256 251 / 202; one expert x 1024 rows, N = 6144, K =
-// 7168 64 / 61; 8 experts, N = 2048, K = 1024 x 512 rows 17.6 / 22.8.  Rows off the boundaries of the wide
-// stores take 3.6 and 3.1 us a tile instead: 13 experts x 1349 rows, N = 2681, K = 1136 96.6 / 91.6; 48 x 384, N =
-// 6143, K = 7168 890 / 810; 8 x 512, N = 2041, K = 1024 21.8 / 26.0; 48 x 1024, N = 7167, K = 256 316 / 323.
+// against 2 x 0.54 us a block for 256 rows, and 2.2 against 3.0 us a tile between the last sums and the next
+// tile's: its TMA stores run under them), a single's wastes fewer rows in a group's last tile, and pairs
+// start 2.4 us later.  TMA stores take whole pieces of 32 rows on 16-byte boundaries: other rows leave by
+// the lanes, 2.9 us a tile, 3.4 on a single CTA (32-byte boundaries: 3.0).  With these figures the slower
+// form costs 0.3-0.5 % on average over 2400 drawn products timed on both sides, 3 % of them more than 5 %, and
+// up to 47 % at one block a tile and a last tile of a few rows (223 x 269 rows, gradient of N = 96, K = 4944:
+// 210 / 309, run on pairs).  single / pair us:
+//   48 experts, N = 6144, K = 7168, rows a group: 64 345 / 411, 128 480 / 431, 192 532 / 441, 256 591 / 589,
+//   320 759 / 821, 384 927 / 839, 512 1119 / 997, 768 1624 / 1428, 1024 2069 / 1739
+//   48 experts x 1024, N = 7168: K = 2048 772 / 641, K = 512 341 / 244, K = 256 248 / 204; N = 7164: K = 2048 815 / 766,
+//   K = 512 380 / 353; N = 7167: K = 2048 827 / 751, K = 256 316 / 317; 48 x 384, N = 6143, K = 7168 926 / 853
+//   32 x 300, N = 4104: K = 2048 115 / 126, K = 512 55 / 55, K = 256 41 / 46; 32 x 140: K = 512 43 / 36
+//   16 x 1 row, N = 200, K = 400 8.6 / 9.9; 1 x 17, N = 1000, K = 272 8.3 / 9.7; 8 x 8, N = 1000, K = 1040 11.6 / 12.7;
+//   1 x 1024, N = 6144, K = 7168 63 / 55; 8 x 512, N = 2048, K = 1024 18 / 22; 13 x 1349, N = 2681, K = 1136 98 / 94
 //
 // Estimated time (us) of the product in row tiles of `rows` rows: a group of r rows, spread by sqrt(r)
 // when there are several, has k + 1 tiles or more with probability P(r > k rows) (a linear ramp here).
@@ -1004,8 +1009,8 @@ cudaError_t launch_direction(const GemmBlockArgs& a, cudaStream_t s) {
   }
   if (split > 1) return launch_tiles<1, DGRAD, true>(a, singles, split, s);
   const uint64_t grid = out_grid(a, cols);
-  if (tile_time(a, 128, col_tiles, RB, 0.54, grid % 32 == 0 ? 2.6 : 3.6) <=
-      tile_time(a, 256, col_tiles, RB, 0.47, grid % 16 == 0 ? 1.6 : 3.1) + 2.0)  // pairs start 2 us later
+  if (tile_time(a, 128, col_tiles, RB, 0.54, grid % 32 == 0 ? 3.0 : 3.4) <=
+      tile_time(a, 256, col_tiles, RB, 0.47, grid % 16 == 0 && avg >= 32 ? 2.2 : 2.9) + 2.4)
     return launch_tiles<1, DGRAD, false>(a, singles, 1, s);
   return launch_tiles<2, DGRAD, false>(a, max_row_tiles(a, BlockGeo<2>::kRows) * col_tiles, 1, s);
 }

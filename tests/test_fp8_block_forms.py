@@ -99,3 +99,21 @@ def test_pair_rows_on_and_off_the_boundaries(cols, red, out_dtype):
 def test_pair_gradient(out_dtype):
     args, out, counts = on_pairs(2064, 1040, True, out_dtype, 3)
     check(args, out, counts, out_dtype, True)
+
+
+@pytest.mark.parametrize("counts,N,K", [([1] * 16, 200, 400), ([17], 1000, 272), ([8] * 8, 1000, 1040)])
+def test_few_rows_off_the_wide_boundaries_run_on_single_ctas(counts, N, K):
+    """Rows on 16 but not 32 bytes, fewer than a TMA store's 32 a group: a pair's stores would not run under the
+    next tile's sums, and pairs are the slower form."""
+    args = problem(sum(counts), N, K, len(counts), False, N)
+    out, form = product(*args, offsets_of(counts).cuda(), torch.bfloat16)
+    assert form == SINGLE
+    check(args, out, counts, torch.bfloat16, False)
+
+
+def test_vector_form():
+    for counts, E in (([1], 1), ([0, 2, 0, 1, 1], 5)):
+        args = problem(sum(counts), 129, 1040, E, False, E)
+        out, form = product(*args, offsets_of(counts).cuda(), torch.float32)
+        assert form == VECTOR
+        check(args, out, counts, torch.float32, False)
