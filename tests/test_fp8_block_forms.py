@@ -117,3 +117,56 @@ def test_vector_form():
         out, form = product(*args, offsets_of(counts).cuda(), torch.float32)
         assert form == VECTOR
         check(args, out, counts, torch.float32, False)
+
+
+def check_contained(run, args, out, counts, out_dtype, dgrad):
+    """A NaN code, an infinite scale and a NaN weight change their own row, row and column, and no other bit, rows of
+    the neighbouring groups in the same 32 among them."""
+    x, xs, w, ws = args
+    off = offsets_of(counts).tolist()
+    spans = [(e, off[e], off[e + 1]) for e in range(len(counts)) if counts[e] > 0]
+    last, first = spans[0][2] - 1, spans[1][1]  # neighbours of two groups
+    e = spans[2][0]
+    x2, xs2, w2 = x.clone(), xs.clone(), w.clone()
+    x2[last, 3] = NAN_CODES[0]
+    xs2[first, 0] = float("inf")
+    w2[e, 7, 9] = NAN_CODES[1]
+    col = 9 if dgrad else 7
+    got = run(x2, xs2, w2, ws)
+    rows = torch.arange(out.shape[0], device="cuda")
+    cols = torch.arange(out.shape[1], device="cuda")
+    inside = (rows >= spans[2][1]) & (rows < spans[2][2])
+    touched = (rows == last)[:, None] | (rows == first)[:, None] | (inside[:, None] & (cols == col))
+    assert bool(torch.isnan(got[last]).all()) and not bool(torch.isfinite(got[first]).any())
+    assert bool(torch.isnan(got[inside][:, col]).all())
+    assert torch.equal(got[~touched], out[~touched])
+
+
+@pytest.mark.parametrize("cols", [1040, 1033])
+@pytest.mark.parametrize("dgrad", [False, True])
+def test_nan_and_inf_stay_in_their_row_and_column_on_pairs(cols, dgrad):
+    if dgrad:
+        cols = ceil_div(cols, 16) * 16
+    N, K = (2064, cols) if dgrad else (cols, 2064)
+    args, out, counts = on_pairs(N, K, dgrad, torch.float32, 5)
+
+    def run(*changed):
+        got, form = product(*changed, offsets_of(counts).cuda(), torch.float32, dgrad)
+        assert form == PAIR
+        return got
+
+    check_contained(run, args, out, counts, torch.float32, dgrad)
+
+
+@pytest.mark.parametrize("dgrad", [False, True])
+def test_nan_and_inf_stay_in_their_row_and_column_under_a_split(dgrad):
+    counts = [9, 0, 14, 3, 0, 0]
+    N, K = (4096, 272) if dgrad else (272, 4096)
+    args = problem(sum(counts), N, K, len(counts), dgrad, 6)
+
+    def run(*changed):
+        got, form = product(*changed, offsets_of(counts).cuda(), torch.float32, dgrad)
+        assert form == SPLIT
+        return got
+
+    check_contained(run, args, run(*args), counts, torch.float32, dgrad)
