@@ -363,9 +363,11 @@ def workspace_views(workspace, T, H, I, E, k, fmt=MOE_ACT_MXFP8):
 
 # ---------------------------------------------------------------- expert rows and FP8 experts
 # The C entry points see only pointers, so these bindings check what a pointer cannot tell: element
-# types, shapes, strides and the device (MOE_ERR_INVALID_ARG naming the tensor).  A decode step is a
-# few microseconds on the GPU, so each binding makes one plain test of everything first; only when
-# it fails do the _want / _matrix / _table checks run, which say what is wrong.
+# types, shapes, strides and the device (MOE_ERR_INVALID_ARG naming the tensor): all tensors of a call on
+# one GPU, which is the current one, whose stream the kernel runs on.  A decode step is a few
+# microseconds on the GPU, so each binding makes one plain test of everything first; only when it fails
+# do the _want / _matrix / _table checks run, which say what is wrong.  ``dev`` is the device of the call's
+# first tensor (-1: the host).
 _F32, _I32, _I64, _U8 = torch.float32, torch.int32, torch.int64, torch.uint8
 
 
@@ -374,35 +376,41 @@ def _want(ok: bool, where: str, what: str):
         raise MoeError(1, f"{where}: {what}")
 
 
-def _matrix(t, where, name, shape, dtypes=None):
+def _place(t, dev, where, name):
+    d = t.get_device()
+    _want(d >= 0, where, f"{name} must be on the GPU")
+    _want(d == dev, where, f"{name} is on cuda:{d}, expected cuda:{dev}")
+
+
+def _matrix(t, dev, where, name, shape, dtypes=None):
     """A row-major matrix on the GPU with unit column stride; None in ``shape``: any size."""
     _want(t is not None and t.dim() == 2, where, f"{name} must be a matrix")
     _want(all(n is None or n == m for n, m in zip(shape, t.shape)), where,
           f"{name} has shape {list(t.shape)}, expected {list(shape)}")
     _want(t.stride(1) == 1 or t.shape[1] <= 1, where, f"{name} must have unit column stride")
     _want(dtypes is None or t.dtype in dtypes, where, f"{name} has the unsupported type {t.dtype}")
-    _want(t.is_cuda, where, f"{name} must be on the GPU")
+    _place(t, dev, where, name)
 
 
-def _table(t, dtype, shape, where, name):
+def _table(t, dev, dtype, shape, where, name):
     _want(t is not None and t.dtype == dtype, where, f"{name} must be {dtype}")
     _want(len(t.shape) == len(shape) and all(n is None or n == m for n, m in zip(shape, t.shape)), where,
           f"{name} has shape {list(t.shape)}, expected {list(shape)}")
     _want(t.is_contiguous(), where, f"{name} must be contiguous")
-    _want(t.is_cuda, where, f"{name} must be on the GPU")
+    _place(t, dev, where, name)
 
 
 _ROWS = {d: c for d, c in _DTYPES.items() if d is not torch.uint8}
 
 
-def _fixed(t, dtype):
-    return t.dtype is dtype and t.is_cuda and t.is_contiguous()
+def _fixed(t, dev, dtype):
+    return t.dtype is dtype and t.get_device() == dev and t.is_contiguous()
 
 
-def _row_stride(t, shape):
-    """Elements between rows, or 0 unless the matrix plainly has unit column stride and is on the GPU."""
+def _row_stride(t, dev, shape):
+    """Elements between rows, or 0 unless the matrix plainly has unit column stride and is on that GPU."""
     st = t.stride()
-    if len(shape) != 2 or st[1] != 1 or not t.is_cuda:
+    if len(shape) != 2 or st[1] != 1 or dev < 0 or t.get_device() != dev:
         return 0
     return st[0] if shape[0] > 1 else max(st[0], shape[1])
 
@@ -412,99 +420,114 @@ def _stride(t):
     return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
 
 
+def _current_device():
+    return torch._C._cuda_getDevice()
+
+
+def _launch_stream(stream, dev, where):
+    """The stream's handle, for a kernel over tensors of device ``dev``."""
+    now = _current_device()
+    if now != dev:
+        raise MoeError(1, f"{where}: the tensors are on cuda:{dev}, the current device is cuda:{now}")
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
+
+
 def moe_permute(x, inv, rows, stream=None):
     """rows[inv[t, j]] = x[t]: x [T, H], inv int32 [T, k] (outside [0, R): dropped) -> rows [R, H]."""
-    dt, sx, si, sr = x.dtype, x.shape, inv.shape, rows.shape
-    tx, tr = _row_stride(x, sx), _row_stride(rows, sr)
-    if not (tx and tr and dt in _DTYPES and rows.dtype is dt and _fixed(inv, _I32) and len(si) == 2 and
+    fn = "moe_permute"
+    dt, sx, si, sr, dev = x.dtype, x.shape, inv.shape, rows.shape, inv.get_device()
+    tx, tr = _row_stride(x, dev, sx), _row_stride(rows, dev, sr)
+    if not (tx and tr and dt in _DTYPES and rows.dtype is dt and _fixed(inv, dev, _I32) and len(si) == 2 and
             si[0] == sx[0] and sr[1] == sx[1]):
-        fn = "moe_permute"
-        _table(inv, _I32, (None, None), fn, "inv")
-        _matrix(x, fn, "x", (si[0], None), _DTYPES)
-        _matrix(rows, fn, "rows", (None, sx[1]), (dt,))
+        _table(inv, dev, _I32, (None, None), fn, "inv")
+        _matrix(x, dev, fn, "x", (si[0], None), _DTYPES)
+        _matrix(rows, dev, fn, "rows", (None, sx[1]), (dt,))
         tx, tr = _stride(x), _stride(rows)
     _check(lib().moe_permute(x.data_ptr(), tx, _DTYPES[dt], inv.data_ptr(), sx[0], sx[1], si[1], rows.data_ptr(), tr,
-                             sr[0], _stream(stream)), "moe_permute")
+                             sr[0], _launch_stream(stream, dev, fn)), fn)
 
 
 def moe_permute_backward(d_rows, inv, d_x, stream=None):
     """Gradient of moe_permute: d_x[t] = sum_j d_rows[inv[t, j]]."""
-    dt, sr, si, sx = d_rows.dtype, d_rows.shape, inv.shape, d_x.shape
-    tr, tx = _row_stride(d_rows, sr), _row_stride(d_x, sx)
-    if not (tr and tx and dt in _ROWS and d_x.dtype is dt and _fixed(inv, _I32) and len(si) == 2 and
+    fn = "moe_permute_backward"
+    dt, sr, si, sx, dev = d_rows.dtype, d_rows.shape, inv.shape, d_x.shape, inv.get_device()
+    tr, tx = _row_stride(d_rows, dev, sr), _row_stride(d_x, dev, sx)
+    if not (tr and tx and dt in _ROWS and d_x.dtype is dt and _fixed(inv, dev, _I32) and len(si) == 2 and
             si[0] == sx[0] and sr[1] == sx[1]):
-        fn = "moe_permute_backward"
-        _table(inv, _I32, (None, None), fn, "inv")
-        _matrix(d_rows, fn, "d_rows", (None, None), _ROWS)
-        _matrix(d_x, fn, "d_x", (si[0], sr[1]), (dt,))
+        _table(inv, dev, _I32, (None, None), fn, "inv")
+        _matrix(d_rows, dev, fn, "d_rows", (None, None), _ROWS)
+        _matrix(d_x, dev, fn, "d_x", (si[0], sr[1]), (dt,))
         tr, tx = _stride(d_rows), _stride(d_x)
     _check(lib().moe_permute_backward(d_rows.data_ptr(), tr, sr[0], _DTYPES[dt], inv.data_ptr(), sx[0], sx[1], si[1],
-                                      d_x.data_ptr(), tx, _stream(stream)), "moe_permute_backward")
+                                      d_x.data_ptr(), tx, _launch_stream(stream, dev, fn)), fn)
 
 
 def moe_unpermute(rows, inv, topk_w, out, stream=None):
     """out[t] = sum_j topk_w[t, j] rows[inv[t, j]]: rows [R, H], topk_w fp32 [T, k] -> out [T, H]."""
-    dt, sr, si, so = rows.dtype, rows.shape, inv.shape, out.shape
-    tr, to = _row_stride(rows, sr), _row_stride(out, so)
-    if not (tr and to and dt in _ROWS and out.dtype is dt and _fixed(inv, _I32) and len(si) == 2 and
-            topk_w is not None and _fixed(topk_w, _F32) and topk_w.shape == si and si[0] == so[0] and sr[1] == so[1]):
-        fn = "moe_unpermute"
-        _table(inv, _I32, (None, None), fn, "inv")
-        _matrix(rows, fn, "rows", (None, None), _ROWS)
-        _matrix(out, fn, "out", (si[0], sr[1]), (dt,))
-        _table(topk_w, _F32, si, fn, "topk_w")
+    fn = "moe_unpermute"
+    dt, sr, si, so, dev = rows.dtype, rows.shape, inv.shape, out.shape, inv.get_device()
+    tr, to = _row_stride(rows, dev, sr), _row_stride(out, dev, so)
+    if not (tr and to and dt in _ROWS and out.dtype is dt and _fixed(inv, dev, _I32) and len(si) == 2 and
+            topk_w is not None and _fixed(topk_w, dev, _F32) and topk_w.shape == si and si[0] == so[0] and
+            sr[1] == so[1]):
+        _table(inv, dev, _I32, (None, None), fn, "inv")
+        _matrix(rows, dev, fn, "rows", (None, None), _ROWS)
+        _matrix(out, dev, fn, "out", (si[0], sr[1]), (dt,))
+        _table(topk_w, dev, _F32, si, fn, "topk_w")
         tr, to = _stride(rows), _stride(out)
     _check(lib().moe_unpermute(rows.data_ptr(), tr, sr[0], _DTYPES[dt], inv.data_ptr(), topk_w.data_ptr(), so[0],
-                               so[1], si[1], out.data_ptr(), to, _stream(stream)), "moe_unpermute")
+                               so[1], si[1], out.data_ptr(), to, _launch_stream(stream, dev, fn)), fn)
 
 
 def moe_unpermute_backward(d_out, rows, inv, topk_w, d_rows, d_topk_w, stream=None):
     """Gradients of moe_unpermute: d_rows[inv[t, j]] = topk_w[t, j] d_out[t] and d_topk_w[t, j] =
     <d_out[t], rows[inv[t, j]]>.  Either result may be None; rows may be None without d_topk_w."""
     fn = "moe_unpermute_backward"
-    dt, so, si = d_out.dtype, d_out.shape, inv.shape
-    to = _row_stride(d_out, so)
-    if not (to and dt in _ROWS and _fixed(inv, _I32) and len(si) == 2 and si[0] == so[0] and
-            topk_w is not None and _fixed(topk_w, _F32) and topk_w.shape == si):
-        _table(inv, _I32, (None, None), fn, "inv")
-        _matrix(d_out, fn, "d_out", (si[0], None), _ROWS)
-        _table(topk_w, _F32, si, fn, "topk_w")
+    dt, so, si, dev = d_out.dtype, d_out.shape, inv.shape, inv.get_device()
+    to = _row_stride(d_out, dev, so)
+    if not (to and dt in _ROWS and _fixed(inv, dev, _I32) and len(si) == 2 and si[0] == so[0] and
+            topk_w is not None and _fixed(topk_w, dev, _F32) and topk_w.shape == si):
+        _table(inv, dev, _I32, (None, None), fn, "inv")
+        _matrix(d_out, dev, fn, "d_out", (si[0], None), _ROWS)
+        _table(topk_w, dev, _F32, si, fn, "topk_w")
         to = _stride(d_out)
     R = rp = tr = dp = td = 0
     wp = None
     if d_rows is not None:
         sd = d_rows.shape
-        td = _row_stride(d_rows, sd)
+        td = _row_stride(d_rows, dev, sd)
         if not (td and d_rows.dtype is dt and sd[1] == so[1]):
-            _matrix(d_rows, fn, "d_rows", (None, so[1]), (dt,))
+            _matrix(d_rows, dev, fn, "d_rows", (None, so[1]), (dt,))
             td = _stride(d_rows)
         R, dp = sd[0], d_rows.data_ptr()
     if d_topk_w is not None:
         _want(rows is not None, fn, "d_topk_w needs rows")
         sr = rows.shape
-        tr = _row_stride(rows, sr)
+        tr = _row_stride(rows, dev, sr)
         if not (tr and rows.dtype is dt and sr[1] == so[1] and (d_rows is None or sr[0] == R) and
-                _fixed(d_topk_w, _F32) and d_topk_w.shape == si):
-            _matrix(rows, fn, "rows", (None if d_rows is None else R, so[1]), (dt,))
-            _table(d_topk_w, _F32, si, fn, "d_topk_w")
+                _fixed(d_topk_w, dev, _F32) and d_topk_w.shape == si):
+            _matrix(rows, dev, fn, "rows", (None if d_rows is None else R, so[1]), (dt,))
+            _table(d_topk_w, dev, _F32, si, fn, "d_topk_w")
             tr = _stride(rows)
         R, rp, wp = sr[0], rows.data_ptr(), d_topk_w.data_ptr()
     _check(lib().moe_unpermute_backward(d_out.data_ptr(), to, rp, tr, R, _DTYPES[dt], inv.data_ptr(),
-                                        topk_w.data_ptr(), so[0], so[1], si[1], dp, td, wp, _stream(stream)), fn)
+                                        topk_w.data_ptr(), so[0], so[1], si[1], dp, td, wp,
+                                        _launch_stream(stream, dev, fn)), fn)
 
 
 def moe_topk_route_backward(topk_ids, topk_w, d_topk_w, d_logits, stream=None):
     """Gradient of moe_topk_route's weights: ids int32, topk_w and d_topk_w fp32 [T, k] -> d_logits fp32 [T, E]."""
-    si, sl = topk_ids.shape, d_logits.shape
-    if not (_fixed(topk_ids, _I32) and _fixed(topk_w, _F32) and _fixed(d_topk_w, _F32) and _fixed(d_logits, _F32) and
-            len(si) == 2 and len(sl) == 2 and topk_w.shape == si and d_topk_w.shape == si and si[0] == sl[0]):
-        fn = "moe_topk_route_backward"
-        _table(topk_ids, _I32, (None, None), fn, "topk_ids")
-        _table(topk_w, _F32, si, fn, "topk_w")
-        _table(d_topk_w, _F32, si, fn, "d_topk_w")
-        _table(d_logits, _F32, (si[0], None), fn, "d_logits")
+    fn = "moe_topk_route_backward"
+    si, sl, dev = topk_ids.shape, d_logits.shape, topk_ids.get_device()
+    if not (dev >= 0 and _fixed(topk_ids, dev, _I32) and _fixed(topk_w, dev, _F32) and
+            _fixed(d_topk_w, dev, _F32) and _fixed(d_logits, dev, _F32) and len(si) == 2 and len(sl) == 2 and
+            topk_w.shape == si and d_topk_w.shape == si and si[0] == sl[0]):
+        _table(topk_ids, dev, _I32, (None, None), fn, "topk_ids")
+        _table(topk_w, dev, _F32, si, fn, "topk_w")
+        _table(d_topk_w, dev, _F32, si, fn, "d_topk_w")
+        _table(d_logits, dev, _F32, (si[0], None), fn, "d_logits")
     _check(lib().moe_topk_route_backward(topk_ids.data_ptr(), topk_w.data_ptr(), d_topk_w.data_ptr(), sl[0], sl[1],
-                                         si[1], d_logits.data_ptr(), _stream(stream)), "moe_topk_route_backward")
+                                         si[1], d_logits.data_ptr(), _launch_stream(stream, dev, fn)), fn)
 
 
 def moe_quantize_fp8_block(x, codes, scales, block_rows=1, stream=None):
@@ -512,33 +535,34 @@ def moe_quantize_fp8_block(x, codes, scales, block_rows=1, stream=None):
     block_rows = 1 or 128."""
     fn = "moe_quantize_fp8_block"
     _want(block_rows == 1 or block_rows == 128, fn, "block_rows must be 1 or 128")
-    dt, sx = x.dtype, x.shape
-    tx = _row_stride(x, sx)
-    if not (tx and dt in _ROWS and _fixed(codes, _U8) and codes.shape == sx and _fixed(scales, _F32) and
+    dt, sx, dev = x.dtype, x.shape, x.get_device()
+    tx = _row_stride(x, dev, sx)
+    if not (tx and dt in _ROWS and _fixed(codes, dev, _U8) and codes.shape == sx and _fixed(scales, dev, _F32) and
             scales.shape == ((sx[0] + block_rows - 1) // block_rows, (sx[1] + 127) // 128)):
-        _matrix(x, fn, "x", (None, None), _ROWS)
-        _table(codes, _U8, sx, fn, "codes")
-        _table(scales, _F32, (-(-sx[0] // block_rows), -(-sx[1] // 128)), fn, "scales")
+        _matrix(x, dev, fn, "x", (None, None), _ROWS)
+        _table(codes, dev, _U8, sx, fn, "codes")
+        _table(scales, dev, _F32, (-(-sx[0] // block_rows), -(-sx[1] // 128)), fn, "scales")
         tx = _stride(x)
     _check(lib().moe_quantize_fp8_block(x.data_ptr(), tx, _DTYPES[dt], sx[0], sx[1], block_rows, codes.data_ptr(),
-                                        scales.data_ptr(), _stream(stream)), fn)
+                                        scales.data_ptr(), _launch_stream(stream, dev, fn)), fn)
 
 
 def moe_permute_quantize_fp8_block(x, inv, codes, scales, stream=None):
     """moe_permute and moe_quantize_fp8_block in one pass: codes u8 [R, K], scales fp32 [R, ceil(K / 128)]."""
-    dt, sx, si, sc = x.dtype, x.shape, inv.shape, codes.shape
-    tx = _row_stride(x, sx)
-    if not (tx and dt in _ROWS and _fixed(inv, _I32) and len(si) == 2 and si[0] == sx[0] and _fixed(codes, _U8) and
-            len(sc) == 2 and sc[1] == sx[1] and _fixed(scales, _F32) and scales.shape == (sc[0], (sx[1] + 127) // 128)):
-        fn = "moe_permute_quantize_fp8_block"
-        _table(inv, _I32, (None, None), fn, "inv")
-        _matrix(x, fn, "x", (si[0], None), _ROWS)
-        _table(codes, _U8, (None, sx[1]), fn, "codes")
-        _table(scales, _F32, (sc[0], (sx[1] + 127) // 128), fn, "scales")
+    fn = "moe_permute_quantize_fp8_block"
+    dt, sx, si, sc, dev = x.dtype, x.shape, inv.shape, codes.shape, inv.get_device()
+    tx = _row_stride(x, dev, sx)
+    if not (tx and dt in _ROWS and _fixed(inv, dev, _I32) and len(si) == 2 and si[0] == sx[0] and
+            _fixed(codes, dev, _U8) and len(sc) == 2 and sc[1] == sx[1] and _fixed(scales, dev, _F32) and
+            scales.shape == (sc[0], (sx[1] + 127) // 128)):
+        _table(inv, dev, _I32, (None, None), fn, "inv")
+        _matrix(x, dev, fn, "x", (si[0], None), _ROWS)
+        _table(codes, dev, _U8, (None, sx[1]), fn, "codes")
+        _table(scales, dev, _F32, (sc[0], (sx[1] + 127) // 128), fn, "scales")
         tx = _stride(x)
     _check(lib().moe_permute_quantize_fp8_block(x.data_ptr(), tx, _DTYPES[dt], inv.data_ptr(), sx[0], sx[1], si[1],
-                                                codes.data_ptr(), scales.data_ptr(), sc[0], _stream(stream)),
-           "moe_permute_quantize_fp8_block")
+                                                codes.data_ptr(), scales.data_ptr(), sc[0],
+                                                _launch_stream(stream, dev, fn)), fn)
 
 
 def moe_gemm_fp8_block_workspace_bytes(M, N, K, E) -> int:
@@ -546,31 +570,32 @@ def moe_gemm_fp8_block_workspace_bytes(M, N, K, E) -> int:
 
 
 def _gemm_block(fn, dgrad, x, x_scale, w, w_scale, out, workspace, offsets, stream):
+    dev, sx, dt = w.get_device(), x.shape, out.dtype
     if len(w.shape) != 3:
-        _table(w, _U8, (None, None, None), fn, "w")
+        _table(w, dev, _U8, (None, None, None), fn, "w")
     E, N, K = w.shape
-    sx, dt = x.shape, out.dtype
     M = sx[0]
     inner, outer = (N, K) if dgrad else (K, N)
-    if not (_fixed(w, _U8) and _fixed(x, _U8) and _fixed(x_scale, _F32) and _fixed(w_scale, _F32) and dt in _ROWS and
-            _fixed(out, dt) and workspace.is_cuda and sx == (M, inner) and out.shape == (M, outer) and
+    if not (dev >= 0 and _fixed(w, dev, _U8) and _fixed(x, dev, _U8) and _fixed(x_scale, dev, _F32) and
+            _fixed(w_scale, dev, _F32) and dt in _ROWS and _fixed(out, dev, dt) and
+            workspace.get_device() == dev and sx == (M, inner) and out.shape == (M, outer) and
             x_scale.shape == (M, (inner + 127) // 128) and
             w_scale.shape == (E, (N + 127) // 128, (K + 127) // 128) and
-            (offsets is None or _fixed(offsets, _I64) and offsets.shape == (E + 1,))):
-        _table(w, _U8, (None, None, None), fn, "w")
-        _table(w_scale, _F32, (E, (N + 127) // 128, (K + 127) // 128), fn, "w_scale")
-        _table(x, _U8, (M, inner), fn, "the codes")
-        _table(x_scale, _F32, (M, (inner + 127) // 128), fn, "the codes' scales")
+            (offsets is None or _fixed(offsets, dev, _I64) and offsets.shape == (E + 1,))):
+        _table(w, dev, _U8, (None, None, None), fn, "w")
+        _table(w_scale, dev, _F32, (E, (N + 127) // 128, (K + 127) // 128), fn, "w_scale")
+        _table(x, dev, _U8, (M, inner), fn, "the codes")
+        _table(x_scale, dev, _F32, (M, (inner + 127) // 128), fn, "the codes' scales")
         _want(dt in _ROWS, fn, "the output must be bf16, f16 or f32")
-        _table(out, dt, (M, outer), fn, "the output")
+        _table(out, dev, dt, (M, outer), fn, "the output")
         if offsets is not None:
-            _table(offsets, _I64, (E + 1,), fn, "offsets")
-        _want(workspace.is_cuda, fn, "the workspace must be on the GPU")
+            _table(offsets, dev, _I64, (E + 1,), fn, "offsets")
+        _place(workspace, dev, fn, "the workspace")
     L = lib()
     _check((L.moe_gemm_fp8_block_dgrad if dgrad else L.moe_gemm_fp8_block)(
         x.data_ptr(), x_scale.data_ptr(), w.data_ptr(), w_scale.data_ptr(),
         None if offsets is None else offsets.data_ptr(), M, N, K, E, out.data_ptr(), _DTYPES[dt], workspace.data_ptr(),
-        workspace.nbytes, _stream(stream)), fn)
+        workspace.nbytes, _launch_stream(stream, dev, fn)), fn)
 
 
 def moe_gemm_fp8_block(x, x_scale, w, w_scale, out, workspace, offsets=None, stream=None):
