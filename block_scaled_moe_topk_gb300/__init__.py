@@ -574,6 +574,8 @@ def _gemm_block(fn, dgrad, x, x_scale, w, w_scale, out, workspace, offsets, stre
     if len(w.shape) != 3:
         _table(w, dev, _U8, (None, None, None), fn, "w")
     E, N, K = w.shape
+    if not sx:
+        _want(False, fn, "the codes have shape []")
     M = sx[0]
     inner, outer = (N, K) if dgrad else (K, N)
     if not (dev >= 0 and _fixed(w, dev, _U8) and _fixed(x, dev, _U8) and _fixed(x_scale, dev, _F32) and

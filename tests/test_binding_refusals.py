@@ -174,7 +174,7 @@ def test_wrong_size(call, arg, dim):
 @pytest.mark.parametrize("call,arg", [(c, a) for c, a in ARGS if a != "workspace"])
 def test_wrong_rank(call, arg):
     args = CALLS[call][1]()
-    for shape in ((1,) + tuple(args[arg].shape), (args[arg].numel(),)):
+    for shape in ((1,) + tuple(args[arg].shape), (args[arg].numel(),), ()):
         if len(shape) == args[arg].dim():
             continue
         bad = dict(args)
