@@ -195,7 +195,7 @@ constexpr int backward_blocks(int vb, int lg, int km) {
 // scaled into the k rows of drows and multiplied into the k dot products, which are then summed over
 // the threads (warp shuffles, then shared memory in warp order: the same bits on every call).  Rounds
 // lie a block apart: adjacent ones leave a row's last warps without work (261 against 225 us at T = 8192,
-// H = 7168, k = 6, bf16).
+// H = 7168, k = 6, bf16).  A round reads its chunks of the rows before it writes them: drows may be rows.
 template <int DT, int VB, int LG, int U, int KM>
 __global__ void __launch_bounds__(LG > 8 ? 1 << LG : kRowThreads, backward_blocks(VB, LG, KM))
     unpermute_backward_kernel(const __grid_constant__ RowsParams p) {

@@ -427,7 +427,8 @@ moe_status_t moe_profile_forward(moe_act_fmt_t fmt, const void* x_bf16, const fl
  *   moe_unpermute_backward, moe_quantize_fp8_block, moe_gemm_fp8_block_dgrad,
  *   moe_permute_backward, moe_topk_route_backward.
  * The rules of this header hold (device pointers, caller's buffers, argument checks before any
- * launch, one kernel per call, capturable).  Outputs must not overlap inputs.
+ * launch, one kernel per call, capturable).  Outputs must not overlap inputs, but for
+ * moe_unpermute_backward's d_rows, which may be rows itself.
  *
  * Common arguments
  *   inv      int32 [T, k]: the expert row of slot j of token t.  The `inv` of moe_sort_by_expert is
@@ -471,6 +472,8 @@ moe_status_t moe_unpermute(const void* rows, int64_t rows_stride, int64_t R, moe
  * are) and d_topk_w[t, j] = <d_out[t], rows[inv[t, j]]> in fp32 (0 for a dropped pair).
  *   d_out [T, H], rows [R, H], d_rows [R, H] of `dtype` (BF16, F16 or F32); d_topk_w fp32 [T, k].
  *   Either result may be NULL and is then not computed; rows is read for d_topk_w only.
+ *   d_rows may be rows itself (with its stride): an element is read before it is written, by the
+ *   thread that writes it.
  */
 moe_status_t moe_unpermute_backward(const void* d_out, int64_t d_out_stride, const void* rows, int64_t rows_stride,
                                     int64_t R, moe_dtype_t dtype, const int32_t* inv, const float* topk_w, int64_t T,

@@ -83,3 +83,16 @@ def test_narrow_accesses(k, dtype, by):
     drows, dw = shifted(torch.full_like(rows, 3.0)), torch.empty(T, k, device="cuda")
     moe.moe_unpermute_backward(shifted(dout), shifted(rows), inv, w, drows, dw)
     check(dout, rows, inv, w, drows, dw, 3.0)
+
+
+@pytest.mark.parametrize("T,H,k,E", [(200, 4104, 6, 16), (200, 2054, 8, 16), (200, 1887, 4, 16), (40, 124, 8, 16),
+                                     (16, 7168, 6, 16), (200, 2048, 7, 16), (200, 1028, 4, 8)])
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_gradient_in_place_of_the_rows(T, H, k, E, dtype):
+    """d_rows may be rows: every element is read before it is written, by the thread that writes it."""
+    dout, rows, inv, w = inputs(T, H, k, E, dtype, 0.3, 7)
+    drows, dw = rows.clone(), torch.empty(T, k, device="cuda")
+    moe.moe_unpermute_backward(dout, rows, inv, w, drows, dw)
+    same, dw2 = rows.clone(), torch.empty_like(dw)
+    moe.moe_unpermute_backward(dout, same, inv, w, same, dw2)
+    assert torch.equal(same, drows) and torch.equal(dw2, dw)
