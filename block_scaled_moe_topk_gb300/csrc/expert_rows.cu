@@ -181,14 +181,24 @@ __global__ void __launch_bounds__(kRowThreads, VB < 16 && KM > 4 ? 3 : 0)
   }
 }
 
-// Blocks of the kernel below that an SM is to hold: loads in flight carry it, and left alone it took up to
-// 98 registers a thread (T = 8192, k = 6, bf16, H = 7166: 276 against 258 us; T = 4096, k = 3, f32, H = 5120: 92
-// against 89).  Warps of their own (LG = 5) with more than four slots spill at four blocks: 54 against
-// 48 us with three at T = 16384, H = 512, k = 8, bf16, and 32 against 25 us at H = 124 left alone.
-constexpr int backward_blocks(int vb, int lg, int km) {
+// Blocks of the kernel below that an SM is to hold: loads in flight carry it, and left alone some instances
+// take up to 98 registers a thread.  us, left alone / held:
+//   f32, k <= 4: T = 4096, H = 5120, k = 3 92 / 89, T = 16384, H = 512, k = 2 70 / 54; bf16 8-byte rows, H = 260, k = 3
+//   60 / 51; k > 4, narrow: T = 16384, H = 1026, k = 6, bf16 147 / 122, f32 (T = 10152) 148 / 102
+// Warps of their own (LG = 5) with more than four slots spill at four blocks: 54 against 48 us with three at
+// T = 16384, H = 512, k = 8, bf16, and 32 against 25 us at H = 124 left alone.
+// 16-bit rows of a block's threads are best left alone on 16 bytes with more than four slots (held to four: T = 16384,
+// H = 768, k = 8 105 / 110, H = 7168 the same) and narrower ones with four or fewer (H = 1026, k = 4 86 / 100).
+// f32 rows with more than four slots are held to four blocks (64 registers, 84 bytes of spills) while short
+// and to three when long: T = 15258, H = 512, k = 8 113 with three / 106 with four, T = 6781, H = 1536, k = 6 90 / 88,
+// T = 2034, H = 5120, k = 6 84 / 87, T = 1089, H = 7168, k = 8 83 / 88; hence kLongChunks.
+constexpr int kLongChunks = 512;
+constexpr int backward_blocks(int bytes, int vb, int lg, int km, bool long_rows) {
   if (lg > 8) return 0;
-  if (lg == 5 && km > 4) return 3;
-  return km > 4 || vb == 2 ? 4 : 5;
+  if (lg == 5) return km > 4 ? 3 : vb == 2 ? 4 : 5;
+  if (bytes == 2 && (km > 4 ? vb == 16 : vb <= 4)) return 0;
+  if (km > 4) return long_rows ? 3 : 4;
+  return 5;
 }
 
 // The 2^LG threads of a token walk its row, U chunks at a time: every chunk of dout is read once,
@@ -196,8 +206,9 @@ constexpr int backward_blocks(int vb, int lg, int km) {
 // the threads (warp shuffles, then shared memory in warp order: the same bits on every call).  Rounds
 // lie a block apart: adjacent ones leave a row's last warps without work (261 against 225 us at T = 8192,
 // H = 7168, k = 6, bf16).  A round reads its chunks of the rows before it writes them: drows may be rows.
-template <int DT, int VB, int LG, int U, int KM>
-__global__ void __launch_bounds__(LG > 8 ? 1 << LG : kRowThreads, backward_blocks(VB, LG, KM))
+template <int DT, int VB, int LG, int U, int KM, bool LONG>
+__global__ void __launch_bounds__(LG > 8 ? 1 << LG : kRowThreads,
+                                  backward_blocks(sizeof(typename Elem<DT>::T), VB, LG, KM, LONG))
     unpermute_backward_kernel(const __grid_constant__ RowsParams p) {
   using C = Chunk<DT, VB>;
   using V = typename Raw<VB>::T;
@@ -381,11 +392,15 @@ cudaError_t backward_vb(const RowsArgs& a, cudaStream_t s) {
   const RowsParams p{a, a.H * dtype_bytes(a.dtype) / VB, 0, dtype_bytes(a.dtype), 1};
   if (p.chunks <= 64 * U) {  // short rows: a warp each
     const unsigned blocks = (unsigned)((a.T + kRowThreads / 32 - 1) / (kRowThreads / 32));
-    unpermute_backward_kernel<DT, VB, 5, U, KM><<<blocks, kRowThreads, 0, s>>>(p);
+    unpermute_backward_kernel<DT, VB, 5, U, KM, false><<<blocks, kRowThreads, 0, s>>>(p);
   } else if (p.chunks > 256 * U && a.T <= kFewTokens) {  // few long rows: a block of 1024 threads each
-    unpermute_backward_kernel<DT, VB, 10, U, KM><<<(unsigned)a.T, 1024, 0, s>>>(p);
+    unpermute_backward_kernel<DT, VB, 10, U, KM, false><<<(unsigned)a.T, 1024, 0, s>>>(p);
   } else {
-    unpermute_backward_kernel<DT, VB, 8, U, KM><<<(unsigned)a.T, kRowThreads, 0, s>>>(p);
+    constexpr bool kByLength = DT == kDtF32 && VB == 16 && KM > 4;
+    if (kByLength && p.chunks >= kLongChunks)
+      unpermute_backward_kernel<DT, VB, 8, U, KM, kByLength><<<(unsigned)a.T, kRowThreads, 0, s>>>(p);
+    else
+      unpermute_backward_kernel<DT, VB, 8, U, KM, false><<<(unsigned)a.T, kRowThreads, 0, s>>>(p);
   }
   return cudaGetLastError();
 }
