@@ -357,6 +357,13 @@ int row_threads_log2(int chunks, int U) {
   return lg;
 }
 
+// Bytes that the threads of a row cover, U chunks of VB bytes each: the row's own and those past its end.
+template <int VB, int U>
+int64_t covered_bytes(const RowsArgs& a) {
+  const int chunks = (int)((int64_t)a.H * dtype_bytes(a.dtype) / VB), span = U << row_threads_log2(chunks, U);
+  return (int64_t)((chunks + span - 1) / span) * span * VB;
+}
+
 // The parameters of a kernel whose threads own U chunks each, and its grid.
 template <int VB, int U>
 RowsParams row_params(const RowsArgs& a, unsigned* blocks) {
@@ -414,17 +421,25 @@ cudaError_t gather_vb(const RowsArgs& a, bool backward, cudaStream_t s) {
 
 template <int DT>
 cudaError_t gather_typed(const RowsArgs& a, bool backward, cudaStream_t s) {
-  // Rows on the 8-byte grid go in four 4-byte accesses a thread and not one of 8 bytes: T = 4096, H = 5118,
-  // f32, k = 6: unpermute 103 against 113 us, backward 174 against 207; T = 8192, H = 7164, bf16: unpermute 87
-  // against 93 us with k = 3 and 163 against 159 with k = 6, backward 255 against 328 with k = 6.  The backward
-  // of few slots is the exception: 146 with 8 bytes against 156 us with k = 3 (H = 116: 8.3 against 9.8).
+  // Rows on the 8-byte grid.  The sums take four 8-byte accesses a thread (us, 4 / 8 bytes: T = 8192, bf16, H =
+  // 7164: k = 6 156 / 135, k = 3 87 / 83; T = 16384, H = 1028: k = 5 60 / 48, k = 4 38 / 34; f32, T = 7614, H = 1026, k = 8
+  // 69 / 57) but for: rows that leave more of their threads' accesses unused that way (T = 12197, bf16, H = 5124, 17
+  // and 37 % unused, k = 2 80 / 94), one slot of long rows (T = 16384, f32, H = 3586 107 / 125, H = 514 25 / 23) and
+  // eight slots of 16-bit rows (T = 16384, H = 252 15 / 17, T = 3049, H = 5124 52 / 61; H = 1028 66 / 64).  Over 486
+  // timed rows this costs 0.6 % against the faster of both, 4 bytes always 7.6.
+  // The gradients take four 4-byte accesses with more than four slots (T = 16384, H = 260, bf16, k = 6 34 against
+  // 173 us with one 8-byte access), and one of 8 bytes otherwise (T = 8192, H = 7164, bf16, k = 3 146 against 156).
+  constexpr int kBytes = sizeof(typename Elem<DT>::T);
   switch (access_bytes(a)) {
     case 16: return gather_vb<DT, 16>(a, backward, s);
     case 8:
-      if (backward && a.k <= 4) return backward_vb<DT, 8, 4>(a, s);
-      return gather_vb<DT, 4>(a, backward, s);
+      if (backward) return a.k <= 4 ? backward_vb<DT, 8, 4>(a, s) : backward_vb<DT, 4, kMaxTopK>(a, s);
+      if (covered_bytes<8, 4>(a) > covered_bytes<4, 4>(a) || (a.k == 1 && a.H > 2048 / kBytes) ||
+          (a.k > 6 && kBytes == 2))
+        return gather_vb<DT, 4>(a, backward, s);
+      return a.k <= 4 ? unpermute_vb<DT, 8, 4>(a, s) : unpermute_vb<DT, 8, kMaxTopK>(a, s);
     case 4: return gather_vb<DT, 4>(a, backward, s);
-    default: return gather_vb<DT, (int)sizeof(typename Elem<DT>::T)>(a, backward, s);
+    default: return gather_vb<DT, kBytes>(a, backward, s);
   }
 }
 
