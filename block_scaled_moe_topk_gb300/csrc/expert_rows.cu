@@ -422,8 +422,8 @@ cudaError_t gather_vb(const RowsArgs& a, bool backward, cudaStream_t s) {
 template <int DT>
 cudaError_t gather_typed(const RowsArgs& a, bool backward, cudaStream_t s) {
   // Rows on the 8-byte grid.  The sums take four 8-byte accesses a thread (us, 4 / 8 bytes: T = 8192, bf16, H =
-  // 7164: k = 6 156 / 135, k = 3 87 / 83; T = 16384, H = 1028: k = 5 60 / 48, k = 4 38 / 34; f32, T = 7614, H = 1026, k = 8
-  // 69 / 57) but for: rows that leave more of their threads' accesses unused that way (T = 12197, bf16, H = 5124, 17
+  // 7164: k = 6 156 / 135, k = 3 87 / 83; T = 16384, H = 1028: k = 5 60 / 48, k = 4 38 / 34; f32, T = 7614, H = 1026,
+  // k = 8 69 / 57) but for: rows that leave more of their threads' accesses unused that way (T = 12197, bf16, H = 5124, 17
   // and 37 % unused, k = 2 80 / 94), one slot of long rows (T = 16384, f32, H = 3586 107 / 125, H = 514 25 / 23) and
   // eight slots of 16-bit rows (T = 16384, H = 252 15 / 17, T = 3049, H = 5124 52 / 61; H = 1028 66 / 64).  Over 486
   // timed rows this costs 0.6 % against the faster of both, 4 bytes always 7.6.

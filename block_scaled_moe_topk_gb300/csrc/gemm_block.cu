@@ -38,8 +38,11 @@
 // tiles with four accumulators (2.15 against 1.89: 1.5 times the operand bytes from L2), polling with
 // test_wait (+4 %), the groups' small remainders as single tiles of a second launch (-0.7 %, but up to
 // +22 % with a short reduction: the weights are read again), reads carried across blocks and scales read
-// a block ahead (the registers of the summing and of the control warps are used up; spills in either
-// cost 10-20 %).
+// a block ahead (the registers of the summing and of the control warps are used up; more spills in either
+// cost 10-20 %: the kernels as they are spill 60 bytes a thread on pairs, 64 on single CTAs, 132 split).
+// With a short reduction it is the tiles' ends: 48 x 1024 rows, N = 7168: K = 2048 641 us for 375 at the tensor
+// cores' rate, K = 512 244 for 134 by bytes.  Beside 0.47 us a block a pair spends 2.2 us a tile, little of it on
+// its stores; the scale warp's four dependent rounds a chunk may be the rest (not measured).
 // Tiles run expert by expert, row tiles fastest, so the pairs running side by side share weight
 // tiles in L2.  Every wait is bounded as in gemm_pair.cu: on expiry the status word records
 // MOE_ERR_DEVICE_TIMEOUT and both CTAs drain before TMEM is freed.
@@ -641,7 +644,8 @@ __global__ void __launch_bounds__(kBThreads, 1)
 #pragma unroll
             for (int i = 0; i < 8; ++i)
 #pragma unroll
-              for (int h = 0; h < 2; ++h) v[i][h] = stage[(r0 + i) * 64 + ((((lane >> 2) + 8 * h) ^ i) << 2) + (lane & 3)];
+              for (int h = 0; h < 2; ++h)
+                v[i][h] = stage[(r0 + i) * 64 + ((((lane >> 2) + 8 * h) ^ i) << 2) + (lane & 3)];
 #pragma unroll
             for (int i = 0; i < 8; ++i, dst += pitch) {
               if (r0 + i >= nr) break;
@@ -969,8 +973,8 @@ cudaError_t split_clusters(int split, int* clusters) {
 // 210 / 309, run on pairs).  single / pair us:
 //   48 experts, N = 6144, K = 7168, rows a group: 64 345 / 411, 128 480 / 431, 192 532 / 441, 256 591 / 589,
 //   320 759 / 821, 384 927 / 839, 512 1119 / 997, 768 1624 / 1428, 1024 2069 / 1739
-//   48 experts x 1024, N = 7168: K = 2048 772 / 641, K = 512 341 / 244, K = 256 248 / 204; N = 7164: K = 2048 815 / 766,
-//   K = 512 380 / 353; N = 7167: K = 2048 827 / 751, K = 256 316 / 317; 48 x 384, N = 6143, K = 7168 926 / 853
+//   48 experts x 1024, N = 7168: K = 2048 772 / 641, K = 512 341 / 244, K = 256 248 / 204; N = 7164: K = 2048 815 /
+//   766, K = 512 380 / 353; N = 7167: K = 2048 827 / 751, K = 256 316 / 317; 48 x 384, N = 6143, K = 7168 926 / 853
 //   32 x 300, N = 4104: K = 2048 115 / 126, K = 512 55 / 55, K = 256 41 / 46; 32 x 140: K = 512 43 / 36
 //   16 x 1 row, N = 200, K = 400 8.6 / 9.9; 1 x 17, N = 1000, K = 272 8.3 / 9.7; 8 x 8, N = 1000, K = 1040 11.6 / 12.7;
 //   1 x 1024, N = 6144, K = 7168 63 / 55; 8 x 512, N = 2048, K = 1024 18 / 22; 13 x 1349, N = 2681, K = 1136 98 / 94

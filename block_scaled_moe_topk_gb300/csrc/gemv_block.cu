@@ -40,7 +40,8 @@ __device__ __forceinline__ float dot4(uint32_t a, uint32_t b, float acc) {
 template <int MR, int U>
 __global__ void __launch_bounds__(kGvThreads) gemv_block_kernel(GemmBlockArgs a) {
   const int lane = threadIdx.x & 31;
-  if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x < 8) a.status[threadIdx.x] = threadIdx.x == kFormWord ? kFormVector : 0;
+  if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x < 8)
+    a.status[threadIdx.x] = threadIdx.x == kFormWord ? kFormVector : 0;
   const int n0 = (blockIdx.x * (kGvThreads / 32) + (threadIdx.x >> 5)) * kGvRows;
   const int64_t r0 = (int64_t)blockIdx.y * MR;
   int e = 0;

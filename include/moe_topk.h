@@ -432,8 +432,9 @@ moe_status_t moe_profile_forward(moe_act_fmt_t fmt, const void* x_bf16, const fl
  *
  * Common arguments
  *   inv      int32 [T, k]: the expert row of slot j of token t.  The `inv` of moe_sort_by_expert is
- *            one; any other injective map serves.  A value outside [0, R) marks a dropped pair
- *            (capacity limits): it is neither read nor written and contributes nothing.
+ *            one, and drops nothing; any other injective map serves.  A value outside [0, R) marks a
+ *            dropped pair (a caller that drops pairs at a capacity writes it there, and offsets to
+ *            match): it is neither read nor written and contributes nothing.
  *   R        rows of the expert-row matrices, 0 <= R <= 2^30; T <= 2^24, 1 <= k <= 8
  *   H, K, N  columns, at most 65536.  Matrices are row-major with unit column stride; *_stride is
  *            the row stride in elements (at least the columns).  Any width and alignment of the
