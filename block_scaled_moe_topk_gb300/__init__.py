@@ -26,6 +26,9 @@ __all__ = [
     "moe_unpermute", "moe_unpermute_backward", "moe_topk_route_backward", "moe_quantize_fp8_block",
     "moe_permute_quantize_fp8_block", "moe_gemm_fp8_block_workspace_bytes", "moe_gemm_fp8_block",
     "moe_gemm_fp8_block_dgrad",
+    "MOE_GATE_UP_INTERLEAVED", "MOE_GATE_UP_STACKED", "moe_rms_norm", "moe_rms_norm_quantize_fp8_block",
+    "moe_rms_norm_quantize_mx", "moe_rms_norm_backward_workspace_bytes", "moe_rms_norm_backward",
+    "moe_swiglu_backward",
 ]
 
 MOE_ACT_MXFP8 = 0
@@ -40,6 +43,8 @@ MOE_DTYPE_BF16 = 0
 MOE_DTYPE_F16 = 1
 MOE_DTYPE_F32 = 2
 MOE_DTYPE_U8 = 3  # moe_permute only: rows of bytes
+MOE_GATE_UP_INTERLEAVED = 0  # rows (columns of the products) 2j gate, 2j + 1 up
+MOE_GATE_UP_STACKED = 1      # [0, I) gate, [I, 2I) up
 _DTYPES = {torch.bfloat16: MOE_DTYPE_BF16, torch.float16: MOE_DTYPE_F16, torch.float32: MOE_DTYPE_F32,
            torch.uint8: MOE_DTYPE_U8}
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libmoe_topk.so")
@@ -130,6 +135,15 @@ def lib():
     L.moe_topk_route_backward.argtypes = [P, P, P, i64, i32, i32, P, P]
     L.moe_quantize_fp8_block.argtypes = [P, i64, i32, i64, i32, i32, P, P, P]
     L.moe_permute_quantize_fp8_block.argtypes = [P, i64, i32, P, i64, i32, i32, P, P, i64, P]
+    f32 = ctypes.c_float
+    rows_in, rows_out = [P, i64, P, i64, i32, P, i32, f32, i64, i32], [P, i64, P, i64, P, P]
+    L.moe_rms_norm.argtypes = rows_in + rows_out
+    L.moe_rms_norm_quantize_fp8_block.argtypes = rows_in + [P, P] + rows_out
+    L.moe_rms_norm_quantize_mx.argtypes = rows_in + [i32, P, P] + rows_out
+    L.moe_rms_norm_backward_workspace_bytes.argtypes = [i64, i32]
+    L.moe_rms_norm_backward_workspace_bytes.restype = sz
+    L.moe_rms_norm_backward.argtypes = [P, i64, P, i64, P, i64, i32, P, i32, P, i64, i32, P, i64, P, P, sz, P]
+    L.moe_swiglu_backward.argtypes = [P, i64, P, i64, i32, i32, i64, i32, P, i64, P, P, P]
     L.moe_gemm_fp8_block_workspace_bytes.argtypes = [i64, i32, i32, i32]
     L.moe_gemm_fp8_block_workspace_bytes.restype = sz
     for name in ("moe_gemm_fp8_block", "moe_gemm_fp8_block_dgrad"):
@@ -609,3 +623,132 @@ def moe_gemm_fp8_block(x, x_scale, w, w_scale, out, workspace, offsets=None, str
 def moe_gemm_fp8_block_dgrad(dy, dy_scale, w, w_scale, dx, workspace, offsets=None, stream=None):
     """Gradient of moe_gemm_fp8_block with respect to x: dy u8 [M, N], dy_scale fp32 [M, ceil(N/128)] -> dx [M, K]."""
     _gemm_block("moe_gemm_fp8_block_dgrad", True, dy, dy_scale, w, w_scale, dx, workspace, offsets, stream)
+
+
+# ---------------------------------------------------------------- norms and gated blocks
+
+def _rows_at(t, shape, dt, dev, where, name):
+    """Pointer and row stride of a matrix of that shape and type; (None, 0) without one."""
+    if t is None:
+        return None, 0
+    st = _row_stride(t, dev, t.shape)
+    if not (st and t.dtype is dt and t.shape == shape):
+        _matrix(t, dev, where, name, shape, (dt,))
+        st = _stride(t)
+    return t.data_ptr(), st
+
+
+def _flat_at(t, shape, dt, dev, where, name):
+    """Pointer of a contiguous tensor of that shape and type; None without one."""
+    if t is None:
+        return None
+    if not (_fixed(t, dev, dt) and t.shape == shape):
+        _table(t, dev, dt, shape, where, name)
+    return t.data_ptr()
+
+
+def _norm_rows(fn, x, weight):
+    """What a norm's rows and weight have to be: (shape, type, device, row stride, the weight's type)."""
+    _want(weight is not None, fn, "weight is needed")
+    sx, dt, dev, wt = x.shape, x.dtype, x.get_device(), weight.dtype
+    tx = _row_stride(x, dev, sx)
+    if not (tx and dt in _ROWS and (wt is dt or wt is _F32) and _fixed(weight, dev, wt) and weight.shape == sx[1:]):
+        _matrix(x, dev, fn, "x", (None, None), _ROWS)
+        _want(wt in (dt, _F32), fn, f"weight has the unsupported type {wt}")
+        _table(weight, dev, wt, (sx[1],), fn, "weight")
+        tx = _stride(x)
+    return sx, dt, dev, tx, wt
+
+
+def _rms_norm(fn, x, weight, eps, quantized, out, residual, residual_out, rstd, stream):
+    sx, dt, dev, tx, wt = _norm_rows(fn, x, weight)
+    rp, tr = _rows_at(residual, sx, dt, dev, fn, "residual")
+    op, to = _rows_at(out, sx, dt, dev, fn, "out")
+    sp, ts = _rows_at(residual_out, sx, dt, dev, fn, "residual_out")
+    rstd = _flat_at(rstd, sx[:1], _F32, dev, fn, "rstd")
+    _check(getattr(lib(), fn)(x.data_ptr(), tx, rp, tr, _DTYPES[dt], weight.data_ptr(), _DTYPES[wt], eps, sx[0], sx[1],
+                              *quantized(sx, dev), op, to, sp, ts, rstd, _launch_stream(stream, dev, fn)), fn)
+
+
+def moe_rms_norm(x, weight, eps, out, residual=None, residual_out=None, rstd=None, stream=None):
+    """out = weight * s / sqrt(mean(s^2) + eps) with s = x + residual: x, residual, out, residual_out (s) [T, H],
+    weight [H] of x's type or fp32, rstd fp32 [T] (1 / sqrt(...), for the gradient)."""
+    fn = "moe_rms_norm"
+    _want(out is not None, fn, "out must be a matrix")
+    _rms_norm(fn, x, weight, eps, lambda sx, dev: (), out, residual, residual_out, rstd, stream)
+
+
+def moe_rms_norm_quantize_fp8_block(x, weight, eps, codes, scales, out=None, residual=None, residual_out=None,
+                                    rstd=None, stream=None):
+    """moe_rms_norm with its result as E4M3 codes u8 [T, H] and fp32 scales [T, ceil(H / 128)], and in out too."""
+    fn = "moe_rms_norm_quantize_fp8_block"
+    _want(codes is not None and scales is not None, fn, "codes and scales are needed")
+
+    def quantized(sx, dev):
+        return (_flat_at(codes, sx, _U8, dev, fn, "codes"),
+                _flat_at(scales, (sx[0], (sx[1] + 127) // 128), _F32, dev, fn, "scales"))
+    _rms_norm(fn, x, weight, eps, quantized, out, residual, residual_out, rstd, stream)
+
+
+def moe_rms_norm_quantize_mx(x, weight, eps, fmt, codes, scales, out=None, residual=None, residual_out=None, rstd=None,
+                             stream=None):
+    """moe_rms_norm with its result as MX codes (fmt MOE_ACT_MXFP8: u8 [T, H], MOE_ACT_MXFP4: u8 [T, H / 2]) and E8M0
+    scales u8 [T, H / 32], as the *_forward_prequant calls read them, and in out too."""
+    fn = "moe_rms_norm_quantize_mx"
+    _want(codes is not None and scales is not None, fn, "codes and scales are needed")
+    _want(fmt in (MOE_ACT_MXFP8, MOE_ACT_MXFP4), fn, "fmt must be MOE_ACT_MXFP8 or MOE_ACT_MXFP4")
+
+    def quantized(sx, dev):
+        _want(sx[1] % 32 == 0, fn, "the rows' width must be a multiple of 32")
+        return (fmt, _flat_at(codes, (sx[0], sx[1] if fmt == MOE_ACT_MXFP8 else sx[1] // 2), _U8, dev, fn, "codes"),
+                _flat_at(scales, (sx[0], sx[1] // 32), _U8, dev, fn, "scales"))
+    _rms_norm(fn, x, weight, eps, quantized, out, residual, residual_out, rstd, stream)
+
+
+def moe_rms_norm_backward_workspace_bytes(T, H) -> int:
+    return int(lib().moe_rms_norm_backward_workspace_bytes(int(T), int(H)))
+
+
+def moe_rms_norm_backward(dy, x, weight, rstd, dx, d_weight=None, workspace=None, d_residual=None, stream=None):
+    """Gradients of moe_rms_norm from its sum x (residual_out) [T, H] and rstd fp32 [T]: dx [T, H], of x and residual
+    alike, with d_residual [T, H] (what reaches residual_out from elsewhere) added; d_weight fp32 [H], which needs the
+    workspace."""
+    fn = "moe_rms_norm_backward"
+    sx, dt, dev, tx, wt = _norm_rows(fn, x, weight)
+    _want(dy is not None and dx is not None and rstd is not None, fn, "dy, rstd and dx are needed")
+    yp, ty = _rows_at(dy, sx, dt, dev, fn, "dy")
+    dp, td = _rows_at(dx, sx, dt, dev, fn, "dx")
+    rp, tr = _rows_at(d_residual, sx, dt, dev, fn, "d_residual")
+    sp = _flat_at(rstd, sx[:1], _F32, dev, fn, "rstd")
+    wp = _flat_at(d_weight, sx[1:], _F32, dev, fn, "d_weight")
+    space = size = None
+    if wp is not None:
+        _want(workspace is not None, fn, "d_weight needs the workspace")
+        _place(workspace, dev, fn, "the workspace")
+        space, size = workspace.data_ptr(), workspace.nbytes
+    _check(lib().moe_rms_norm_backward(yp, ty, x.data_ptr(), tx, rp, tr, _DTYPES[dt], weight.data_ptr(), _DTYPES[wt],
+                                       sp, sx[0], sx[1], dp, td, wp, space, size or 0,
+                                       _launch_stream(stream, dev, fn)), fn)
+
+
+def moe_swiglu_backward(gate_up, d_h, d_gate_up=None, codes=None, scales=None, layout=MOE_GATE_UP_INTERLEAVED,
+                        stream=None):
+    """Gradient of h = silu(gate) * up: gate_up [R, 2I] (columns as ``layout`` says), d_h [R, I] -> d_gate_up [R, 2I],
+    or E4M3 codes u8 [R, 2I] with fp32 scales [R, ceil(2I / 128)], or both."""
+    fn = "moe_swiglu_backward"
+    _want(layout in (MOE_GATE_UP_INTERLEAVED, MOE_GATE_UP_STACKED), fn, "unknown layout")
+    _want(d_gate_up is not None or codes is not None, fn, "d_gate_up or codes are needed")
+    _want((codes is None) == (scales is None), fn, "codes and scales come together")
+    sh, dt, dev = d_h.shape, d_h.dtype, d_h.get_device()
+    th = _row_stride(d_h, dev, sh)
+    if not (th and dt in _ROWS):
+        _matrix(d_h, dev, fn, "d_h", (None, None), _ROWS)
+        th = _stride(d_h)
+    wide = (sh[0], 2 * sh[1])
+    _want(gate_up is not None, fn, "gate_up must be a matrix")
+    gp, tg = _rows_at(gate_up, wide, dt, dev, fn, "gate_up")
+    dp, td = _rows_at(d_gate_up, wide, dt, dev, fn, "d_gate_up")
+    cp = _flat_at(codes, wide, _U8, dev, fn, "codes")
+    sp = _flat_at(scales, (sh[0], (wide[1] + 127) // 128), _F32, dev, fn, "scales")
+    _check(lib().moe_swiglu_backward(gp, tg, d_h.data_ptr(), th, _DTYPES[dt], layout, sh[0], sh[1], dp, td, cp, sp,
+                                     _launch_stream(stream, dev, fn)), fn)

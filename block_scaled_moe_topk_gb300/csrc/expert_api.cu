@@ -1,6 +1,8 @@
-// expert_api.cu -- the C ABI of the expert-row and FP8 block-scaled operators: argument validation
-// and one launch per call.  Nothing here allocates or synchronises.
+// expert_api.cu -- the C ABI of the expert-row, norm, gated and FP8 block-scaled operators: argument
+// validation and the launch (two for a norm's weight gradient).  Nothing here allocates or synchronises.
 #include <cuda_runtime.h>
+
+#include <algorithm>
 
 #include "api_common.h"
 #include "expert_internal.h"
@@ -83,6 +85,48 @@ moe_status_t quantize(const void* x, int64_t x_stride, moe_dtype_t dtype, int64_
   MOE_TRY(device_ok());
   const moe::QuantBlockArgs a{x, x_stride, rows, K, dtype, block_rows, codes, scales, inv, k, R};
   return status_of(moe::launch_quant_block(a, static_cast<cudaStream_t>(stream)));
+}
+
+moe_status_t rms_norm(moe::NormArgs a, void* stream) {
+  if (a.T < 0 || a.H <= 0) return MOE_ERR_INVALID_ARG;
+  if (!float_dtype(a.dtype) || (a.weight_dtype != a.dtype && a.weight_dtype != MOE_DTYPE_F32)) return MOE_ERR_INVALID_ARG;
+  if (!(a.eps >= 0.0f)) return MOE_ERR_INVALID_ARG;
+  if (a.T > kMaxRows || a.H > moe::kMaxNormWidth) return MOE_ERR_UNSUPPORTED_SHAPE;
+  if (a.quant == moe::kQuantMx && a.H % 32 != 0) return MOE_ERR_UNSUPPORTED_SHAPE;
+  if (a.weight == nullptr) return MOE_ERR_INVALID_ARG;
+  if (a.T > 0 && a.quant == moe::kQuantNone && a.out == nullptr) return MOE_ERR_INVALID_ARG;
+  if (a.T > 0 && a.quant != moe::kQuantNone && (a.codes == nullptr || a.scales == nullptr)) return MOE_ERR_INVALID_ARG;
+  MOE_TRY(check_matrix(a.x, a.T, a.x_stride, a.H, a.dtype));
+  if (a.residual != nullptr) MOE_TRY(check_matrix(a.residual, a.T, a.residual_stride, a.H, a.dtype));
+  if (a.residual_out != nullptr) MOE_TRY(check_matrix(a.residual_out, a.T, a.residual_out_stride, a.H, a.dtype));
+  if (a.out != nullptr) MOE_TRY(check_matrix(a.out, a.T, a.out_stride, a.H, a.dtype));
+  if (!aligned(a.weight, moe::dtype_bytes(a.weight_dtype)) || !aligned(a.rstd, 4)) return MOE_ERR_MISALIGNED;
+  if (a.quant == moe::kQuantFp8Block && !aligned(a.scales, 4)) return MOE_ERR_MISALIGNED;
+  if (a.T == 0) return MOE_OK;
+  MOE_TRY(device_ok());
+  return status_of(moe::launch_rms_norm(a, static_cast<cudaStream_t>(stream)));
+}
+
+moe::NormArgs norm_args(const void* x, int64_t x_stride, const void* residual, int64_t residual_stride,
+                        moe_dtype_t dtype, const void* weight, moe_dtype_t weight_dtype, float eps, int64_t T, int H,
+                        void* out, int64_t out_stride, void* residual_out, int64_t residual_out_stride, float* rstd) {
+  moe::NormArgs a{};
+  a.x = x;
+  a.x_stride = x_stride;
+  a.residual = residual;
+  a.residual_stride = residual_stride;
+  a.dtype = dtype;
+  a.weight = weight;
+  a.weight_dtype = weight_dtype;
+  a.eps = eps;
+  a.T = T;
+  a.H = H;
+  a.out = out;
+  a.out_stride = out_stride;
+  a.residual_out = residual_out;
+  a.residual_out_stride = residual_out_stride;
+  a.rstd = rstd;
+  return a;
 }
 
 moe_status_t check_gemm(int64_t M, int N, int K, int E) {
@@ -220,6 +264,108 @@ moe_status_t moe_permute_quantize_fp8_block(const void* x, int64_t x_stride, moe
   if (k <= 0 || (T > 0 && inv == nullptr)) return MOE_ERR_INVALID_ARG;
   if (T > kMaxTokens || k > moe::kMaxTopK) return MOE_ERR_UNSUPPORTED_SHAPE;
   return quantize(x, x_stride, dtype, T, K, 1, inv, k, R, codes, scales, stream);
+}
+
+moe_status_t moe_rms_norm(const void* x, int64_t x_stride, const void* residual, int64_t residual_stride,
+                          moe_dtype_t dtype, const void* weight, moe_dtype_t weight_dtype, float eps, int64_t T, int H,
+                          void* out, int64_t out_stride, void* residual_out, int64_t residual_out_stride, float* rstd,
+                          void* stream) {
+  return rms_norm(norm_args(x, x_stride, residual, residual_stride, dtype, weight, weight_dtype, eps, T, H, out,
+                            out_stride, residual_out, residual_out_stride, rstd), stream);
+}
+
+moe_status_t moe_rms_norm_quantize_fp8_block(const void* x, int64_t x_stride, const void* residual,
+                                             int64_t residual_stride, moe_dtype_t dtype, const void* weight,
+                                             moe_dtype_t weight_dtype, float eps, int64_t T, int H, uint8_t* codes,
+                                             float* scales, void* out, int64_t out_stride, void* residual_out,
+                                             int64_t residual_out_stride, float* rstd, void* stream) {
+  moe::NormArgs a = norm_args(x, x_stride, residual, residual_stride, dtype, weight, weight_dtype, eps, T, H, out,
+                              out_stride, residual_out, residual_out_stride, rstd);
+  a.quant = moe::kQuantFp8Block;
+  a.codes = codes;
+  a.scales = scales;
+  return rms_norm(a, stream);
+}
+
+moe_status_t moe_rms_norm_quantize_mx(const void* x, int64_t x_stride, const void* residual, int64_t residual_stride,
+                                      moe_dtype_t dtype, const void* weight, moe_dtype_t weight_dtype, float eps,
+                                      int64_t T, int H, moe_act_fmt_t fmt, uint8_t* codes, uint8_t* scales, void* out,
+                                      int64_t out_stride, void* residual_out, int64_t residual_out_stride, float* rstd,
+                                      void* stream) {
+  if (fmt != MOE_ACT_MXFP8 && fmt != MOE_ACT_MXFP4) return MOE_ERR_INVALID_ARG;
+  moe::NormArgs a = norm_args(x, x_stride, residual, residual_stride, dtype, weight, weight_dtype, eps, T, H, out,
+                              out_stride, residual_out, residual_out_stride, rstd);
+  a.quant = moe::kQuantMx;
+  a.mx_fmt = fmt == MOE_ACT_MXFP8 ? 0 : 1;
+  a.codes = codes;
+  a.scales = scales;
+  return rms_norm(a, stream);
+}
+
+size_t moe_rms_norm_backward_workspace_bytes(int64_t T, int H) {
+  if (T < 0 || H <= 0 || T > kMaxRows || H > moe::kMaxNormWidth) return 0;
+  return (size_t)std::max(1, moe::norm_backward_parts(T, H)) * (size_t)H * 4;
+}
+
+moe_status_t moe_rms_norm_backward(const void* dy, int64_t dy_stride, const void* x, int64_t x_stride,
+                                   const void* d_residual, int64_t d_residual_stride, moe_dtype_t dtype,
+                                   const void* weight, moe_dtype_t weight_dtype, const float* rstd, int64_t T, int H,
+                                   void* dx, int64_t dx_stride, float* d_weight, void* workspace,
+                                   size_t workspace_bytes, void* stream) {
+  if (T < 0 || H <= 0) return MOE_ERR_INVALID_ARG;
+  if (!float_dtype(dtype) || (weight_dtype != dtype && weight_dtype != MOE_DTYPE_F32)) return MOE_ERR_INVALID_ARG;
+  if (T > kMaxRows || H > moe::kMaxNormWidth) return MOE_ERR_UNSUPPORTED_SHAPE;
+  if (weight == nullptr || (T > 0 && rstd == nullptr) || (d_weight != nullptr && workspace == nullptr))
+    return MOE_ERR_INVALID_ARG;
+  MOE_TRY(check_matrix(dy, T, dy_stride, H, dtype));
+  MOE_TRY(check_matrix(x, T, x_stride, H, dtype));
+  if (d_residual != nullptr) MOE_TRY(check_matrix(d_residual, T, d_residual_stride, H, dtype));
+  MOE_TRY(check_matrix(dx, T, dx_stride, H, dtype));
+  if (!aligned(weight, moe::dtype_bytes(weight_dtype)) || !aligned(rstd, 4) || !aligned(d_weight, 4) ||
+      !aligned(workspace, 256))
+    return MOE_ERR_MISALIGNED;
+  if (d_weight != nullptr && workspace_bytes < moe_rms_norm_backward_workspace_bytes(T, H))
+    return MOE_ERR_WORKSPACE_TOO_SMALL;
+  if (T == 0 && d_weight == nullptr) return MOE_OK;
+  MOE_TRY(device_ok());
+  moe::NormBackwardArgs a{};
+  a.dy = dy;
+  a.dy_stride = dy_stride;
+  a.x = x;
+  a.x_stride = x_stride;
+  a.dres = d_residual;
+  a.dres_stride = d_residual_stride;
+  a.dtype = dtype;
+  a.weight = weight;
+  a.weight_dtype = weight_dtype;
+  a.rstd = rstd;
+  a.T = T;
+  a.H = H;
+  a.dx = dx;
+  a.dx_stride = dx_stride;
+  a.dw = d_weight;
+  a.partial = static_cast<float*>(workspace);
+  return status_of(moe::launch_rms_norm_backward(a, static_cast<cudaStream_t>(stream)));
+}
+
+moe_status_t moe_swiglu_backward(const void* gate_up, int64_t gate_up_stride, const void* d_h, int64_t d_h_stride,
+                                 moe_dtype_t dtype, moe_gate_up_t layout, int64_t R, int I, void* d_gate_up,
+                                 int64_t d_gate_up_stride, uint8_t* codes, float* scales, void* stream) {
+  if (R < 0 || I <= 0 || !float_dtype(dtype)) return MOE_ERR_INVALID_ARG;
+  if (layout != MOE_GATE_UP_INTERLEAVED && layout != MOE_GATE_UP_STACKED) return MOE_ERR_INVALID_ARG;
+  if (R > kMaxRows || I > kMaxWidth / 2) return MOE_ERR_UNSUPPORTED_SHAPE;
+  if (layout == MOE_GATE_UP_STACKED && I % moe::kFp8Block != 0) return MOE_ERR_UNSUPPORTED_SHAPE;
+  if (R > 0 && d_gate_up == nullptr && codes == nullptr) return MOE_ERR_INVALID_ARG;
+  if ((codes == nullptr) != (scales == nullptr)) return MOE_ERR_INVALID_ARG;
+  MOE_TRY(check_matrix(gate_up, R, gate_up_stride, 2 * I, dtype));
+  MOE_TRY(check_matrix(d_h, R, d_h_stride, I, dtype));
+  if (d_gate_up != nullptr) MOE_TRY(check_matrix(d_gate_up, R, d_gate_up_stride, 2 * I, dtype));
+  if (!aligned(scales, 4)) return MOE_ERR_MISALIGNED;
+  if (R == 0) return MOE_OK;
+  MOE_TRY(device_ok());
+  const moe::SwigluBackwardArgs a{gate_up, gate_up_stride, d_h, d_h_stride, dtype, layout == MOE_GATE_UP_STACKED, R, I,
+                                  d_gate_up, d_gate_up_stride, codes, scales};
+  return status_of(moe::launch_swiglu_backward(a, static_cast<cudaStream_t>(stream)));
 }
 
 size_t moe_gemm_fp8_block_workspace_bytes(int64_t M, int N, int K, int E) {

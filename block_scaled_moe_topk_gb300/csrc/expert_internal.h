@@ -59,6 +59,72 @@ struct QuantBlockArgs {
 };
 cudaError_t launch_quant_block(const QuantBlockArgs& a, cudaStream_t s);
 
+// rms_norm.cu, rms_norm_backward.cu.  Strides are in elements.
+enum : int { kQuantNone = 0, kQuantFp8Block = 1, kQuantMx = 2 };
+constexpr int kMaxNormWidth = 32768;      // columns of a row: 512 threads of 64
+constexpr int64_t kSpreadRows = 2 * 152;  // up to so many rows the SMs are not filled by rows alone
+struct NormArgs {
+  const void* x;
+  int64_t x_stride;
+  const void* residual;  // or null
+  int64_t residual_stride;
+  int dtype;             // of x, residual, residual_out and out
+  const void* weight;    // [H]
+  int weight_dtype;      // dtype or fp32
+  float eps;
+  int64_t T;
+  int H;
+  void* out;             // or null (with codes)
+  int64_t out_stride;
+  void* residual_out;    // or null
+  int64_t residual_out_stride;
+  float* rstd;           // [T] or null
+  int quant;             // kQuant...
+  int mx_fmt;            // kQuantMx: 0 E4M3, 1 E2M1
+  uint8_t* codes;        // [T, H] (E2M1: [T, H / 2])
+  void* scales;          // fp32 [T, H / 128 (rounded up)], or E8M0 [T, H / 32]
+};
+cudaError_t launch_rms_norm(const NormArgs& a, cudaStream_t s);
+
+struct NormBackwardArgs {
+  const void* dy;
+  int64_t dy_stride;
+  const void* x;
+  int64_t x_stride;
+  const void* dres;      // or null
+  int64_t dres_stride;
+  int dtype;             // of dy, x, dres and dx
+  const void* weight;    // [H]
+  int weight_dtype;      // dtype or fp32
+  const float* rstd;     // [T]
+  int64_t T;
+  int H;
+  void* dx;
+  int64_t dx_stride;
+  float* dw;             // [H] or null
+  float* partial;        // [norm_backward_parts(T, H), H] with dw
+};
+// How many partial sums of the weight's gradient the kernel leaves (one a block), from the sizes alone.
+int norm_backward_parts(int64_t T, int H);
+cudaError_t launch_rms_norm_backward(const NormBackwardArgs& a, cudaStream_t s);
+
+// swiglu.cu
+struct SwigluBackwardArgs {
+  const void* gate_up;   // [R, 2I]
+  int64_t gate_up_stride;
+  const void* dh;        // [R, I]
+  int64_t dh_stride;
+  int dtype;
+  int stacked;           // columns [0, I) gate, [I, 2I) up; else 2j gate, 2j + 1 up
+  int64_t R;
+  int I;
+  void* d_gate_up;       // [R, 2I] or null
+  int64_t d_gate_up_stride;
+  uint8_t* codes;        // [R, 2I] or null
+  float* scales;         // [R, 2I / 128 (rounded up)]
+};
+cudaError_t launch_swiglu_backward(const SwigluBackwardArgs& a, cudaStream_t s);
+
 // gemm_block.cu.  Forward (dgrad = 0): out[r, n] = sum_c x[r, c] w[e, n, c], reduction K, N output
 // columns.  dgrad = 1: out[r, c] = sum_n x[r, n] w[e, n, c], reduction N, K output columns.
 struct GemmBlockArgs {

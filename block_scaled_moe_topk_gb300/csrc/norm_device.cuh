@@ -1,0 +1,177 @@
+// norm_device.cuh -- what the norm's and the gated block's row kernels share: 8 elements of a row at a time,
+// which columns a thread owns, the sum of a row over its threads, and the quantisation of 8 elements.
+#pragma once
+#include "fp8_block_device.cuh"
+#include "mx_device.cuh"
+
+namespace moe {
+namespace {
+
+// The columns of a thread's chunk c.  VEC: 8 consecutive ones; else element j is 32 j further.
+template <bool VEC>
+struct ColumnMap {
+  int first, step;
+  __device__ __forceinline__ ColumnMap(int i, int tpr)
+      : first(VEC ? 8 * i : (i >> 5) * 256 + (i & 31)), step(8 * tpr) {}
+  __device__ __forceinline__ int col(int c) const { return first + c * step; }
+};
+
+// 16 bytes of 16-bit elements as 8 fp32 values.
+template <int DT>
+__device__ __forceinline__ void unpack8(uint4 r, float (&v)[8]) {
+  const uint32_t u[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (DT == kDtBf16) {
+      v[2 * i] = __uint_as_float(u[i] << 16);
+      v[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
+    } else {
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&u[i]));
+      v[2 * i] = f.x, v[2 * i + 1] = f.y;
+    }
+  }
+}
+
+// The 8 elements of a chunk at column c of the row that starts at element `base`; columns from n on read as 0.
+// VEC: the row starts on a 16-byte boundary and n is a multiple of 8.
+template <int DT, bool VEC>
+__device__ __forceinline__ void load8(const void* x, int64_t base, int c, int n, float (&v)[8]) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) v[j] = 0.0f;
+  if (!VEC) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (c + 32 * j < n) v[j] = load1<DT>(x, base + c + 32 * j);
+  } else if (c < n) {
+    if (DT == kDtF32) {
+      const float4* src = reinterpret_cast<const float4*>(static_cast<const float*>(x) + base + c);
+      const float4 f0 = src[0], f1 = src[1];
+      v[0] = f0.x, v[1] = f0.y, v[2] = f0.z, v[3] = f0.w;
+      v[4] = f1.x, v[5] = f1.y, v[6] = f1.z, v[7] = f1.w;
+    } else {
+      unpack8<DT>(*reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(x) + base + c), v);
+    }
+  }
+}
+
+template <int DT>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  if (DT == kDtBf16) {
+    const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&b);
+  }
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+template <int DT, bool VEC>
+__device__ __forceinline__ void store8(void* x, int64_t base, int c, int n, const float (&v)[8]) {
+  if (!VEC) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      if (c + 32 * j >= n) continue;
+      if (DT == kDtF32) static_cast<float*>(x)[base + c + 32 * j] = v[j];
+      else static_cast<uint16_t*>(x)[base + c + 32 * j] = (uint16_t)pack2<DT>(v[j], 0.0f);
+    }
+  } else if (c < n) {
+    if (DT == kDtF32) {
+      float4* dst = reinterpret_cast<float4*>(static_cast<float*>(x) + base + c);
+      dst[0] = make_float4(v[0], v[1], v[2], v[3]);
+      dst[1] = make_float4(v[4], v[5], v[6], v[7]);
+    } else {
+      *reinterpret_cast<uint4*>(static_cast<uint16_t*>(x) + base + c) =
+          make_uint4(pack2<DT>(v[0], v[1]), pack2<DT>(v[2], v[3]), pack2<DT>(v[4], v[5]), pack2<DT>(v[6], v[7]));
+    }
+  }
+}
+
+// The sum over the tpr threads of a row (a power of two up to 32, or whole warps), the same for all of them, in an
+// order that depends on tpr alone.  rb: the row's place in the block.  Every thread of the block calls it.
+__device__ __forceinline__ float row_sum(float v, int tpr, int rb) {
+  __shared__ float part[32];
+  if (tpr <= 32) {
+    for (int o = tpr >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  const int nw = tpr >> 5, lane = threadIdx.x & 31;
+  if (lane == 0) part[threadIdx.x >> 5] = v;
+  __syncthreads();
+  v = lane < nw ? part[rb * nw + lane] : 0.0f;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+__device__ __forceinline__ float lanes_max(float m, int lanes) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+    if (o < lanes) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  return m;
+}
+
+// 8 values of a row of H columns at column c as codes with one fp32 scale per 128 columns, in rows of H codes and of
+// H / 128 (rounded up) scales.  Every lane of the warp calls it; values past H are 0.
+template <bool VEC>
+__device__ __forceinline__ void put_fp8(uint8_t* codes, float* scales, int64_t row, int H, int c, bool on,
+                                        const float (&v)[8]) {
+  const int HB = (H + kFp8Block - 1) / kFp8Block;
+  if (VEC) {  // 16 lanes a block
+    float m = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) m = fmaxf(m, finite_abs(v[j]));
+    const BlockScale sc = block_scale(lanes_max(m, 16));
+    if (!on || c >= H) return;
+    uint32_t w[2];
+    encode<8>(v, sc.mult, w);
+    *reinterpret_cast<uint2*>(codes + row * H + c) = make_uint2(w[0], w[1]);
+    if ((c & (kFp8Block - 1)) == 0) scales[row * HB + c / kFp8Block] = sc.scale;
+    return;
+  }
+#pragma unroll
+  for (int b = 0; b < 2; ++b) {  // four elements of every lane a block
+    float m = 0.0f;
+#pragma unroll
+    for (int j = 4 * b; j < 4 * b + 4; ++j) m = fmaxf(m, finite_abs(v[j]));
+    const BlockScale sc = block_scale(lanes_max(m, 32));
+    const int c0 = c + 128 * b;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (on && c0 + 32 * j < H) codes[row * H + c0 + 32 * j] = (uint8_t)encode2(v[4 * b + j], 0.0f, sc.mult);
+    if (on && c0 < H && (c0 & (kFp8Block - 1)) == 0) scales[row * HB + c0 / kFp8Block] = sc.scale;
+  }
+}
+
+// The same as MX codes (FMT 0: E4M3, 1: E2M1, two a byte) with one E8M0 scale per 32 columns, H a multiple of 32.
+template <bool VEC, int FMT>
+__device__ __forceinline__ void put_mx(uint8_t* codes, uint8_t* scales, int64_t row, int H, int c, bool on,
+                                       const float (&v)[8]) {
+  if (VEC) {  // 4 lanes a block
+    float m = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) m = fmaxf(m, fabsf(v[j]));
+    const MxScale sc = mx_scale<FMT>(lanes_max(m, 4));
+    if (!on || c >= H) return;
+    if (FMT == 0) *reinterpret_cast<uint2*>(codes + row * H + c) = pack_e4m3x8(v, sc.mult);
+    else *reinterpret_cast<uint32_t*>(codes + (row * H + c) / 2) = pack_e2m1x8(v, sc.mult);
+    if ((c & 31) == 0) scales[(row * H + c) / 32] = sc.byte;
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {  // one element of every lane a block
+    const MxScale sc = mx_scale<FMT>(lanes_max(fabsf(v[j]), 32));
+    const int cj = c + 32 * j;
+    const float next = __shfl_down_sync(0xffffffffu, v[j], 1);
+    if (!on || cj >= H) continue;
+    if (FMT == 0)
+      codes[row * H + cj] = (uint8_t)__nv_cvt_float2_to_fp8x2(make_float2(v[j] * sc.mult, 0.0f), __NV_SATFINITE, __NV_E4M3);
+    else if ((cj & 1) == 0)
+      codes[(row * H + cj) / 2] =
+          (uint8_t)__nv_cvt_float2_to_fp4x2(make_float2(v[j] * sc.mult, next * sc.mult), __NV_E2M1, cudaRoundNearest);
+    if ((cj & 31) == 0) scales[(row * H + cj) / 32] = sc.byte;
+  }
+}
+
+}  // namespace
+}  // namespace moe

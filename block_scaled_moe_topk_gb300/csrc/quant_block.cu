@@ -5,71 +5,16 @@
 // 448 x / m, ties to the even code.  m < 2^-100 gives scale 0 and signed-zero codes; a non-finite
 // x becomes the NaN code and leaves the block's scale to the finite elements.
 //
-// The quotient is formed as q = x * (448 / m), at most 2^-23 (relative) off.  A 16-bit x and m have
-// at most 11 significant bits, so 448 x / m either is a tie between two codes or lies 2^-16
-// (relative) or more away from every tie; ties are frequent (about one element in 300 of bf16
-// data).  Rounding q to 20 significant bits first (tie_snap: three fp32 operations) puts it back
-// on the tie, so the codes are those of the exact quotient at a fifth of an IEEE division's
-// instructions.  For fp32 x a quotient within 2^-20 of a tie may take either neighbour.
-//
 // HBM-bound: 8 lanes form a block of 128 columns, 16 columns each (two 16-byte loads of 16-bit x),
 // agree on m with three shuffles, and write 16 codes a lane to each of the row's destinations, one
 // destination after the other.
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
-#include <cuda_fp8.h>
-
 #include "expert_internal.h"
+#include "fp8_block_device.cuh"
 
 namespace moe {
 namespace {
 
 constexpr int kQbThreads = 256;
-constexpr float kMaxE4m3 = 448.0f;
-
-// q rounded to 20 significant bits (Veltkamp's splitting; the _rn forms are never fused).
-__device__ __forceinline__ float tie_snap(float q) {
-  const float c = __fmul_rn(q, 17.0f);
-  return __fsub_rn(c, __fsub_rn(c, q));
-}
-
-struct BlockScale {
-  float scale, mult;
-};
-__device__ __forceinline__ BlockScale block_scale(float m) {
-  if (m < 7.888609052210118e-31f) return {0.0f, 0.0f};  // 2^-100
-  return {__fdiv_rn(m, kMaxE4m3), __fdiv_rn(kMaxE4m3, m)};
-}
-
-__device__ __forceinline__ float finite_abs(float v) {
-  const float a = fabsf(v);
-  return a <= 3.402823466e38f ? a : 0.0f;  // false for NaN and infinities
-}
-
-// 16 values -> 16 E4M3 bytes, element 0 in the lowest byte.  The conversion saturates, so an
-// infinity is turned into a NaN first (inf - inf) and NaN stays NaN.
-__device__ __forceinline__ uint4 encode16(const float (&v)[16], float mult) {
-  uint32_t w[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    float q[2];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const float x = v[2 * i + h];
-      q[h] = tie_snap(__fmul_rn(x, mult));
-      if (!(fabsf(x) <= 3.402823466e38f)) q[h] = __int_as_float(0x7fffffff);
-    }
-    w[i] = (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(q[0], q[1]), __NV_SATFINITE, __NV_E4M3);
-  }
-  return make_uint4(w[0] | (w[1] << 16), w[2] | (w[3] << 16), w[4] | (w[5] << 16), w[6] | (w[7] << 16));
-}
-
-template <int DT>
-__device__ __forceinline__ float load1(const void* p, int64_t i) {
-  if (DT == kDtBf16) return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
-  if (DT == kDtF16) return __half2float(static_cast<const __half*>(p)[i]);
-  return static_cast<const float*>(p)[i];
-}
 
 // Columns [c, c + 16) of a row of n columns starting at element `base`; columns past n read as 0.
 // VEC: the row start is 16-byte aligned and n a multiple of 16.
@@ -117,6 +62,12 @@ __device__ __forceinline__ void store16(uint8_t* row, int c, int n, uint4 q) {
     for (int i = 0; i < 16; ++i)
       if (c + i < n) row[c + i] = (uint8_t)(w[i >> 2] >> (8 * (i & 3)));
   }
+}
+
+__device__ __forceinline__ uint4 encode16(const float (&v)[16], float mult) {
+  uint32_t w[4];
+  encode<16>(v, mult, w);
+  return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 struct QuantRowsParams {

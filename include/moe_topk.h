@@ -508,6 +508,78 @@ moe_status_t moe_permute_quantize_fp8_block(const void* x, int64_t x_stride, moe
                                             void* stream);
 
 /*
+ * Root-mean-square norm of rows, with the residual's addition in front of it:
+ *   s = x + residual (x where residual is NULL),  y = weight * s / sqrt(mean(s^2) + eps)
+ * in fp32 from the unrounded sum, each output rounded once.
+ *   x, residual, residual_out, out  [T, H] of `dtype` (BF16, F16 or F32), T <= 2^30, H <= 32768
+ *   residual      in, or NULL;  residual_out: s out, or NULL (it may be x or residual itself, with its stride)
+ *   out           y out; may be x or residual itself where that is not residual_out
+ *   weight        [H] of `weight_dtype`: `dtype` or F32;  eps >= 0
+ *   rstd          fp32 [T] out: 1 / sqrt(mean(s^2) + eps), which the gradient needs; or NULL
+ * A row whose squares' sum passes fp32's range (magnitudes of 1e19 and more) has no finite norm; NaN and
+ * infinities stay in their row.
+ */
+moe_status_t moe_rms_norm(const void* x, int64_t x_stride, const void* residual, int64_t residual_stride,
+                          moe_dtype_t dtype, const void* weight, moe_dtype_t weight_dtype, float eps, int64_t T, int H,
+                          void* out, int64_t out_stride, void* residual_out, int64_t residual_out_stride, float* rstd,
+                          void* stream);
+
+/* The same with y as FP8 codes, quantised from fp32 as moe_quantize_fp8_block (block_rows = 1) does:
+ * codes u8 [T, H], scales fp32 [T, ceil(H / 128)].  out may be NULL; given, it gets y too (a router
+ * reads it while the experts read the codes). */
+moe_status_t moe_rms_norm_quantize_fp8_block(const void* x, int64_t x_stride, const void* residual,
+                                             int64_t residual_stride, moe_dtype_t dtype, const void* weight,
+                                             moe_dtype_t weight_dtype, float eps, int64_t T, int H, uint8_t* codes,
+                                             float* scales, void* out, int64_t out_stride, void* residual_out,
+                                             int64_t residual_out_stride, float* rstd, void* stream);
+
+/* The same with y as MX codes, quantised from fp32 by the rule of moe_quantize_mx: codes E4M3 u8 [T, H] or
+ * E2M1 u8 [T, H / 2], scales E8M0 u8 [T, H / 32], H % 32 == 0, as the *_forward_prequant calls read them. */
+moe_status_t moe_rms_norm_quantize_mx(const void* x, int64_t x_stride, const void* residual, int64_t residual_stride,
+                                      moe_dtype_t dtype, const void* weight, moe_dtype_t weight_dtype, float eps,
+                                      int64_t T, int H, moe_act_fmt_t fmt, uint8_t* codes, uint8_t* scales, void* out,
+                                      int64_t out_stride, void* residual_out, int64_t residual_out_stride, float* rstd,
+                                      void* stream);
+
+/*
+ * Gradients of the norm.  With xh = x * rstd (x: the sum, as residual_out holds it) and g = weight * dy:
+ *   dx = rstd * (g - xh * mean(g * xh)) + d_residual,   d_weight = sum over rows of dy * xh
+ *   dy, x, dx     [T, H] of `dtype`; dx is the gradient of x and of residual alike
+ *   d_residual    [T, H] of `dtype`: the gradient that reaches residual_out from elsewhere; or NULL
+ *   rstd          fp32 [T], as the norm wrote it;  weight as there
+ *   d_weight      fp32 [H] out, summed in fp32 in an order that depends on the sizes alone; or NULL
+ *   workspace     device, 256-byte aligned, >= moe_rms_norm_backward_workspace_bytes(T, H); needed with
+ *                 d_weight only, for its partial sums (two kernels run then)
+ *   dx may be dy, x or d_residual itself, with its stride.
+ */
+size_t moe_rms_norm_backward_workspace_bytes(int64_t T, int H);
+moe_status_t moe_rms_norm_backward(const void* dy, int64_t dy_stride, const void* x, int64_t x_stride,
+                                   const void* d_residual, int64_t d_residual_stride, moe_dtype_t dtype,
+                                   const void* weight, moe_dtype_t weight_dtype, const float* rstd, int64_t T, int H,
+                                   void* dx, int64_t dx_stride, float* d_weight, void* workspace,
+                                   size_t workspace_bytes, void* stream);
+
+/*
+ * How a gated block's two projections lie in the 2I rows of its weights, and in the 2I columns of their
+ * products: in turn (2j gate, 2j + 1 up; as in W1 of the layer), or one after the other ([0, I) gate,
+ * [I, 2I) up), where I is a multiple of 128, so that no scale block holds rows of both.
+ */
+typedef enum { MOE_GATE_UP_INTERLEAVED = 0, MOE_GATE_UP_STACKED = 1 } moe_gate_up_t;
+
+/*
+ * Gradient of h = silu(gate) * up:
+ *   d_up = d_h * silu(gate),   d_gate = d_h * up * sig(gate) * (1 + gate * (1 - sig(gate)))
+ *   gate_up    [R, 2I], d_h [R, I], d_gate_up [R, 2I] of `dtype` (BF16, F16 or F32), R <= 2^30, 2I <= 65536
+ *   d_gate_up  out, or NULL; may be gate_up itself, with its stride
+ *   codes, scales  u8 [R, 2I], fp32 [R, ceil(2I / 128)] out: the same as FP8 codes, quantised from fp32 as
+ *              moe_quantize_fp8_block does, for moe_gemm_fp8_block_dgrad; or both NULL
+ * At least one form of the result is given.
+ */
+moe_status_t moe_swiglu_backward(const void* gate_up, int64_t gate_up_stride, const void* d_h, int64_t d_h_stride,
+                                 moe_dtype_t dtype, moe_gate_up_t layout, int64_t R, int I, void* d_gate_up,
+                                 int64_t d_gate_up_stride, uint8_t* codes, float* scales, void* stream);
+
+/*
  * Matrix product in FP8 with a scale for each block of 128, over groups of rows:
  *   out[r, n] = sum_b x_scale[r, b] * w_scale[e, n / 128, b] * sum_{c in block b} x[r, c] * w[e, n, c]
  * for the rows offsets[e] <= r < offsets[e + 1] of expert e.  The inner sum of a block runs on the
