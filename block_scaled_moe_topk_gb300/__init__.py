@@ -28,7 +28,7 @@ __all__ = [
     "moe_gemm_fp8_block_dgrad",
     "MOE_GATE_UP_INTERLEAVED", "MOE_GATE_UP_STACKED", "moe_rms_norm", "moe_rms_norm_quantize_fp8_block",
     "moe_rms_norm_quantize_mx", "moe_rms_norm_backward_workspace_bytes", "moe_rms_norm_backward",
-    "moe_swiglu_backward",
+    "moe_swiglu_backward", "moe_gemm_fp8_block_swiglu",
 ]
 
 MOE_ACT_MXFP8 = 0
@@ -144,6 +144,7 @@ def lib():
     L.moe_rms_norm_backward_workspace_bytes.restype = sz
     L.moe_rms_norm_backward.argtypes = [P, i64, P, i64, P, i64, i32, P, i32, P, i64, i32, P, i64, P, P, sz, P]
     L.moe_swiglu_backward.argtypes = [P, i64, P, i64, i32, i32, i64, i32, P, i64, P, P, P]
+    L.moe_gemm_fp8_block_swiglu.argtypes = [P, P, P, P, i32, P, i64, i32, i32, i32, P, P, i32, P, P, P, sz, P]
     L.moe_gemm_fp8_block_workspace_bytes.argtypes = [i64, i32, i32, i32]
     L.moe_gemm_fp8_block_workspace_bytes.restype = sz
     for name in ("moe_gemm_fp8_block", "moe_gemm_fp8_block_dgrad"):
@@ -752,3 +753,38 @@ def moe_swiglu_backward(gate_up, d_h, d_gate_up=None, codes=None, scales=None, l
     sp = _flat_at(scales, (sh[0], (wide[1] + 127) // 128), _F32, dev, fn, "scales")
     _check(lib().moe_swiglu_backward(gp, tg, d_h.data_ptr(), th, _DTYPES[dt], layout, sh[0], sh[1], dp, td, cp, sp,
                                      _launch_stream(stream, dev, fn)), fn)
+
+
+def moe_gemm_fp8_block_swiglu(x, x_scale, w, w_scale, workspace, out=None, codes=None, scales=None, gate_up=None,
+                              layout=MOE_GATE_UP_INTERLEAVED, offsets=None, stream=None):
+    """h = silu(gate) * up of the products of x u8 [M, K], x_scale fp32 [M, ceil(K/128)] with w u8 [E, 2I, K] (gate and
+    up rows as ``layout`` says), w_scale fp32 [E, ceil(2I/128), ceil(K/128)], rows grouped by offsets int64 [E + 1]
+    (None: E = 1, all rows) -> out [M, I], or E4M3 codes u8 [M, I] with fp32 scales [M, ceil(I/128)], or both; the
+    products themselves to gate_up [M, 2I] of out's type."""
+    fn = "moe_gemm_fp8_block_swiglu"
+    _want(layout in (MOE_GATE_UP_INTERLEAVED, MOE_GATE_UP_STACKED), fn, "unknown layout")
+    _want(out is not None or codes is not None, fn, "out or codes are needed")
+    _want((codes is None) == (scales is None), fn, "codes and scales come together")
+    dev, sw, sx = w.get_device(), w.shape, x.shape
+    if not (_fixed(w, dev, _U8) and len(sw) == 3 and sw[1] % 2 == 0 and dev >= 0):
+        _table(w, dev, _U8, (None, None, None), fn, "w")
+        _want(sw[1] % 2 == 0, fn, f"w has {sw[1]} rows, gate and up make an even number")
+    E, N, K = sw
+    if not (len(sx) == 2 and sx[1] == K and _fixed(x, dev, _U8) and _fixed(x_scale, dev, _F32) and
+            x_scale.shape == (sx[0], (K + 127) // 128) and _fixed(w_scale, dev, _F32) and
+            w_scale.shape == (E, (N + 127) // 128, (K + 127) // 128) and workspace.get_device() == dev):
+        _table(w_scale, dev, _F32, (E, (N + 127) // 128, (K + 127) // 128), fn, "w_scale")
+        _table(x, dev, _U8, (None, K), fn, "x")
+        _table(x_scale, dev, _F32, (sx[0], (K + 127) // 128), fn, "x_scale")
+        _place(workspace, dev, fn, "the workspace")
+    M, I = sx[0], N // 2
+    dt = out.dtype if out is not None else gate_up.dtype if gate_up is not None else torch.bfloat16
+    _want(dt in _ROWS, fn, "out and gate_up must be bf16, f16 or f32")
+    op = _flat_at(out, (M, I), dt, dev, fn, "out")
+    gp = _flat_at(gate_up, (M, N), dt, dev, fn, "gate_up")
+    cp = _flat_at(codes, (M, I), _U8, dev, fn, "codes")
+    sp = _flat_at(scales, (M, (I + 127) // 128), _F32, dev, fn, "scales")
+    rp = _flat_at(offsets, (E + 1,), _I64, dev, fn, "offsets")
+    _check(lib().moe_gemm_fp8_block_swiglu(x.data_ptr(), x_scale.data_ptr(), w.data_ptr(), w_scale.data_ptr(), layout,
+                                           rp, M, I, K, E, op, gp, _DTYPES[dt], cp, sp, workspace.data_ptr(),
+                                           workspace.nbytes, _launch_stream(stream, dev, fn)), fn)

@@ -135,21 +135,32 @@ moe_status_t check_gemm(int64_t M, int N, int K, int E) {
   return MOE_OK;
 }
 
-moe_status_t gemm_block(int dgrad, const uint8_t* x, const float* x_scale, const uint8_t* w, const float* w_scale,
-                        const int64_t* offsets, int64_t M, int N, int K, int E, void* out, moe_dtype_t out_dtype,
-                        void* workspace, size_t workspace_bytes, void* stream) {
-  MOE_TRY(check_gemm(M, N, K, E));
-  if (K % 16 != 0 || (dgrad && N % 16 != 0)) return MOE_ERR_UNSUPPORTED_SHAPE;
-  if (!float_dtype(out_dtype)) return MOE_ERR_INVALID_ARG;
-  if (offsets == nullptr && E != 1) return MOE_ERR_INVALID_ARG;
-  if (!w || !w_scale || !workspace || (M > 0 && (!x || !x_scale || !out))) return MOE_ERR_INVALID_ARG;
-  if (!aligned(x, 16) || !aligned(w, 16) || !aligned(x_scale, 4) || !aligned(w_scale, 4) || !aligned(offsets, 8) ||
-      !aligned(out, moe::dtype_bytes(out_dtype)) || !aligned(workspace, 256))
+// `a` holds the pointers and sizes of a product (dgrad, or gated by `gated`); checked and launched.
+moe_status_t gemm_block(moe::GemmBlockArgs a, bool gated, void* workspace, size_t workspace_bytes, void* stream) {
+  MOE_TRY(check_gemm(a.M, a.N, a.K, a.E));
+  if (a.K % 16 != 0 || (a.dgrad && a.N % 16 != 0)) return MOE_ERR_UNSUPPORTED_SHAPE;
+  if (!float_dtype(a.out_dtype)) return MOE_ERR_INVALID_ARG;
+  if (a.offsets == nullptr && a.E != 1) return MOE_ERR_INVALID_ARG;
+  const bool result = a.out != nullptr || (gated && a.codes != nullptr);
+  if (!a.w || !a.w_scale || !workspace || (a.M > 0 && (!a.x || !a.x_scale || !result))) return MOE_ERR_INVALID_ARG;
+  if (!aligned(a.x, 16) || !aligned(a.w, 16) || !aligned(a.x_scale, 4) || !aligned(a.w_scale, 4) ||
+      !aligned(a.offsets, 8) || !aligned(a.out, moe::dtype_bytes(a.out_dtype)) ||
+      !aligned(a.gate_up, moe::dtype_bytes(a.out_dtype)) || !aligned(a.codes, 16) || !aligned(a.scales, 4) ||
+      !aligned(workspace, 256))
     return MOE_ERR_MISALIGNED;
-  if (workspace_bytes < moe_gemm_fp8_block_workspace_bytes(M, N, K, E)) return MOE_ERR_WORKSPACE_TOO_SMALL;
-  if (M == 0) return MOE_OK;
-  moe::GemmBlockArgs a{};
+  if (workspace_bytes < moe_gemm_fp8_block_workspace_bytes(a.M, a.N, a.K, a.E)) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  if (a.M == 0) return MOE_OK;
   MOE_TRY(device_ok(&a.num_sms));
+  a.status = static_cast<uint32_t*>(workspace);
+  a.timeout_ns = moe::wait_timeout_ns();
+  a.test_stall = moe::test_stall_producer();
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return status_of(gated ? moe::launch_gemm_swiglu(a, s) : moe::launch_gemm_block(a, s));
+}
+
+moe::GemmBlockArgs gemm_args(int dgrad, const uint8_t* x, const float* x_scale, const uint8_t* w, const float* w_scale,
+                             const int64_t* offsets, int64_t M, int N, int K, int E, void* out, moe_dtype_t out_dtype) {
+  moe::GemmBlockArgs a{};
   a.dgrad = dgrad;
   a.x = x;
   a.x_scale = x_scale;
@@ -162,10 +173,7 @@ moe_status_t gemm_block(int dgrad, const uint8_t* x, const float* x_scale, const
   a.E = E;
   a.out = out;
   a.out_dtype = out_dtype;
-  a.status = static_cast<uint32_t*>(workspace);
-  a.timeout_ns = moe::wait_timeout_ns();
-  a.test_stall = moe::test_stall_producer();
-  return status_of(moe::launch_gemm_block(a, static_cast<cudaStream_t>(stream)));
+  return a;
 }
 
 }  // namespace
@@ -375,13 +383,31 @@ size_t moe_gemm_fp8_block_workspace_bytes(int64_t M, int N, int K, int E) {
 moe_status_t moe_gemm_fp8_block(const uint8_t* x, const float* x_scale, const uint8_t* w, const float* w_scale,
                                 const int64_t* offsets, int64_t M, int N, int K, int E, void* out,
                                 moe_dtype_t out_dtype, void* workspace, size_t workspace_bytes, void* stream) {
-  return gemm_block(0, x, x_scale, w, w_scale, offsets, M, N, K, E, out, out_dtype, workspace, workspace_bytes, stream);
+  return gemm_block(gemm_args(0, x, x_scale, w, w_scale, offsets, M, N, K, E, out, out_dtype), false, workspace,
+                    workspace_bytes, stream);
 }
 
 moe_status_t moe_gemm_fp8_block_dgrad(const uint8_t* dy, const float* dy_scale, const uint8_t* w, const float* w_scale,
                                       const int64_t* offsets, int64_t M, int N, int K, int E, void* dx,
                                       moe_dtype_t dx_dtype, void* workspace, size_t workspace_bytes, void* stream) {
-  return gemm_block(1, dy, dy_scale, w, w_scale, offsets, M, N, K, E, dx, dx_dtype, workspace, workspace_bytes, stream);
+  return gemm_block(gemm_args(1, dy, dy_scale, w, w_scale, offsets, M, N, K, E, dx, dx_dtype), false, workspace,
+                    workspace_bytes, stream);
+}
+
+moe_status_t moe_gemm_fp8_block_swiglu(const uint8_t* x, const float* x_scale, const uint8_t* w, const float* w_scale,
+                                       moe_gate_up_t layout, const int64_t* offsets, int64_t M, int I, int K, int E,
+                                       void* out, void* gate_up, moe_dtype_t dtype, uint8_t* codes, float* scales,
+                                       void* workspace, size_t workspace_bytes, void* stream) {
+  if (layout != MOE_GATE_UP_INTERLEAVED && layout != MOE_GATE_UP_STACKED) return MOE_ERR_INVALID_ARG;
+  if (I <= 0 || (codes == nullptr) != (scales == nullptr)) return MOE_ERR_INVALID_ARG;
+  if (I > kMaxWidth / 2 || (layout == MOE_GATE_UP_STACKED && I % moe::kFp8Block != 0) || (codes && I % 16 != 0))
+    return MOE_ERR_UNSUPPORTED_SHAPE;
+  moe::GemmBlockArgs a = gemm_args(0, x, x_scale, w, w_scale, offsets, M, 2 * I, K, E, out, dtype);
+  a.stacked = layout == MOE_GATE_UP_STACKED;
+  a.gate_up = gate_up;
+  a.codes = codes;
+  a.scales = scales;
+  return gemm_block(a, true, workspace, workspace_bytes, stream);
 }
 
 }  // extern "C"

@@ -142,8 +142,14 @@ struct GemmBlockArgs {
   uint64_t timeout_ns;
   int num_sms;
   int test_stall;
+  // The gated product: N = 2I weight rows, out [M, I] or null (out_dtype is gate_up's type too)
+  int stacked;            // rows [0, I) gate, [I, 2I) up; else 2j gate, 2j + 1 up
+  void* gate_up;          // [M, 2I] or null
+  uint8_t* codes;         // [M, I] or null
+  float* scales;          // [M, I / 128 (rounded up)]
 };
 cudaError_t launch_gemm_block(const GemmBlockArgs& a, cudaStream_t s);
+cudaError_t launch_gemm_swiglu(const GemmBlockArgs& a, cudaStream_t s);  // gemm_swiglu.cu
 // What ran is left in status word 7 (the other words start at 0): the choice between the forms is an
 // estimate, and a test or a timing that means one of them can see that it got it.
 constexpr int kFormWord = 7;
@@ -151,5 +157,6 @@ enum : uint32_t { kFormVector = 1, kFormSingle = 2, kFormPair = 3, kFormSplit = 
 // gemv_block.cu: the forward product of a few rows, and whether a product is one.
 bool use_gemv(const GemmBlockArgs& a);
 cudaError_t launch_gemv_block(const GemmBlockArgs& a, cudaStream_t s);
+cudaError_t launch_gemv_swiglu(const GemmBlockArgs& a, cudaStream_t s);  // gemv_swiglu.cu
 
 }  // namespace moe

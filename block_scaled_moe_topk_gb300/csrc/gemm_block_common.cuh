@@ -1,8 +1,9 @@
-// gemm_block_common.cuh -- what the kernels of the FP8 block-scaled product share: rounding to the
-// output type and the clamped row ranges of the groups.
+// gemm_block_common.cuh -- what the kernels of the FP8 block-scaled products share: rounding to the
+// output type, the clamped row ranges of the groups, and the vector forms' products.
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
+#include <cuda_fp8.h>
 
 #include "expert_internal.h"
 
@@ -94,6 +95,18 @@ __device__ __forceinline__ int64_t group_start(const int64_t* offsets, int e, in
   if (offsets == nullptr) return e == 0 ? 0 : M;
   const int64_t v = offsets[e];
   return v < 0 ? 0 : (v > M ? M : v);
+}
+
+// acc + the products of 4 E4M3 pairs (a 32-bit word holds two pairs).
+__device__ __forceinline__ float dot4(uint32_t a, uint32_t b, float acc) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const __half2_raw x = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(a >> (16 * h)), __NV_E4M3);
+    const __half2_raw y = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(b >> (16 * h)), __NV_E4M3);
+    asm("fma.rn.f32.f16 %0, %1, %2, %0;" : "+f"(acc) : "h"(x.x), "h"(y.x));
+    asm("fma.rn.f32.f16 %0, %1, %2, %0;" : "+f"(acc) : "h"(x.y), "h"(y.y));
+  }
+  return acc;
 }
 
 }  // namespace

@@ -13,9 +13,6 @@
 // loads: two rows 5.5 against 10.2 us, four 7.3 against 9.9 (N = 2304) but 18.9 against 15.0 (N =
 // 6144), hence the rule in use_gemv.  Grouped rows run one by one: three rows of 384 experts 6.7
 // against 14.5 us, six of N = 6144 67 against 55.
-#include <cuda_fp16.h>
-#include <cuda_fp8.h>
-
 #include "gemm_block_common.cuh"
 
 namespace moe {
@@ -23,18 +20,6 @@ namespace {
 
 constexpr int kGvThreads = 256;
 constexpr int kGvRows = 2;  // weight rows of a warp
-
-// acc + the products of 4 E4M3 pairs (a 32-bit word holds two pairs).
-__device__ __forceinline__ float dot4(uint32_t a, uint32_t b, float acc) {
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const __half2_raw x = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(a >> (16 * h)), __NV_E4M3);
-    const __half2_raw y = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(b >> (16 * h)), __NV_E4M3);
-    asm("fma.rn.f32.f16 %0, %1, %2, %0;" : "+f"(acc) : "h"(x.x), "h"(y.x));
-    asm("fma.rn.f32.f16 %0, %1, %2, %0;" : "+f"(acc) : "h"(x.y), "h"(y.y));
-  }
-  return acc;
-}
 
 // MR rows of x a pass (one expert: they share the weights), U column chunks in flight.
 template <int MR, int U>

@@ -613,6 +613,26 @@ moe_status_t moe_gemm_fp8_block_dgrad(const uint8_t* dy, const float* dy_scale, 
                                       const int64_t* offsets, int64_t M, int N, int K, int E, void* dx,
                                       moe_dtype_t dx_dtype, void* workspace, size_t workspace_bytes, void* stream);
 
+/*
+ * The gated product: both projections of a gated block, the activation and its quantisation in one kernel:
+ *   h = silu(gate) * up  with  gate = x G_e^T, up = x U_e^T  over the rows of each expert, as moe_gemm_fp8_block
+ * forms the products; h and its codes come from the unrounded fp32 products.
+ *   x, x_scale, offsets, M, K, E, workspace  as there, with N = 2I in moe_gemm_fp8_block_workspace_bytes
+ *   w          E4M3 codes u8 [E, 2I, K], 16-byte aligned, gate and up rows as `layout` says;
+ *              w_scale fp32 [E, ceil(2I / 128), ceil(K / 128)]
+ *   out        h [M, I] of `dtype` (BF16, F16 or F32), or NULL
+ *   gate_up    [M, 2I] of `dtype`: the products in the columns' order of w's rows, which moe_swiglu_backward reads;
+ *              or NULL
+ *   codes, scales  u8 [M, I] (16-byte aligned, I % 16 == 0), fp32 [M, ceil(I / 128)]: h as FP8 codes, as
+ *              moe_quantize_fp8_block writes them and the next moe_gemm_fp8_block reads them; or both NULL
+ * out or codes is given, or both.  2I <= 65536.  The gradient: moe_swiglu_backward, then
+ * moe_gemm_fp8_block_dgrad with w.
+ */
+moe_status_t moe_gemm_fp8_block_swiglu(const uint8_t* x, const float* x_scale, const uint8_t* w, const float* w_scale,
+                                       moe_gate_up_t layout, const int64_t* offsets, int64_t M, int I, int K, int E,
+                                       void* out, void* gate_up, moe_dtype_t dtype, uint8_t* codes, float* scales,
+                                       void* workspace, size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -6,7 +6,7 @@ import pytest
 import torch
 
 import block_scaled_moe_topk_gb300 as moe
-from test_binding_refusals import Accepted, BF16, END, F32, U8, elsewhere, fake, fakes, host
+from test_binding_refusals import Accepted, BF16, END, F32, I64, U8, elsewhere, fake, fakes, host
 
 EPS = 1e-6
 
@@ -54,6 +54,11 @@ CALLS = {
     "swiglu_backward": (moe.moe_swiglu_backward,
                         lambda: fakes(gate_up=((6, 288), BF16), d_h=((6, 144), BF16), d_gate_up=((6, 288), BF16),
                                       codes=((6, 288), U8), scales=((6, 3), F32))),
+    "gemm_swiglu": (moe.moe_gemm_fp8_block_swiglu,
+                    lambda: fakes(x=((7, 144), U8), x_scale=((7, 2), F32), w=((3, 416, 144), U8),
+                                  w_scale=((3, 4, 2), F32), workspace=((256,), U8), out=((7, 208), BF16),
+                                  codes=((7, 208), U8), scales=((7, 2), F32), gate_up=((7, 416), BF16),
+                                  offsets=((4,), I64))),
 }
 STRIDED = {"x", "out", "residual", "residual_out", "dy", "dx", "d_residual", "gate_up", "d_h", "d_gate_up"}
 ARGS = [(c, a) for c, (_, make) in CALLS.items() for a in make()]
@@ -91,14 +96,14 @@ def test_another_current_device(monkeypatch):
 def test_wrong_type(call, arg):
     args = CALLS[call][1]()
     refused(call, {**args, arg: fake(*args[arg].shape, dtype=torch.float64)},
-            f"{arg} |has the unsupported type torch.")
+            f"{arg} |has the unsupported type torch.|must be (bf16|torch)")
 
 
 @pytest.mark.parametrize("call,arg,dim", [(c, a, d) for c, a in TYPED for d in range(CALLS[c][1]()[a].dim())])
 def test_wrong_size(call, arg, dim):
     args = CALLS[call][1]()
     shape = list(args[arg].shape)
-    shape[dim] += 32
+    shape[dim] += 256  # more than a scale block
     refused(call, {**args, arg: fake(*shape, dtype=args[arg].dtype)}, " has shape ")
 
 
@@ -114,7 +119,7 @@ def test_wrong_rank(call, arg):
 def test_wrong_strides(call, arg):
     args = CALLS[call][1]()
     t = args[arg]
-    if arg not in STRIDED:
+    if arg not in STRIDED or call == "gemm_swiglu":
         apart = torch.zeros(*t.shape[:-1], 2 * t.shape[-1], dtype=t.dtype)[..., ::2].as_subclass(type(t))
         refused(call, {**args, arg: apart}, f"{arg} must be contiguous" + END)
         return
@@ -126,10 +131,11 @@ def test_wrong_strides(call, arg):
 
 OPTIONAL = {"norm": ("residual", "residual_out", "rstd"), "norm_fp8": ("out", "residual", "residual_out", "rstd"),
             "norm_mx": ("out", "residual", "residual_out"), "norm_mx4": (), "norm_backward": ("d_weight", "d_residual"),
-            "swiglu_backward": ("d_gate_up",)}
+            "swiglu_backward": ("d_gate_up",), "gemm_swiglu": ("out", "gate_up", "offsets")}
+NEEDED = ("x", "d_h", "w", "x_scale", "w_scale", "workspace")  # left out they raise as any missing argument does
 
 
-@pytest.mark.parametrize("call,arg", [(c, a) for c, a in ARGS if a not in ("x", "d_h")])
+@pytest.mark.parametrize("call,arg", [(c, a) for c, a in ARGS if a not in NEEDED or (c, a) == ("norm_backward", "workspace")])
 def test_left_out(call, arg):
     args = {**CALLS[call][1](), arg: None}
     if arg in OPTIONAL[call]:
@@ -143,6 +149,14 @@ def test_values():
     args = CALLS["swiglu_backward"][1]()
     refused("swiglu_backward", {**args, "layout": 2}, "unknown layout" + END)
     refused("swiglu_backward", {**args, "d_gate_up": None, "codes": None, "scales": None}, "d_gate_up or codes are needed" + END)
+    gated = CALLS["gemm_swiglu"][1]()
+    refused("gemm_swiglu", {**gated, "layout": 2}, "unknown layout" + END)
+    refused("gemm_swiglu", {**gated, "out": None, "codes": None, "scales": None}, "out or codes are needed" + END)
+    refused("gemm_swiglu", {**gated, "w": fake(3, 415, 144, dtype=U8)}, "w has 415 rows")
+    with pytest.raises(Accepted):
+        moe.moe_gemm_fp8_block_swiglu(**{**gated, "codes": None, "scales": None})
+    with pytest.raises(Accepted):
+        moe.moe_gemm_fp8_block_swiglu(**{**gated, "out": None, "gate_up": None})
     odd = fakes(x=((6, 100), BF16), weight=((100,), BF16), codes=((6, 100), U8), scales=((6, 3), U8))
     refused("norm_mx", odd, "multiple of 32" + END)
     with pytest.raises(moe.MoeError, match="fmt must be"):
@@ -210,3 +224,24 @@ def swiglu_c(gu=A, gus=256, dh=A, dhs=128, dt=0, layout=0, R=4, I=128, d=A, ds=2
     (7, dict(scales=ODD))])
 def test_swiglu_backward_refuses(status, args):
     assert swiglu_c(**args) == status
+
+
+def gated_c(x=A, xs=A, w=A, ws=A, layout=0, off=A, M=5, I=128, K=256, E=2, out=A, gu=A, dt=0, codes=A, scales=A, space=A,
+            size=256):
+    return moe.lib().moe_gemm_fp8_block_swiglu(x, xs, w, ws, layout, off, M, I, K, E, out, gu, dt, codes, scales, space,
+                                               size, None)
+
+
+A8 = ctypes.c_void_p((1 << 20) + 8)
+
+
+@pytest.mark.parametrize("status,args", [
+    (1, dict(x=None)), (1, dict(xs=None)), (1, dict(w=None)), (1, dict(ws=None)), (1, dict(off=None)),
+    (1, dict(out=None, codes=None, scales=None)), (1, dict(codes=None)), (1, dict(scales=None)), (1, dict(space=None)),
+    (1, dict(layout=2)), (1, dict(dt=3)), (1, dict(M=-1)), (1, dict(I=0)), (1, dict(K=0)), (1, dict(E=0)),
+    (2, dict(K=264)), (2, dict(E=1025)), (2, dict(I=40000)), (2, dict(I=136)), (2, dict(layout=1, I=192)),
+    (2, dict(M=(1 << 30) + 1)), (4, dict(size=255)), (7, dict(x=A8)), (7, dict(w=A8)), (7, dict(codes=A8)),
+    (7, dict(out=ODD)), (7, dict(gu=ODD)), (7, dict(scales=ODD)), (7, dict(xs=ODD)), (7, dict(ws=ODD)),
+    (7, dict(off=ODD)), (7, dict(space=ctypes.c_void_p((1 << 20) + 128)))])
+def test_gated_product_refuses(status, args):
+    assert gated_c(**args) == status
