@@ -55,6 +55,90 @@ __device__ __forceinline__ void encode(const float* v, float mult, uint32_t (&w)
     w[i] = encode2(v[4 * i], v[4 * i + 1], mult) | (encode2(v[4 * i + 2], v[4 * i + 3], mult) << 16);
 }
 
+// ---- Values that a kernel has computed in fp32 and quantises at once.  They do not sit on ties more often than any
+// number does, so their quotients are not put back on them, and the scale is m times the rounded 1 / 448 (off by one
+// unit at most): a quotient within 2^-20 of a tie may take either neighbour, as for fp32 rows above.
+
+// Two fp32 values in a register pair: one instruction on both is half the issue slots, which bound
+// the elementwise kernels that quantise.
+__device__ __forceinline__ uint64_t two(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void apart(uint64_t v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
+// The largest finite magnitude of N values, and whether one of any lane's is infinite: a NaN loses every comparison,
+// so only then (a branch of the whole warp) are the values looked at one by one.
+template <int N>
+__device__ __forceinline__ float finite_max(const float* v, bool& infinite) {
+  float m = 0.0f;
+#pragma unroll
+  for (int j = 0; j < N; ++j) m = fmaxf(m, fabsf(v[j]));
+  infinite = __any_sync(0xffffffffu, m > 3.402823466e38f);
+  if (infinite) {
+    m = 0.0f;
+#pragma unroll
+    for (int j = 0; j < N; ++j) m = fmaxf(m, finite_abs(v[j]));
+  }
+  return m;
+}
+
+// The reciprocal of m / 256, so that it is a normal number whatever the m.
+__device__ __forceinline__ BlockScale computed_scale(float m) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(m * 0.00390625f));
+  const bool tiny = m < 7.888609052210118e-31f;
+  return {tiny ? 0.0f : m * (1.0f / kMaxE4m3), tiny ? 0.0f : r * (kMaxE4m3 * 0.00390625f)};
+}
+
+// N values times mult -> E4M3 codes, element 0 in the lowest byte of w[0].  The conversion saturates, so infinities, of
+// which finite_max told, become NaN first.
+template <int N>
+__device__ __forceinline__ void encode_computed(const float* v, float mult, bool infinite, uint32_t (&w)[(N + 3) / 4]) {
+  if (infinite) {
+    float t[N];
+#pragma unroll
+    for (int j = 0; j < N; ++j) t[j] = fabsf(v[j]) > 3.402823466e38f ? __int_as_float(0x7fffffff) : v[j] * mult;
+#pragma unroll
+    for (int i = 0; i < (N + 3) / 4; ++i) {
+      w[i] = 0;
+#pragma unroll
+      for (int j = 4 * i; j < N && j < 4 * i + 4; ++j)
+        w[i] |= ((uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(t[j], 0.0f), __NV_SATFINITE, __NV_E4M3) & 0xffu) << (8 * (j - 4 * i));
+    }
+    return;
+  }
+  const uint64_t m = two(mult, mult);
+#pragma unroll
+  for (int i = 0; i < (N + 3) / 4; ++i) {
+    w[i] = 0;
+#pragma unroll
+    for (int j = 4 * i; j < N && j < 4 * i + 4; j += 2) {
+      float q0, q1;
+      apart(mul2(two(v[j], j + 1 < N ? v[j + 1] : 0.0f), m), q0, q1);
+      w[i] |= (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(q0, q1), __NV_SATFINITE, __NV_E4M3) << (8 * (j - 4 * i));
+    }
+  }
+}
+
 template <int DT>
 __device__ __forceinline__ float load1(const void* p, int64_t i) {
   if (DT == kDtBf16) return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);

@@ -436,7 +436,7 @@ __device__ __forceinline__ void gated_split_end(const BlockParams& p, uint8_t* s
   for (int i = threadIdx.x; i < n; i += kBThreads) {
     const int r = i >> lgq, j = c0 + 4 * (i & ((1 << lgq) - 1)), col = nt * 128 + j;
     if (col >= I) continue;
-    const BlockScale sc = block_scale(row_amax[r]);
+    const BlockScale sc = computed_scale(row_amax[r]);
     const float4 hv = hbuf[i];
     const float h[4] = {hv.x, hv.y, hv.z, hv.w};
     uint32_t w[1];
@@ -834,9 +834,8 @@ __global__ void __launch_bounds__(kBThreads, 1)
         if (a.codes != nullptr) {
           // a block of 128 columns of h: this warp's 64 and those of the warp that has the other half of the tile
           const int w = warp - kBFirstEpiWarp;
-          float m = 0.0f;
-#pragma unroll
-          for (int i = 0; i < 64; ++i) m = fmaxf(m, finite_abs(h[i]));
+          bool infinite;
+          float m = finite_max<64>(h, infinite);
           if (!sums_wait(amax_empty(w), amax_phase ^ 1u, sync)) {
             ok = false;
             break;
@@ -852,13 +851,13 @@ __global__ void __launch_bounds__(kBThreads, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive(amax_empty(w ^ 4));
           amax_phase ^= 1u;
-          const BlockScale sc = block_scale(m);
+          const BlockScale sc = computed_scale(m);
           if (any && valid) {
             uint8_t* dst = a.codes + row * cols + col0;
 #pragma unroll
             for (int i = 0; i < 64; i += 16) {
               uint32_t q[4];
-              encode<16>(h + i, sc.mult, q);
+              encode_computed<16>(h + i, sc.mult, infinite, q);
               if (col0 + i < cols) *reinterpret_cast<uint4*>(dst + i) = make_uint4(q[0], q[1], q[2], q[3]);
             }
             if (half == 0) a.scales[row * NT + hd.z] = sc.scale;

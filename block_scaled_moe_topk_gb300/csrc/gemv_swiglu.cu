@@ -128,7 +128,7 @@ __global__ void __launch_bounds__(kGsThreads) gemv_swiglu_kernel(const __grid_co
     float v = block_max[m][lane % kGsCluster];
 #pragma unroll
     for (int o = kGsCluster / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-    const BlockScale sc = block_scale(v);
+    const BlockScale sc = computed_scale(v);
     if (lane != 0 || j >= I || r0 + m >= a.M) continue;
     a.codes[(r0 + m) * I + j] = (uint8_t)encode2(h[m], 0.0f, sc.mult);
     if (j % kFp8Block == 0) a.scales[(r0 + m) * ((I + kFp8Block - 1) / kFp8Block) + j / kFp8Block] = sc.scale;

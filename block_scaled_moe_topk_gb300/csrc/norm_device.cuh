@@ -118,27 +118,25 @@ __device__ __forceinline__ void put_fp8(uint8_t* codes, float* scales, int64_t r
                                         const float (&v)[8]) {
   const int HB = (H + kFp8Block - 1) / kFp8Block;
   if (VEC) {  // 16 lanes a block
-    float m = 0.0f;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) m = fmaxf(m, finite_abs(v[j]));
-    const BlockScale sc = block_scale(lanes_max(m, 16));
-    if (!on || c >= H) return;
+    bool infinite;
+    const BlockScale sc = computed_scale(lanes_max(finite_max<8>(v, infinite), 16));
     uint32_t w[2];
-    encode<8>(v, sc.mult, w);
+    encode_computed<8>(v, sc.mult, infinite, w);
+    if (!on || c >= H) return;
     *reinterpret_cast<uint2*>(codes + row * H + c) = make_uint2(w[0], w[1]);
     if ((c & (kFp8Block - 1)) == 0) scales[row * HB + c / kFp8Block] = sc.scale;
     return;
   }
 #pragma unroll
   for (int b = 0; b < 2; ++b) {  // four elements of every lane a block
-    float m = 0.0f;
-#pragma unroll
-    for (int j = 4 * b; j < 4 * b + 4; ++j) m = fmaxf(m, finite_abs(v[j]));
-    const BlockScale sc = block_scale(lanes_max(m, 32));
+    bool infinite;
+    const BlockScale sc = computed_scale(lanes_max(finite_max<4>(v + 4 * b, infinite), 32));
+    uint32_t w[1];
+    encode_computed<4>(v + 4 * b, sc.mult, infinite, w);
     const int c0 = c + 128 * b;
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-      if (on && c0 + 32 * j < H) codes[row * H + c0 + 32 * j] = (uint8_t)encode2(v[4 * b + j], 0.0f, sc.mult);
+      if (on && c0 + 32 * j < H) codes[row * H + c0 + 32 * j] = (uint8_t)(w[0] >> (8 * j));
     if (on && c0 < H && (c0 & (kFp8Block - 1)) == 0) scales[row * HB + c0 / kFp8Block] = sc.scale;
   }
 }

@@ -29,7 +29,7 @@ struct NormParams {
 
 // NCH chunks of 8 columns a thread; QF: how y is quantised.
 template <int DT, bool VEC, int NCH, int QF, int THREADS>
-__global__ void __launch_bounds__(THREADS) rms_norm_kernel(const __grid_constant__ NormParams p) {
+__global__ void __launch_bounds__(THREADS, 1) rms_norm_kernel(const __grid_constant__ NormParams p) {
   const NormArgs& a = p.a;
   const int H = a.H, tpr = p.tpr;
   const int rb = p.rpb == 1 ? 0 : threadIdx.x / tpr;

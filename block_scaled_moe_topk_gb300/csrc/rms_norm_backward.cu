@@ -86,7 +86,7 @@ __device__ __forceinline__ void load_weight(const NormBackwardArgs& a, int col, 
 
 // Rows through the ring.  Shared memory: [stage][array][chunk half][thread] of 16 bytes.
 template <int DT, bool DRES>
-__global__ void __launch_bounds__(kNbMaxThreads) norm_backward_ring_kernel(const __grid_constant__ NormBackwardParams p) {
+__global__ void __launch_bounds__(kNbMaxThreads, 1) norm_backward_ring_kernel(const __grid_constant__ NormBackwardParams p) {
   constexpr int NCH = 4, kParts = DT == kDtF32 ? 2 : 1, kArrays = DRES ? 3 : 2;
   extern __shared__ __align__(16) uint8_t ring[];
   const NormBackwardArgs& a = p.a;
@@ -179,7 +179,7 @@ __global__ void __launch_bounds__(kNbMaxThreads) norm_backward_ring_kernel(const
 
 // Rows read directly.
 template <int DT, bool VEC>
-__global__ void __launch_bounds__(kNbMaxThreads) norm_backward_kernel(const __grid_constant__ NormBackwardParams p) {
+__global__ void __launch_bounds__(kNbMaxThreads, 1) norm_backward_kernel(const __grid_constant__ NormBackwardParams p) {
   constexpr int NCH = 8;
   extern __shared__ __align__(16) uint8_t ring[];
   const NormBackwardArgs& a = p.a;

@@ -1,8 +1,9 @@
 """The gated activation's gradient against fp64, in both layouts, as values and as FP8 codes.
 
-u = 2^-24.  The logistic function is off by d(g) = (2 + 1.173 |g| + 2 + 1) 2^-23 of itself (the documented bounds of
-the exponential and the division, an addition and a multiplication).  d_up = dh g sig: d + 3u.  d_gate = dh u sig (1 + g (1 - sig)): the
-bracket is off by |g| (sig d + 2u) + 2u and the rest by d + 4u of itself.
+u = 2^-24.  The logistic function's exponent is off by 2^-23 |g| (a product and a rounded constant), its exponential and
+reciprocal by 2^-22.5 and 2^-23 (PTX's bounds), its addition by u: together below d(g) = (5 + 1.173 |g|) 2^-23 of
+itself, and a result below 2^-126 is 0: d sig + 2^-126 in all.  d_up = dh g sig: d + 3u.  d_gate = dh u sig (1 + g (1 -
+sig)): the bracket is off by |g| (sig d + 2u) + 2u and the rest by d + 4u of itself.
 """
 import pytest
 import torch
@@ -41,7 +42,10 @@ def gradient64(gate_up, dh, layout):
         a, b = halves(out, layout)
         a.copy_(gate)
         b.copy_(up)
-    return grad, bound + 1e-37
+    # 2^-126 on the logistic function, times what it multiplies; products below fp32's normal numbers, 2^-149 each
+    for out, lost in zip(halves(bound, layout), ((d * u).abs() * (1 + g.abs()) + 1, (d * g).abs() + 1)):
+        out.add_(lost * 2.0 ** -126)
+    return grad, bound
 
 
 def check_codes(codes, scales, v, off):
