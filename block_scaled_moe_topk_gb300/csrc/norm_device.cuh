@@ -54,6 +54,35 @@ __device__ __forceinline__ void load8(const void* x, int64_t base, int c, int n,
   }
 }
 
+// The same as they lie in memory, 16 bytes of 16-bit elements in four registers, for kernels that hold several chunks.
+template <int DT>
+struct Raw8 {
+  uint32_t w[DT == kDtF32 ? 8 : 4];
+};
+template <int DT>
+__device__ __forceinline__ Raw8<DT> raw8(const void* x, int64_t base, int c, int n) {
+  Raw8<DT> r;
+#pragma unroll
+  for (int i = 0; i < (DT == kDtF32 ? 2 : 1); ++i) {
+    uint4 v = make_uint4(0, 0, 0, 0);
+    if (c < n) v = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(x) + (base + c) * (DT == kDtF32 ? 4 : 2))[i];
+    r.w[4 * i] = v.x, r.w[4 * i + 1] = v.y, r.w[4 * i + 2] = v.z, r.w[4 * i + 3] = v.w;
+  }
+  return r;
+}
+// Elements 2i and 2i + 1.
+template <int DT>
+__device__ __forceinline__ void raw_pair(const Raw8<DT>& r, int i, float& lo, float& hi) {
+  if (DT == kDtF32) {
+    lo = __uint_as_float(r.w[(2 * i) & (DT == kDtF32 ? 7 : 3)]), hi = __uint_as_float(r.w[(2 * i + 1) & (DT == kDtF32 ? 7 : 3)]);
+  } else if (DT == kDtBf16) {
+    lo = __uint_as_float(r.w[i] << 16), hi = __uint_as_float(r.w[i] & 0xFFFF0000u);
+  } else {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&r.w[i]));
+    lo = f.x, hi = f.y;
+  }
+}
+
 template <int DT>
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   if (DT == kDtBf16) {

@@ -32,7 +32,7 @@ template <int DT, bool VEC, int NCH, int QF, int THREADS>
 __global__ void __launch_bounds__(THREADS, 1) rms_norm_kernel(const __grid_constant__ NormParams p) {
   const NormArgs& a = p.a;
   const int H = a.H, tpr = p.tpr;
-  const int rb = p.rpb == 1 ? 0 : threadIdx.x / tpr;
+  const int rb = tpr >= (int)blockDim.x ? 0 : threadIdx.x / tpr;
   const int i = threadIdx.x - rb * tpr;  // this thread among the row's
   const int64_t row = (int64_t)blockIdx.x * p.rpb + rb;
   const bool on = rb < p.rpb && row < a.T;  // half a warp may be left over

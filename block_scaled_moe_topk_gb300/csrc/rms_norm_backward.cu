@@ -18,6 +18,7 @@ namespace {
 
 constexpr int kNbThreads = 256;     // of a block that holds several rows
 constexpr int kNbMaxThreads = 512;
+constexpr int kNbHeldThreads = 448;  // with the weight in registers, two blocks an SM
 constexpr int kNbMaxStages = 4;
 constexpr int kNbRingBytes = 108 * 1024;  // a block's share of an SM that holds two
 constexpr int kNbMaxRing = 216 * 1024;
@@ -54,28 +55,31 @@ __device__ __forceinline__ float row_sum_again(float v, int tpr, int rb, int tur
   return v;
 }
 
-// The block's sums of dw: the row groups' own sums meet in shared memory, in the groups' order.
-template <bool VEC, int NCH>
-__device__ __forceinline__ void leave_dw(const NormBackwardParams& p, const ColumnMap<VEC>& map, int rb, float* sums,
-                                         const float (&dw)[NCH][8]) {
-  const int H = p.a.H;
-  float* out = p.a.partial + (int64_t)blockIdx.x * H;
-  for (int g = 0; g < p.rpb; ++g) {
-    if (p.rpb > 1) __syncthreads();
-    if (g != rb) continue;
-    const bool last = g == p.rpb - 1;
+// The block's sums of dw, N columns a thread, the q-th at column col(q).  Rows that share a warp meet by shuffles, the
+// warps (or groups of warps) of different rows in shared memory, one after the other: the same order every time.
+template <int N, typename Col>
+__device__ __forceinline__ void leave_dw(const NormBackwardParams& p, Col col, float* sums, float (&dw)[N]) {
+  const int H = p.a.H, tpr = p.tpr, lane = threadIdx.x & 31;
 #pragma unroll
-    for (int c = 0; c < NCH; ++c)
+  for (int o = 16; o > 0; o >>= 1)
+    if (o >= tpr) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int col = map.col(c) + (VEC ? j : 32 * j);
-        if (col >= H) continue;
-        float v = dw[c][j];
-        if (g > 0) v += sums[col];
-        if (last) out[col] = v;
-        else sums[col] = v;
+      for (int q = 0; q < N; ++q) dw[q] += __shfl_xor_sync(0xffffffffu, dw[q], o);
+    }
+  const int per = max(tpr, 32), groups = (blockDim.x + per - 1) / per, mine = threadIdx.x / per;
+  for (int g = 0; g < groups; ++g) {
+    if (g == mine && (tpr >= 32 || lane < tpr)) {
+#pragma unroll
+      for (int q = 0; q < N; ++q) {
+        const int c = col(q);
+        if (c < H) sums[c] = g > 0 ? sums[c] + dw[q] : dw[q];
       }
+    }
+    __syncthreads();
   }
+  // a thread's own columns are 16 bytes or more apart from its neighbour's: the row leaves in order instead
+  float* out = p.a.partial + (int64_t)blockIdx.x * H;
+  for (int c = threadIdx.x; c < H; c += blockDim.x) out[c] = sums[c];
 }
 
 template <int DT, bool VEC>
@@ -84,97 +88,145 @@ __device__ __forceinline__ void load_weight(const NormBackwardArgs& a, int col, 
   else load8<kDtF32, VEC>(a.weight, 0, col, a.H, w);
 }
 
-// Rows through the ring.  Shared memory: [stage][array][chunk half][thread] of 16 bytes.
-template <int DT, bool DRES>
-__global__ void __launch_bounds__(kNbMaxThreads, 1) norm_backward_ring_kernel(const __grid_constant__ NormBackwardParams p) {
-  constexpr int NCH = 4, kParts = DT == kDtF32 ? 2 : 1, kArrays = DRES ? 3 : 2;
+// Rows through the ring.  A thread owns pieces of 16 bytes (8 columns of 16-bit rows, 4 of fp32 ones), neighbouring
+// threads neighbouring pieces.  Shared memory: [stage][array][piece][thread] of 16 bytes.
+template <int DT, bool DRES, int NCH, int THREADS, int BLOCKS>
+__global__ void __launch_bounds__(THREADS, BLOCKS) norm_backward_ring_kernel(const __grid_constant__ NormBackwardParams p) {
+  constexpr int kArrays = DRES ? 3 : 2, es = DT == kDtF32 ? 4 : 2, EP = 16 / es, NP = NCH * 8 / EP;
+  constexpr bool kHoldWeight = NCH <= 2;  // in registers; else from L1 every time
   extern __shared__ __align__(16) uint8_t ring[];
   const NormBackwardArgs& a = p.a;
-  const int H = a.H, tpr = p.tpr, es = DT == kDtF32 ? 4 : 2;
-  const int rb = p.rpb == 1 ? 0 : threadIdx.x / tpr;
-  const int i = threadIdx.x - rb * tpr;
-  const ColumnMap<true> map(i, tpr);
-  const uint32_t ring0 = (uint32_t)__cvta_generic_to_shared(ring);
+  const int H = a.H, tpr = p.tpr;
+  const int rb = tpr >= (int)blockDim.x ? 0 : threadIdx.x / tpr;
+  const int first = (threadIdx.x - rb * tpr) * EP;
+  auto col = [&](int q) { return first + q * tpr * EP; };
+  const uint32_t ring0 = (uint32_t)__cvta_generic_to_shared(ring) + threadIdx.x * 16u;
   const int64_t step = (int64_t)gridDim.x * p.rpb;
-  const int64_t first = (int64_t)blockIdx.x * p.rpb;  // of the block; every row group makes the same rounds
-  const uint32_t slot_bytes = kArrays * NCH * kParts * blockDim.x * 16;
-  auto at = [&](int array, int c, int h) { return (uint32_t)(((array * NCH + c) * kParts + h) * blockDim.x + threadIdx.x) * 16u; };
-  auto fetch = [&](int64_t base, int slot) {
-    const int64_t row = base + rb;
-    const bool on = base < a.T && rb < p.rpb && row < a.T;
+  const uint32_t piece = blockDim.x * 16u, array = NP * piece, slot_bytes = kArrays * array;
+  int64_t ahead = (int64_t)blockIdx.x * p.rpb + rb;  // the next row to fetch; every row group makes the same rounds
+  const bool group = rb < p.rpb;
+  auto fetch = [&](uint32_t dst) {
+    const bool on = group && ahead < a.T;
+    const int64_t r = on ? ahead : 0;
+    const uint8_t* dy = static_cast<const uint8_t*>(a.dy) + r * a.dy_stride * es;
+    const uint8_t* x = static_cast<const uint8_t*>(a.x) + r * a.x_stride * es;
+    const uint8_t* dres = DRES ? static_cast<const uint8_t*>(a.dres) + r * a.dres_stride * es : nullptr;
 #pragma unroll
-    for (int c = 0; c < NCH; ++c)
-#pragma unroll
-      for (int h = 0; h < kParts; ++h) {
-        const int col = map.col(c) + 4 * h;
-        const bool in = on && col < H;
-        const uint32_t dst = ring0 + slot * slot_bytes;
-        const int64_t o = in ? col : 0, r = in ? row : 0;
-        copy16(dst + at(0, c, h), static_cast<const uint8_t*>(a.dy) + (r * a.dy_stride + o) * es, in);
-        copy16(dst + at(1, c, h), static_cast<const uint8_t*>(a.x) + (r * a.x_stride + o) * es, in);
-        if (DRES) copy16(dst + at(2, c, h), static_cast<const uint8_t*>(a.dres) + (r * a.dres_stride + o) * es, in);
-      }
+    for (int q = 0; q < NP; ++q) {
+      const bool in = on && col(q) < H;
+      const uint32_t o = in ? (uint32_t)(col(q) * es) : 0u, at = dst + (uint32_t)q * piece;
+      copy16(at, dy + o, in);
+      copy16(at + array, x + o, in);
+      if (DRES) copy16(at + 2 * array, dres + o, in);
+    }
     copy_commit();
+    ahead += step;
   };
-  auto read = [&](int slot, int array, int c, float (&v)[8]) {
-    const uint8_t* src = ring + slot * slot_bytes;
-    const uint4 u = *reinterpret_cast<const uint4*>(src + at(array, c, 0));
-    if (DT == kDtF32) {
-      const uint4 t = *reinterpret_cast<const uint4*>(src + at(array, c, kParts - 1));
-      v[0] = __uint_as_float(u.x), v[1] = __uint_as_float(u.y), v[2] = __uint_as_float(u.z), v[3] = __uint_as_float(u.w);
-      v[4] = __uint_as_float(t.x), v[5] = __uint_as_float(t.y), v[6] = __uint_as_float(t.z), v[7] = __uint_as_float(t.w);
+  auto read = [&](uint32_t src, int which, int q) {
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(src + which * array + (uint32_t)q * piece) : "memory");
+    return v;
+  };
+  // elements 2j and 2j + 1 of a piece
+  auto pair = [&](const uint4& v, int j) {
+    const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+    if (DT == kDtF32) return two(__uint_as_float(u[(2 * j) & 3]), __uint_as_float(u[(2 * j + 1) & 3]));
+    if (DT == kDtBf16) return two(__uint_as_float(u[j] << 16), __uint_as_float(u[j] & 0xFFFF0000u));
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&u[j]));
+    return two(f.x, f.y);
+  };
+  float w[NP][EP];
+  auto weight = [&](int q) {
+    const int c = col(q);
+#pragma unroll
+    for (int j = 0; j < EP; ++j) w[q][j] = 0.0f;
+    if (c >= H) return;
+    if (DT != kDtF32 && a.weight_dtype == DT) {
+      const uint4 v = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.weight) + c);
+#pragma unroll
+      for (int j = 0; j < EP / 2; ++j) apart(pair(v, j), w[q][2 * j], w[q][2 * j + 1]);
     } else {
-      unpack8<DT>(u, v);
+#pragma unroll
+      for (int j = 0; j < EP; j += 4) {
+        const float4 v = *reinterpret_cast<const float4*>(static_cast<const float*>(a.weight) + c + j);
+        w[q][j] = v.x, w[q][j + 1] = v.y, w[q][j + 2] = v.z, w[q][j + 3] = v.w;
+      }
     }
   };
-  float dw[NCH][8] = {};
-  for (int s = 0; s < p.stages; ++s) fetch(first + s * step, s);
+  auto weight_pair = [&](int q, int j) { return two(w[q][2 * j], w[q][2 * j + 1]); };
+  if (kHoldWeight) {
+#pragma unroll
+    for (int q = 0; q < NP; ++q) weight(q);
+  }
+  uint64_t dw[NP][EP / 2] = {};
+  for (int s = 0; s < p.stages; ++s) fetch(ring0 + s * slot_bytes);
   int slot = 0, turn = 0;
-  for (int64_t base = first; base < a.T; base += step) {
-    const int64_t row = base + rb;
-    const bool on = rb < p.rpb && row < a.T;
-    const float rstd = on ? a.rstd[row] : 0.0f;
+  const float inv_h = 1.0f / (float)H;
+  int64_t row = (int64_t)blockIdx.x * p.rpb + rb;
+  float next = group && row < a.T ? a.rstd[row] : 0.0f;  // the next round's rstd
+  for (int64_t base = (int64_t)blockIdx.x * p.rpb; base < a.T; base += step, row += step) {
+    const bool on = group && row < a.T;
+    const float rstd = next;
+    next = group && row + step < a.T ? a.rstd[row + step] : 0.0f;
     // one group of copies a round, in the rows' order: this round's is complete when at most stages - 1 are not
     if (p.stages == 4) copy_wait<3>();
     else if (p.stages == 3) copy_wait<2>();
     else copy_wait<1>();
-    float dot = 0.0f;
+    const uint32_t src = ring0 + slot * slot_bytes;
+    const uint64_t rstd2 = two(rstd, rstd);
+    uint64_t dot2 = two(0.0f, 0.0f);
 #pragma unroll
-    for (int c = 0; c < NCH; ++c) {
-      float w[8], dy[8], x[8];
-      load_weight<DT, true>(a, map.col(c), w);
-      read(slot, 0, c, dy);
-      read(slot, 1, c, x);
+    for (int q = 0; q < NP; ++q) {
+      if (!kHoldWeight) weight(q);
+      const uint4 dy = read(src, 0, q), x = read(src, 1, q);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float t = dy[j] * (x[j] * rstd);
-        dw[c][j] += t;
-        dot = fmaf(w[j], t, dot);
+      for (int j = 0; j < EP / 2; ++j) {
+        const uint64_t t = mul2(pair(dy, j), mul2(pair(x, j), rstd2));
+        dw[q][j] = add2(dw[q][j], t);
+        dot2 = fma2(weight_pair(q, j), t, dot2);
       }
     }
-    dot = row_sum_again(dot, tpr, rb, turn) / (float)H;
+    float lo, hi;
+    apart(dot2, lo, hi);
+    const float dot = row_sum_again(lo + hi, tpr, rb, turn) * inv_h;
     turn ^= 1;
+    const float k = -(rstd * rstd) * dot;
+    const uint64_t k2 = two(k, k);
 #pragma unroll
-    for (int c = 0; c < NCH; ++c) {
-      float w[8], dy[8], x[8], dres[8];
-      load_weight<DT, true>(a, map.col(c), w);
-      read(slot, 0, c, dy);
-      read(slot, 1, c, x);
-      if (DRES) read(slot, 2, c, dres);
+    for (int q = 0; q < NP; ++q) {
+      if (!kHoldWeight) weight(q);
+      const uint4 dy = read(src, 0, q), x = read(src, 1, q);
+      uint4 dres = dy;
+      if (DRES) dres = read(src, 2, q);
+      float v[EP];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        dy[j] = rstd * (w[j] * dy[j] - x[j] * rstd * dot);
-        if (DRES) dy[j] += dres[j];
+      for (int j = 0; j < EP / 2; ++j) {
+        uint64_t t = mul2(pair(x, j), k2);
+        if (DRES) t = add2(t, pair(dres, j));
+        apart(fma2(mul2(weight_pair(q, j), pair(dy, j)), rstd2, t), v[2 * j], v[2 * j + 1]);
       }
-      store8<DT, true>(a.dx, row * a.dx_stride, map.col(c), on ? H : 0, dy);
+      if (on && col(q) < H) {
+        uint4 r;
+        if constexpr (DT == kDtF32)
+          r = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+        else
+          r = make_uint4(pack2<DT>(v[0], v[1]), pack2<DT>(v[2], v[3]), pack2<DT>(v[4], v[5]), pack2<DT>(v[6], v[7]));
+        *reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.dx) + (row * a.dx_stride + col(q)) * es) = r;
+      }
     }
-    fetch(base + p.stages * step, slot);
+    fetch(src);
     if (++slot == p.stages) slot = 0;
   }
   copy_wait<0>();
   if (a.dw == nullptr) return;
   __syncthreads();  // the ring is free
-  leave_dw<true, NCH>(p, map, rb, reinterpret_cast<float*>(ring), dw);
+  float sums[NP * EP];
+#pragma unroll
+  for (int q = 0; q < NP; ++q)
+#pragma unroll
+    for (int j = 0; j < EP / 2; ++j) apart(dw[q][j], sums[q * EP + 2 * j], sums[q * EP + 2 * j + 1]);
+  leave_dw<NP * EP>(p, [&](int q) { return col(q / EP) + q % EP; }, reinterpret_cast<float*>(ring), sums);
 }
 
 // Rows read directly.
@@ -184,7 +236,7 @@ __global__ void __launch_bounds__(kNbMaxThreads, 1) norm_backward_kernel(const _
   extern __shared__ __align__(16) uint8_t ring[];
   const NormBackwardArgs& a = p.a;
   const int H = a.H, tpr = p.tpr;
-  const int rb = p.rpb == 1 ? 0 : threadIdx.x / tpr;
+  const int rb = tpr >= (int)blockDim.x ? 0 : threadIdx.x / tpr;
   const int i = threadIdx.x - rb * tpr;
   const ColumnMap<VEC> map(i, tpr);
   float dw[NCH][8] = {};
@@ -230,23 +282,34 @@ __global__ void __launch_bounds__(kNbMaxThreads, 1) norm_backward_kernel(const _
     }
   }
   if (a.dw == nullptr) return;
-  leave_dw<VEC, NCH>(p, map, rb, reinterpret_cast<float*>(ring), dw);
+  float sums[NCH * 8];
+#pragma unroll
+  for (int q = 0; q < NCH * 8; ++q) sums[q] = dw[q / 8][q % 8];
+  leave_dw<NCH * 8>(p, [&](int q) { return map.col(q / 8) + (VEC ? 1 : 32) * (q % 8); }, reinterpret_cast<float*>(ring), sums);
 }
 
-// dw[c] = the blocks' sums of column c.  32 columns a block, 16 threads a column.
+// dw[c] = the blocks' sums of column c.  32 columns a block, 16 threads a column, each with all its loads in flight.
 constexpr int kSumWays = 16;
-__global__ void __launch_bounds__(32 * kSumWays) norm_weight_sum_kernel(const float* partial, int parts, int H, float* dw) {
+constexpr int kNbParts = 2 * 152;  // the most blocks: two an SM
+__global__ void __launch_bounds__(32 * kSumWays, 1) norm_weight_sum_kernel(const float* partial, int parts, int H, float* dw) {
   __shared__ float sums[kSumWays][32];
   const int lane = threadIdx.x & 31, way = threadIdx.x >> 5, col = blockIdx.x * 32 + lane;
-  float v = 0.0f;
-  if (col < H)
-    for (int q = way; q < parts; q += kSumWays) v += partial[(int64_t)q * H + col];
-  sums[way][lane] = v;
+  constexpr int kEach = kNbParts / kSumWays;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  float v[kEach], sum = 0.0f;
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    const int q = way + i * kSumWays;
+    v[i] = col < H && q < parts ? partial[(int64_t)q * H + col] : 0.0f;
+  }
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) sum += v[i];
+  sums[way][lane] = sum;
   __syncthreads();
   if (way > 0 || col >= H) return;
 #pragma unroll
-  for (int q = 1; q < kSumWays; ++q) v += sums[q][lane];
-  dw[col] = v;
+  for (int q = 1; q < kSumWays; ++q) sum += sums[q][lane];
+  dw[col] = sum;
 }
 
 struct Shape {
@@ -277,13 +340,19 @@ cudaError_t allow_smem(K kernel, std::atomic<int> (&ready)[64]) {
   return err;
 }
 
-template <int DT, bool DRES>
-cudaError_t launch_ring(const NormBackwardParams& p, int grid, int threads, int64_t smem, cudaStream_t s) {
+template <int DT, bool DRES, int NCH, int THREADS, int BLOCKS>
+cudaError_t launch_kernel(const NormBackwardParams& p, int grid, int threads, int64_t smem, cudaStream_t s) {
   static std::atomic<int> ready[64];
-  const cudaError_t err = allow_smem(norm_backward_ring_kernel<DT, DRES>, ready);
+  const cudaError_t err = allow_smem(norm_backward_ring_kernel<DT, DRES, NCH, THREADS, BLOCKS>, ready);
   if (err != cudaSuccess) return err;
-  norm_backward_ring_kernel<DT, DRES><<<grid, threads, smem, s>>>(p);
+  norm_backward_ring_kernel<DT, DRES, NCH, THREADS, BLOCKS><<<grid, threads, smem, s>>>(p);
   return cudaGetLastError();
+}
+
+template <int DT, int NCH, int THREADS, int BLOCKS>
+cudaError_t launch_ring(const NormBackwardParams& p, int grid, int threads, int64_t smem, cudaStream_t s) {
+  return p.a.dres != nullptr ? launch_kernel<DT, true, NCH, THREADS, BLOCKS>(p, grid, threads, smem, s)
+                             : launch_kernel<DT, false, NCH, THREADS, BLOCKS>(p, grid, threads, smem, s);
 }
 
 template <int DT>
@@ -291,9 +360,10 @@ cudaError_t launch_typed(const NormBackwardArgs& a, bool vec, cudaStream_t s) {
   NormBackwardParams p{a, 0, 1, 0};
   const int chunks = vec ? (a.H + 7) / 8 : (a.H + 255) / 256 * 32;
   const int64_t es = DT == kDtF32 ? 4 : 2, arrays = a.dres != nullptr ? 3 : 2;
-  Shape sh = shape_of(chunks, 4, vec, a.T);
+  const int nch = chunks <= 2 * kNbHeldThreads ? 2 : 4;
+  Shape sh = shape_of(chunks, nch, vec, a.T);
   int threads = (sh.tpr * sh.rpb + 31) / 32 * 32;
-  const int64_t stage = arrays * 4 * 8 * es * threads;
+  const int64_t stage = arrays * nch * 8 * es * threads;
   p.stages = (int)std::min<int64_t>(kNbMaxStages, kNbRingBytes / stage);
   if (p.stages < 2) p.stages = (int)std::min<int64_t>(kNbMaxStages, kNbMaxRing / stage);
   cudaError_t err;
@@ -301,9 +371,9 @@ cudaError_t launch_typed(const NormBackwardArgs& a, bool vec, cudaStream_t s) {
     p.tpr = sh.tpr;
     p.rpb = sh.rpb;
     const int grid = (int)std::min<int64_t>(norm_backward_parts(a.T, a.H), (a.T + sh.rpb - 1) / sh.rpb);
-    const int64_t smem = std::max<int64_t>(p.stages * stage, sh.rpb > 1 ? 4 * (int64_t)a.H : 0);
-    err = a.dres != nullptr ? launch_ring<DT, true>(p, grid, threads, smem, s)
-                            : launch_ring<DT, false>(p, grid, threads, smem, s);
+    const int64_t smem = std::max<int64_t>(p.stages * stage, 4 * (int64_t)a.H);
+    err = nch == 2 ? launch_ring<DT, 2, kNbHeldThreads, 2>(p, grid, threads, smem, s)
+                   : launch_ring<DT, 4, kNbMaxThreads, 1>(p, grid, threads, smem, s);
     p.stages = grid;
   } else {
     sh = shape_of(chunks, 8, vec, a.T);
@@ -311,21 +381,33 @@ cudaError_t launch_typed(const NormBackwardArgs& a, bool vec, cudaStream_t s) {
     p.rpb = sh.rpb;
     threads = (sh.tpr * sh.rpb + 31) / 32 * 32;
     const int grid = (int)std::min<int64_t>(norm_backward_parts(a.T, a.H), (a.T + sh.rpb - 1) / sh.rpb);
-    const int64_t smem = sh.rpb > 1 ? 4 * (int64_t)a.H : 0;  // rows of at most 8 K columns share a block
+    const int64_t smem = 4 * (int64_t)a.H;
+    static std::atomic<int> ready[2][64];
+    err = vec ? allow_smem(norm_backward_kernel<DT, true>, ready[0]) : allow_smem(norm_backward_kernel<DT, false>, ready[1]);
+    if (err != cudaSuccess) return err;
     if (vec) norm_backward_kernel<DT, true><<<grid, threads, smem, s>>>(p);
     else norm_backward_kernel<DT, false><<<grid, threads, smem, s>>>(p);
     err = cudaGetLastError();
     p.stages = grid;
   }
   if (err != cudaSuccess || a.dw == nullptr) return err;
-  norm_weight_sum_kernel<<<(a.H + 31) / 32, 32 * kSumWays, 0, s>>>(a.partial, p.stages, a.H, a.dw);
-  return cudaGetLastError();
+  // launched while the first kernel ends; it waits for it before it reads
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((a.H + 31) / 32));
+  cfg.blockDim = dim3(32 * kSumWays);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, norm_weight_sum_kernel, (const float*)a.partial, p.stages, a.H, a.dw);
 }
 
 }  // namespace
 
 // Two blocks an SM of the 152, fewer for fewer rows.
-int norm_backward_parts(int64_t T, int) { return (int)std::min<int64_t>(T, 2 * 152); }
+int norm_backward_parts(int64_t T, int) { return (int)std::min<int64_t>(T, kNbParts); }
 
 cudaError_t launch_rms_norm_backward(const NormBackwardArgs& a, cudaStream_t s) {
   if (a.T == 0) return a.dw != nullptr ? cudaMemsetAsync(a.dw, 0, (size_t)a.H * 4, s) : cudaSuccess;
