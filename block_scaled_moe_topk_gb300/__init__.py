@@ -632,18 +632,17 @@ def _rows_at(t, shape, dt, dev, where, name):
     """Pointer and row stride of a matrix of that shape and type; (None, 0) without one."""
     if t is None:
         return None, 0
-    st = _row_stride(t, dev, t.shape)
-    if not (st and t.dtype is dt and t.shape == shape):
-        _matrix(t, dev, where, name, shape, (dt,))
-        st = _stride(t)
-    return t.data_ptr(), st
+    if t.dtype is dt and t.get_device() == dev and t.is_contiguous() and t.shape == shape:
+        return t.data_ptr(), shape[1]
+    _matrix(t, dev, where, name, shape, (dt,))
+    return t.data_ptr(), _stride(t)
 
 
 def _flat_at(t, shape, dt, dev, where, name):
     """Pointer of a contiguous tensor of that shape and type; None without one."""
     if t is None:
         return None
-    if not (_fixed(t, dev, dt) and t.shape == shape):
+    if not (t.dtype is dt and t.get_device() == dev and t.is_contiguous() and t.shape == shape):
         _table(t, dev, dt, shape, where, name)
     return t.data_ptr()
 
@@ -652,23 +651,38 @@ def _norm_rows(fn, x, weight):
     """What a norm's rows and weight have to be: (shape, type, device, row stride, the weight's type)."""
     _want(weight is not None, fn, "weight is needed")
     sx, dt, dev, wt = x.shape, x.dtype, x.get_device(), weight.dtype
-    tx = _row_stride(x, dev, sx)
-    if not (tx and dt in _ROWS and (wt is dt or wt is _F32) and _fixed(weight, dev, wt) and weight.shape == sx[1:]):
-        _matrix(x, dev, fn, "x", (None, None), _ROWS)
-        _want(wt in (dt, _F32), fn, f"weight has the unsupported type {wt}")
-        _table(weight, dev, wt, (sx[1],), fn, "weight")
-        tx = _stride(x)
-    return sx, dt, dev, tx, wt
+    if (dev >= 0 and len(sx) == 2 and dt in _ROWS and x.is_contiguous() and (wt is dt or wt is _F32) and
+            weight.get_device() == dev and weight.is_contiguous() and weight.shape == sx[1:]):
+        return sx, dt, dev, sx[1], wt
+    _matrix(x, dev, fn, "x", (None, None), _ROWS)
+    _want(wt in (dt, _F32), fn, f"weight has the unsupported type {wt}")
+    _table(weight, dev, wt, (sx[1],), fn, "weight")
+    return sx, dt, dev, _stride(x), wt
 
 
-def _rms_norm(fn, x, weight, eps, quantized, out, residual, residual_out, rstd, stream):
+def _rms_norm(fn, call, x, weight, eps, fmt, codes, scales, out, residual, residual_out, rstd, stream):
+    """``fmt``: None (values), -1 (FP8 block codes), or an MX format."""
     sx, dt, dev, tx, wt = _norm_rows(fn, x, weight)
-    rp, tr = _rows_at(residual, sx, dt, dev, fn, "residual")
-    op, to = _rows_at(out, sx, dt, dev, fn, "out")
-    sp, ts = _rows_at(residual_out, sx, dt, dev, fn, "residual_out")
-    rstd = _flat_at(rstd, sx[:1], _F32, dev, fn, "rstd")
-    _check(getattr(lib(), fn)(x.data_ptr(), tx, rp, tr, _DTYPES[dt], weight.data_ptr(), _DTYPES[wt], eps, sx[0], sx[1],
-                              *quantized(sx, dev), op, to, sp, ts, rstd, _launch_stream(stream, dev, fn)), fn)
+    rp = op = sp = tp = None
+    tr = to = ts = 0
+    if residual is not None:
+        rp, tr = _rows_at(residual, sx, dt, dev, fn, "residual")
+    if out is not None:
+        op, to = _rows_at(out, sx, dt, dev, fn, "out")
+    if residual_out is not None:
+        sp, ts = _rows_at(residual_out, sx, dt, dev, fn, "residual_out")
+    if rstd is not None:
+        tp = _flat_at(rstd, sx[:1], _F32, dev, fn, "rstd")
+    T, H = sx
+    xp, wp, d, w, stream = x.data_ptr(), weight.data_ptr(), _DTYPES[dt], _DTYPES[wt], _launch_stream(stream, dev, fn)
+    if fmt is None:
+        status = call(xp, tx, rp, tr, d, wp, w, eps, T, H, op, to, sp, ts, tp, stream)
+    elif fmt < 0:
+        status = call(xp, tx, rp, tr, d, wp, w, eps, T, H, codes, scales, op, to, sp, ts, tp, stream)
+    else:
+        status = call(xp, tx, rp, tr, d, wp, w, eps, T, H, fmt, codes, scales, op, to, sp, ts, tp, stream)
+    if status:
+        _check(status, fn)
 
 
 def moe_rms_norm(x, weight, eps, out, residual=None, residual_out=None, rstd=None, stream=None):
@@ -676,7 +690,7 @@ def moe_rms_norm(x, weight, eps, out, residual=None, residual_out=None, rstd=Non
     weight [H] of x's type or fp32, rstd fp32 [T] (1 / sqrt(...), for the gradient)."""
     fn = "moe_rms_norm"
     _want(out is not None, fn, "out must be a matrix")
-    _rms_norm(fn, x, weight, eps, lambda sx, dev: (), out, residual, residual_out, rstd, stream)
+    _rms_norm(fn, lib().moe_rms_norm, x, weight, eps, None, None, None, out, residual, residual_out, rstd, stream)
 
 
 def moe_rms_norm_quantize_fp8_block(x, weight, eps, codes, scales, out=None, residual=None, residual_out=None,
@@ -684,11 +698,13 @@ def moe_rms_norm_quantize_fp8_block(x, weight, eps, codes, scales, out=None, res
     """moe_rms_norm with its result as E4M3 codes u8 [T, H] and fp32 scales [T, ceil(H / 128)], and in out too."""
     fn = "moe_rms_norm_quantize_fp8_block"
     _want(codes is not None and scales is not None, fn, "codes and scales are needed")
-
-    def quantized(sx, dev):
-        return (_flat_at(codes, sx, _U8, dev, fn, "codes"),
-                _flat_at(scales, (sx[0], (sx[1] + 127) // 128), _F32, dev, fn, "scales"))
-    _rms_norm(fn, x, weight, eps, quantized, out, residual, residual_out, rstd, stream)
+    sx, dev = x.shape, x.get_device()
+    if len(sx) != 2 or dev < 0:
+        _matrix(x, dev, fn, "x", (None, None), _ROWS)
+    cp = _flat_at(codes, sx, _U8, dev, fn, "codes")
+    sp = _flat_at(scales, (sx[0], (sx[1] + 127) // 128), _F32, dev, fn, "scales")
+    _rms_norm(fn, lib().moe_rms_norm_quantize_fp8_block, x, weight, eps, -1, cp, sp, out, residual, residual_out, rstd,
+              stream)
 
 
 def moe_rms_norm_quantize_mx(x, weight, eps, fmt, codes, scales, out=None, residual=None, residual_out=None, rstd=None,
@@ -698,12 +714,14 @@ def moe_rms_norm_quantize_mx(x, weight, eps, fmt, codes, scales, out=None, resid
     fn = "moe_rms_norm_quantize_mx"
     _want(codes is not None and scales is not None, fn, "codes and scales are needed")
     _want(fmt in (MOE_ACT_MXFP8, MOE_ACT_MXFP4), fn, "fmt must be MOE_ACT_MXFP8 or MOE_ACT_MXFP4")
-
-    def quantized(sx, dev):
-        _want(sx[1] % 32 == 0, fn, "the rows' width must be a multiple of 32")
-        return (fmt, _flat_at(codes, (sx[0], sx[1] if fmt == MOE_ACT_MXFP8 else sx[1] // 2), _U8, dev, fn, "codes"),
-                _flat_at(scales, (sx[0], sx[1] // 32), _U8, dev, fn, "scales"))
-    _rms_norm(fn, x, weight, eps, quantized, out, residual, residual_out, rstd, stream)
+    sx, dev = x.shape, x.get_device()
+    if len(sx) != 2 or dev < 0:
+        _matrix(x, dev, fn, "x", (None, None), _ROWS)
+    T, H = sx
+    _want(H % 32 == 0, fn, "the rows' width must be a multiple of 32")
+    cp = _flat_at(codes, (T, H if fmt == MOE_ACT_MXFP8 else H // 2), _U8, dev, fn, "codes")
+    sp = _flat_at(scales, (T, H // 32), _U8, dev, fn, "scales")
+    _rms_norm(fn, lib().moe_rms_norm_quantize_mx, x, weight, eps, fmt, cp, sp, out, residual, residual_out, rstd, stream)
 
 
 def moe_rms_norm_backward_workspace_bytes(T, H) -> int:
@@ -741,8 +759,9 @@ def moe_swiglu_backward(gate_up, d_h, d_gate_up=None, codes=None, scales=None, l
     _want(d_gate_up is not None or codes is not None, fn, "d_gate_up or codes are needed")
     _want((codes is None) == (scales is None), fn, "codes and scales come together")
     sh, dt, dev = d_h.shape, d_h.dtype, d_h.get_device()
-    th = _row_stride(d_h, dev, sh)
-    if not (th and dt in _ROWS):
+    if dev >= 0 and dt in _ROWS and len(sh) == 2 and d_h.is_contiguous():
+        th = sh[1]
+    else:
         _matrix(d_h, dev, fn, "d_h", (None, None), _ROWS)
         th = _stride(d_h)
     wide = (sh[0], 2 * sh[1])
