@@ -107,7 +107,8 @@ struct PairParams : BlockParams {
   CUtensorMap tmap_out;  // output, box 128 B x 32 rows
   int out_tma;           // output rows start on 16-byte boundaries
   int out_stage;         // rows go through the staging and leave a row at a time
-  CUtensorMap tmap_gate_up;  // gated: the kept products, and whether they leave so
+  CUtensorMap tmap_codes;    // gated: codes of h [M, I], box 64 B x 32 rows
+  CUtensorMap tmap_gate_up;  // the kept products, and whether they leave so
   int gate_up_tma;
 };
 
@@ -852,15 +853,35 @@ __global__ void __launch_bounds__(kBThreads, 1)
           if (lane == 0) mbar_arrive(amax_empty(w ^ 4));
           amax_phase ^= 1u;
           const BlockScale sc = computed_scale(m);
-          if (any && valid) {
+          // Whole pieces of 32 rows leave as a swizzled box by a TMA store, which clips the columns past the last one,
+          // others by their lanes (48 x 1024 rows, I = K = 2048: 419 us by the lanes, 409 so)
+          const bool box = G == 2 && rows_here >= 32;
+          uint8_t* codes_stage = stage;
+          if (box && any) {
+            if (lane == 0) bulk_wait_read_1();
+            __syncwarp();
+            codes_stage += (slot & 1) * 4096;
+          }
+          if (any) {
             uint8_t* dst = a.codes + row * cols + col0;
 #pragma unroll
-            for (int i = 0; i < 64; i += 16) {
+            for (int i = 0; i < 4; ++i) {
               uint32_t q[4];
-              encode_computed<16>(h + i, sc.mult, infinite, q);
-              if (col0 + i < cols) *reinterpret_cast<uint4*>(dst + i) = make_uint4(q[0], q[1], q[2], q[3]);
+              encode_computed<16>(h + 16 * i, sc.mult, infinite, q);
+              const uint4 v = make_uint4(q[0], q[1], q[2], q[3]);
+              if (box) *reinterpret_cast<uint4*>(codes_stage + lane * 64 + ((i ^ ((lane >> 1) & 3)) << 4)) = v;
+              else if (valid && col0 + 16 * i < cols) *reinterpret_cast<uint4*>(dst + 16 * i) = v;
             }
-            if (half == 0) a.scales[row * NT + hd.z] = sc.scale;
+            if (half == 0 && valid) a.scales[row * NT + hd.z] = sc.scale;
+          }
+          if (box && any) {
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              if constexpr (G == 2) tma_store_2d(&p.tmap_codes, smem_u32(codes_stage), col0, (int)row);
+              bulk_commit_group();
+            }
+            ++slot;
           }
         }
         continue;
@@ -1219,6 +1240,10 @@ cudaError_t launch_tiles(const GemmBlockArgs& a, int64_t tiles, int split, cudaS
     p.out_tma = a.out != nullptr && grid % 16 == 0;
     p.out_stage = grid % 4 != 0 && red > kStageCols;
     p.gate_up_tma = KIND == kGated && a.gate_up != nullptr && out_grid(a, a.gate_up, a.N) % 16 == 0;
+    if (KIND == kGated && a.codes != nullptr) {
+      const cuuint64_t hd[2] = {I, (cuuint64_t)a.M}, hst[1] = {I};
+      if (!encode_codes(&p.tmap_codes, a.codes, 2, hd, hst, 64, 32)) return cudaErrorInvalidValue;
+    }
     if (p.out_tma && !encode_out(&p.tmap_out, a, a.out, cols)) return cudaErrorInvalidValue;
     if (p.gate_up_tma && !encode_out(&p.tmap_gate_up, a, a.gate_up, a.N)) return cudaErrorInvalidValue;
   }
