@@ -830,7 +830,10 @@ __global__ void __launch_bounds__(kBThreads, 1)
         }
         float h[64];
 #pragma unroll
-        for (int i = 0; i < 64; ++i) h[i] = acc[i] * sigmoid(acc[i]) * acc[64 + i];
+        for (int i = 0; i < 64; i += 2) {
+          const uint64_t g = two(acc[i], acc[i + 1]);
+          apart(mul2(mul2(g, sigmoid2(g)), two(acc[64 + i], acc[65 + i])), h[i], h[i + 1]);
+        }
         if (a.out != nullptr && any) put_rows64<G>(p, h, a.out, false, cols, col0, row - lane, rows_here, stage, slot);
         if (a.codes != nullptr) {
           // a block of 128 columns of h: this warp's 64 and those of the warp that has the other half of the tile

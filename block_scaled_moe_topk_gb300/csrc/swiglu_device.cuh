@@ -1,6 +1,6 @@
 // swiglu_device.cuh -- the logistic function in fp32 for the gated activation and its gradient.
 #pragma once
-#include <cstdint>
+#include "fp8_block_device.cuh"
 
 namespace moe {
 namespace {
@@ -13,6 +13,19 @@ __device__ __forceinline__ float sigmoid(float g) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -1.4426950408889634f));
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
   return r;
+}
+
+// The same of two values with one reciprocal, 1 / a = b / (a b): the special-function unit, 16 lanes a clock, is what a
+// tile's 16384 activations wait for.  Exponents are cut at 60 so that the product is finite: a gate below -41.6
+// gets 2^-60.
+__device__ __forceinline__ uint64_t sigmoid2(uint64_t g) {
+  float t0, t1, a0, a1, r;
+  apart(mul2(g, two(-1.4426950408889634f, -1.4426950408889634f)), t0, t1);
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(a0) : "f"(fminf(t0, 60.0f)));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(a1) : "f"(fminf(t1, 60.0f)));
+  apart(add2(two(a0, a1), two(1.0f, 1.0f)), a0, a1);
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(a0 * a1));
+  return mul2(two(r, r), two(a1, a0));
 }
 
 }  // namespace

@@ -62,7 +62,7 @@ def reference(args, counts, layout):
     sig = torch.sigmoid(g)
     h = g * sig * u
     eh = 1.1 * u.abs() * eg + (g * sig).abs() * eu + 1.1 * eg * eu + h.abs() * ((5 + 1.173 * g.abs()) * 2.0 ** -23 + 3 * U)
-    return v, e, h, eh + (1 + (g * u).abs()) * 2.0 ** -126  # a logistic function below 2^-126 is 0
+    return v, e, h, eh + (1 + (g * u).abs()) * 2.0 ** -60  # a logistic function below 2^-60 is 2^-60 or less
 
 
 def check(args, got, counts, layout, dtype):
@@ -188,7 +188,14 @@ def test_nan_and_inf_stay_in_their_row_and_block(form, layout):
     touched = (rows == last)[:, None] | (rows == first)[:, None] | (inside[:, None] & (cols == col))
     assert bool(torch.isnan(new["out"][last]).all()) and not bool(torch.isfinite(new["gate_up"][first]).any())
     assert bool(torch.isnan(new["out"][inside][:, col]).all())
-    assert torch.equal(new["out"][~touched], got["out"][~touched])
+    # Columns 2j and 2j + 1 share a reciprocal: the neighbour of the NaN's column keeps its value, within what two
+    # logistic functions may differ by, and every other element keeps its bits.
+    beside = inside[:, None] & (cols == (col ^ 1)) & ~touched
+    assert torch.equal(new["out"][~touched & ~beside], got["out"][~touched & ~beside])
+    gate = halves(got["gate_up"], layout)[0].to(F64)
+    apart = (new["out"].to(F64) - got["out"].to(F64)).abs()
+    bound = got["out"].to(F64).abs() * ((10 + 2.4 * gate.abs()) * 2.0 ** -23 + 6 * U) + 2.0 ** -126
+    assert bool((apart <= bound)[beside].all())
     assert bool(((new["codes"][inside][:, col] & 127) == 127).all()) and bool(((new["codes"][last] & 127) == 127).all())
     assert bool((new["scales"][last] == 0).all())
     other = ~touched & (~inside[:, None] | (cols >= 128))
