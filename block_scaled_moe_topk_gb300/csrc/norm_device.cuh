@@ -84,6 +84,13 @@ __device__ __forceinline__ void raw_pair(const Raw8<DT>& r, int i, float& lo, fl
 }
 
 template <int DT>
+__device__ __forceinline__ uint64_t raw_two(const Raw8<DT>& r, int i) {
+  float lo, hi;
+  raw_pair<DT>(r, i, lo, hi);
+  return two(lo, hi);
+}
+
+template <int DT>
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   if (DT == kDtBf16) {
     const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
@@ -112,6 +119,16 @@ __device__ __forceinline__ void store8(void* x, int64_t base, int c, int n, cons
           make_uint4(pack2<DT>(v[0], v[1]), pack2<DT>(v[2], v[3]), pack2<DT>(v[4], v[5]), pack2<DT>(v[6], v[7]));
     }
   }
+}
+
+// 8 values in pairs to column c of a row that lies on a 16-byte boundary; nothing from column n on.
+template <int DT>
+__device__ __forceinline__ void put8(uint8_t* row, int c, int n, const uint64_t (&v)[4]) {
+  if (c >= n) return;
+  float f[8];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) apart(v[j], f[2 * j], f[2 * j + 1]);
+  store8<DT, true>(row, 0, c, n, f);
 }
 
 // The sum over the tpr threads of a row (a power of two up to 32, or whole warps), the same for all of them, in an
@@ -170,23 +187,38 @@ __device__ __forceinline__ void put_fp8(uint8_t* codes, float* scales, int64_t r
   }
 }
 
-// The same as MX codes (FMT 0: E4M3, 1: E2M1, two a byte) with one E8M0 scale per 32 columns, H a multiple of 32.
-template <bool VEC, int FMT>
-__device__ __forceinline__ void put_mx(uint8_t* codes, uint8_t* scales, int64_t row, int H, int c, bool on,
-                                       const float (&v)[8]) {
-  if (VEC) {  // 4 lanes a block
-    float m = 0.0f;
+// The same for a thread's chunk of a row on an 8-byte boundary: `codes` and `scales` are the row's, `first` the thread's
+// first column and codes' start, n the columns from there on.
+__device__ __forceinline__ void put_fp8_chunk(uint8_t* codes, float* scales, int first, int c, int n, const float (&v)[8]) {
+  bool infinite;
+  const BlockScale sc = computed_scale(lanes_max(finite_max<8>(v, infinite), 16));
+  uint32_t w[2];
+  encode_computed<8>(v, sc.mult, infinite, w);
+  if (c >= n) return;
+  *reinterpret_cast<uint2*>(codes + c) = make_uint2(w[0], w[1]);
+  if (((first + c) & (kFp8Block - 1)) == 0) scales[(first + c) / kFp8Block] = sc.scale;
+}
+
+// 8 values as MX codes (FMT 0: E4M3, 1: E2M1, two a byte) with one E8M0 scale per 32 columns, 4 lanes: `at` is the first
+// one's place in the whole matrix, whose rows are whole blocks.
+template <int FMT>
+__device__ __forceinline__ void put_mx_chunk(uint8_t* codes, uint8_t* scales, int64_t at, bool on, const float (&v)[8]) {
+  float m = 0.0f;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) m = fmaxf(m, fabsf(v[j]));
-    const MxScale sc = mx_scale<FMT>(lanes_max(m, 4));
-    if (!on || c >= H) return;
-    if (FMT == 0) *reinterpret_cast<uint2*>(codes + row * H + c) = pack_e4m3x8(v, sc.mult);
-    else *reinterpret_cast<uint32_t*>(codes + (row * H + c) / 2) = pack_e2m1x8(v, sc.mult);
-    if ((c & 31) == 0) scales[(row * H + c) / 32] = sc.byte;
-    return;
-  }
+  for (int j = 0; j < 8; ++j) m = fmaxf(m, fabsf(v[j]));
+  const MxScale sc = mx_scale<FMT>(lanes_max(m, 4));
+  if (!on) return;
+  if (FMT == 0) *reinterpret_cast<uint2*>(codes + at) = pack_e4m3x8(v, sc.mult);
+  else *reinterpret_cast<uint32_t*>(codes + at / 2) = pack_e2m1x8(v, sc.mult);
+  if ((at & 31) == 0) scales[at / 32] = sc.byte;
+}
+
+// The same for single elements, one of every lane a block.
+template <int FMT>
+__device__ __forceinline__ void put_mx_single(uint8_t* codes, uint8_t* scales, int64_t row, int H, int c, bool on,
+                                              const float (&v)[8]) {
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {  // one element of every lane a block
+  for (int j = 0; j < 8; ++j) {
     const MxScale sc = mx_scale<FMT>(lanes_max(fabsf(v[j]), 32));
     const int cj = c + 32 * j;
     const float next = __shfl_down_sync(0xffffffffu, v[j], 1);
