@@ -59,7 +59,7 @@ struct QuantBlockArgs {
 };
 cudaError_t launch_quant_block(const QuantBlockArgs& a, cudaStream_t s);
 
-// rms_norm.cu, rms_norm_backward.cu.  Strides are in elements.
+// rms_norm*.cu.  Strides are in elements.
 enum : int { kQuantNone = 0, kQuantFp8Block = 1, kQuantMx = 2 };
 constexpr int kMaxNormWidth = 32768;      // columns of a row: 512 threads of 64
 constexpr int64_t kSpreadRows = 2 * 152;  // up to so many rows the SMs are not filled by rows alone
@@ -85,6 +85,8 @@ struct NormArgs {
   void* scales;          // fp32 [T, H / 128 (rounded up)], or E8M0 [T, H / 32]
 };
 cudaError_t launch_rms_norm(const NormArgs& a, cudaStream_t s);
+cudaError_t launch_rms_norm_fp8(const NormArgs& a, cudaStream_t s);  // rms_norm_fp8.cu
+cudaError_t launch_rms_norm_mx(const NormArgs& a, cudaStream_t s);   // rms_norm_mx.cu
 
 struct NormBackwardArgs {
   const void* dy;
