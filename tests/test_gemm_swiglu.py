@@ -62,7 +62,7 @@ def reference(args, counts, layout):
     sig = torch.sigmoid(g)
     h = g * sig * u
     eh = 1.1 * u.abs() * eg + (g * sig).abs() * eu + 1.1 * eg * eu + h.abs() * ((5 + 1.173 * g.abs()) * 2.0 ** -23 + 3 * U)
-    return v, e, h, eh + (1 + (g * u).abs()) * 2.0 ** -60  # a logistic function below 2^-60 is 2^-60 or less
+    return v, e, h, eh + (1 + (g * u).abs()) * 2.0 ** -60  # a logistic function below 2^-60 is 2^-60 or 0
 
 
 def check(args, got, counts, layout, dtype):
