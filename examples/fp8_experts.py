@@ -2,10 +2,13 @@
 
 The expert layer with its weights as E4M3 codes and one fp32 scale per 128x128 block:
 
-  forward   route -> sort -> permute + quantise -> gate/up product -> SwiGLU -> quantise ->
+  forward   route -> sort -> permute + quantise -> gated product (SwiGLU and its codes in the same kernel) ->
             down product -> unpermute
-  backward  unpermute backward -> quantise -> down input gradient -> SwiGLU backward -> quantise ->
+  backward  unpermute backward -> quantise -> down input gradient -> SwiGLU backward to codes ->
             gate/up input gradient -> permute backward, and route backward for the logits
+
+``Fp8Block`` puts the layer behind the residual stream as a model does: residual's addition, RMS norm and quantisation
+in one kernel, whose bf16 rows go to the router and whose codes go to the experts; and all of it back.
 
 ``python examples/fp8_experts.py`` trains a router (a linear map from the tokens to the logits) whose
 experts stay fixed, towards the outputs that another router would give, and prints the loss.
@@ -48,18 +51,19 @@ class Fp8Experts:
         self.w2, self.s2 = quantize_weights(w2)
         self.device = w1.device
 
+    def _space(self, M, N, K):
+        return torch.empty(moe.moe_gemm_fp8_block_workspace_bytes(M, N, K, self.E), dtype=torch.uint8, device=self.device)
+
     def _gemm(self, call, x, w, scales, cols):
-        out = torch.empty(x.shape[0], cols, dtype=torch.bfloat16, device=self.device)
-        E, N, K = w.shape
-        space = torch.empty(moe.moe_gemm_fp8_block_workspace_bytes(x.shape[0], N, K, E), dtype=torch.uint8,
-                            device=self.device)
         codes, xs = x if isinstance(x, tuple) else quantize(x)
-        call(codes, xs, w, scales, out, space, offsets=self.offsets)
+        out = torch.empty(codes.shape[0], cols, dtype=torch.bfloat16, device=self.device)
+        call(codes, xs, w, scales, out, self._space(codes.shape[0], *w.shape[1:]), offsets=self.offsets)
         return out
 
-    def forward(self, x, logits):
+    def forward(self, x, logits, quantized=None):
+        """``quantized``: (codes, scales) of x's rows, where they are at hand."""
         T, dev = x.shape[0], self.device
-        R = T * self.k
+        R, blocks = T * self.k, -(-self.H // 128)
         new = lambda *shape, dtype: torch.empty(*shape, dtype=dtype, device=dev)  # noqa: E731
         self.ids, self.w = new(T, self.k, dtype=torch.int32), new(T, self.k, dtype=torch.float32)
         moe.moe_topk_route(logits, self.k, self.ids, self.w)
@@ -67,14 +71,17 @@ class Fp8Experts:
         pair, self.inv = new(R, dtype=torch.int32), new(T, self.k, dtype=torch.int32)
         scratch = new(moe.moe_workspace_bytes(T, 128, 128, self.E, self.k), dtype=torch.uint8)
         moe.moe_sort_by_expert(self.ids, self.E, counts, self.offsets, pair, self.inv, scratch)
-        codes, scales = new(R, self.H, dtype=torch.uint8), new(R, -(-self.H // 128), dtype=torch.float32)
-        moe.moe_permute_quantize_fp8_block(x, self.inv, codes, scales)
-        h = new(R, 2 * self.I, dtype=torch.bfloat16)
-        space = new(moe.moe_gemm_fp8_block_workspace_bytes(R, 2 * self.I, self.H, self.E), dtype=torch.uint8)
-        moe.moe_gemm_fp8_block(codes, scales, self.w1, self.s1, h, space, offsets=self.offsets)
-        self.gate, self.up = h.float()[:, 0::2], h.float()[:, 1::2]
-        act = (torch.nn.functional.silu(self.gate) * self.up).to(torch.bfloat16)
-        self.y = self._gemm(moe.moe_gemm_fp8_block, act, self.w2, self.s2, self.H)
+        codes, scales = new(R, self.H, dtype=torch.uint8), new(R, blocks, dtype=torch.float32)
+        if quantized is None:
+            moe.moe_permute_quantize_fp8_block(x, self.inv, codes, scales)
+        else:
+            moe.moe_permute(quantized[0], self.inv, codes)
+            moe.moe_permute(quantized[1], self.inv, scales)
+        h, hs = new(R, self.I, dtype=torch.uint8), new(R, -(-self.I // 128), dtype=torch.float32)
+        self.gate_up = new(R, 2 * self.I, dtype=torch.bfloat16)  # the backward pass reads the products
+        moe.moe_gemm_fp8_block_swiglu(codes, scales, self.w1, self.s1, self._space(R, 2 * self.I, self.H), codes=h,
+                                      scales=hs, gate_up=self.gate_up, offsets=self.offsets)
+        self.y = self._gemm(moe.moe_gemm_fp8_block, (h, hs), self.w2, self.s2, self.H)
         out = torch.empty_like(x)
         moe.moe_unpermute(self.y, self.inv, self.w, out)
         return out
@@ -83,17 +90,46 @@ class Fp8Experts:
         """Gradients of x and of the logits for the last forward."""
         dy, dw = torch.empty_like(self.y), torch.empty_like(self.w)
         moe.moe_unpermute_backward(dout, self.y, self.inv, self.w, dy, dw)
-        dact = self._gemm(moe.moe_gemm_fp8_block_dgrad, dy, self.w2, self.s2, self.I).float()
-        sig = torch.sigmoid(self.gate)
-        dgate = dact * self.up * sig * (1 + self.gate * (1 - sig))
-        dup = dact * self.gate * sig
-        dh = torch.stack([dgate, dup], 2).reshape(dy.shape[0], 2 * self.I).to(torch.bfloat16)
-        drows = self._gemm(moe.moe_gemm_fp8_block_dgrad, dh, self.w1, self.s1, self.H)
+        dh = self._gemm(moe.moe_gemm_fp8_block_dgrad, dy, self.w2, self.s2, self.I)
+        codes = torch.empty(self.gate_up.shape, dtype=torch.uint8, device=self.device)
+        scales = torch.empty(codes.shape[0], -(-codes.shape[1] // 128), dtype=torch.float32, device=self.device)
+        moe.moe_swiglu_backward(self.gate_up, dh, codes=codes, scales=scales)
+        drows = self._gemm(moe.moe_gemm_fp8_block_dgrad, (codes, scales), self.w1, self.s1, self.H)
         dx = torch.empty_like(dout)
         moe.moe_permute_backward(drows, self.inv, dx)
         dlogits = torch.empty(dout.shape[0], self.E, dtype=torch.float32, device=self.device)
         moe.moe_topk_route_backward(self.ids, self.w, dw, dlogits)
         return dx, dlogits
+
+
+class Fp8Block:
+    """out = experts(norm(stream)) with stream = x + residual, the norm's rows routed by a linear map [H, E]."""
+
+    def __init__(self, experts, weight, router, eps=1e-6):
+        self.experts, self.weight, self.router, self.eps = experts, weight, router, eps
+
+    def forward(self, x, residual):
+        """(experts' output, stream): the next block adds them up in its own norm."""
+        T, H = x.shape
+        self.stream, self.normed = torch.empty_like(x), torch.empty_like(x)
+        self.rstd = torch.empty(T, dtype=torch.float32, device=x.device)
+        codes = torch.empty(T, H, dtype=torch.uint8, device=x.device)
+        scales = torch.empty(T, -(-H // 128), dtype=torch.float32, device=x.device)
+        moe.moe_rms_norm_quantize_fp8_block(x, self.weight, self.eps, codes, scales, out=self.normed, residual=residual,
+                                            residual_out=self.stream, rstd=self.rstd)
+        return self.experts.forward(self.normed, self.normed.float() @ self.router, (codes, scales)), self.stream
+
+    def backward(self, dout, dstream):
+        """Gradients of x (and of residual, the same), of the norm's weight and of the router, from those of the two
+        outputs."""
+        dnormed, dlogits = self.experts.backward(dout)
+        self.dnormed = (dnormed.float() + dlogits @ self.router.t()).to(dout.dtype)
+        drouter = self.normed.float().t() @ dlogits
+        dx, dweight = torch.empty_like(dout), torch.empty(self.weight.shape, dtype=torch.float32, device=dout.device)
+        space = torch.empty(moe.moe_rms_norm_backward_workspace_bytes(*dout.shape), dtype=torch.uint8, device=dout.device)
+        moe.moe_rms_norm_backward(self.dnormed, self.stream, self.weight, self.rstd, dx, dweight, space,
+                                  d_residual=dstream)
+        return dx, dweight, drouter
 
 
 def make_experts(E, H, I, k, seed=0, device="cuda"):
