@@ -159,6 +159,8 @@ enum : uint32_t { kFormVector = 1, kFormSingle = 2, kFormPair = 3, kFormSplit = 
 // gemv_block.cu: the forward product of a few rows, and whether a product is one.
 bool use_gemv(const GemmBlockArgs& a);
 cudaError_t launch_gemv_block(const GemmBlockArgs& a, cudaStream_t s);
-cudaError_t launch_gemv_swiglu(const GemmBlockArgs& a, cudaStream_t s);  // gemv_swiglu.cu
+// gemv_swiglu.cu: the same for the gated product.
+bool use_gemv_swiglu(const GemmBlockArgs& a);
+cudaError_t launch_gemv_swiglu(const GemmBlockArgs& a, cudaStream_t s);
 
 }  // namespace moe

@@ -12,7 +12,7 @@ namespace moe {
 
 cudaError_t launch_gemm_swiglu(const GemmBlockArgs& a, cudaStream_t s) {
   if (a.M == 0) return cudaSuccess;
-  if (use_gemv(a)) return launch_gemv_swiglu(a, s);
+  if (use_gemv_swiglu(a)) return launch_gemv_swiglu(a, s);
   return launch_direction<kGated>(a, s);
 }
 
