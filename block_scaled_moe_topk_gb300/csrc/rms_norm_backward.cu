@@ -5,11 +5,15 @@
 // order every time (no atomics).
 //
 // A row's rstd is known, so one sum (of g xh) stands between its loads and its dx.  To keep HBM busy
-// meanwhile, rows on 16-byte boundaries come through shared memory by asynchronous 16-byte copies, a few
-// rows ahead; a thread copies what it will read itself, so no barrier guards the ring.  Rows off those
-// boundaries, and rows too long for the ring, are read directly, twice (the second time from L1 or L2).
+// meanwhile, rows come through shared memory by asynchronous 16-byte copies, a few rows ahead; a thread copies
+// what it will read itself, so no barrier guards the ring.  Rows that start off the 16-byte boundaries are
+// copied from the boundary below: a thread's columns then begin `shift` elements earlier.  The shift repeats
+// every 2 to 8 rows, and a block takes rows of one shift only, so that its columns of dw stay its own
+// (37401 x 1570 bf16 with d_residual 317 us element by element, 129 so; 8192 x 7167 90 against 82 of 7168).  Rows of matrices that disagree on the shift,
+// and rows too long for the ring, are read directly, twice (the second time from L1 or L2).
 #include <algorithm>
 #include <atomic>
+#include <utility>
 
 #include "norm_device.cuh"
 
@@ -20,17 +24,18 @@ constexpr int kNbThreads = 256;     // of a block that holds several rows
 constexpr int kNbMaxThreads = 512;
 constexpr int kNbHeldThreads = 448;  // with the weight in registers, two blocks an SM
 constexpr int kNbMaxStages = 4;
-constexpr int kNbRingBytes = 108 * 1024;  // a block's share of an SM that holds two
-constexpr int kNbMaxRing = 216 * 1024;
+constexpr int kNbMaxRing = 216 * 1024;  // of an SM
 
 struct NormBackwardParams {
   NormBackwardArgs a;
   int tpr, rpb;  // as in rms_norm.cu
   int stages;    // rows of the ring per row group
+  int classes;   // rows r and r + classes start at the same place between two 16-byte boundaries
 };
 
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool on) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0) : "memory");
+// `bytes` of 16 from a 16-byte boundary, the rest zeros.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -72,7 +77,7 @@ __device__ __forceinline__ void leave_dw(const NormBackwardParams& p, Col col, f
 #pragma unroll
       for (int q = 0; q < N; ++q) {
         const int c = col(q);
-        if (c < H) sums[c] = g > 0 ? sums[c] + dw[q] : dw[q];
+        if (c >= 0 && c < H) sums[c] = g > 0 ? sums[c] + dw[q] : dw[q];
       }
     }
     __syncthreads();
@@ -90,20 +95,24 @@ __device__ __forceinline__ void load_weight(const NormBackwardArgs& a, int col, 
 
 // Rows through the ring.  A thread owns pieces of 16 bytes (8 columns of 16-bit rows, 4 of fp32 ones), neighbouring
 // threads neighbouring pieces.  Shared memory: [stage][array][piece][thread] of 16 bytes.
-template <int DT, bool DRES, int NCH, int THREADS, int BLOCKS>
+template <int DT, bool DRES, bool SHIFT, int NCH, int THREADS, int BLOCKS>
 __global__ void __launch_bounds__(THREADS, BLOCKS) norm_backward_ring_kernel(const __grid_constant__ NormBackwardParams p) {
   constexpr int kArrays = DRES ? 3 : 2, es = DT == kDtF32 ? 4 : 2, EP = 16 / es, NP = NCH * 8 / EP;
-  constexpr bool kHoldWeight = NCH <= 2;  // in registers; else from L1 every time
+  constexpr bool kHoldWeight = NCH <= 2 || SHIFT;  // in registers; else from L1 every time
   extern __shared__ __align__(16) uint8_t ring[];
   const NormBackwardArgs& a = p.a;
   const int H = a.H, tpr = p.tpr;
   const int rb = tpr >= (int)blockDim.x ? 0 : threadIdx.x / tpr;
-  const int first = (threadIdx.x - rb * tpr) * EP;
+  // this block's rows: cls, cls + classes, ...; they start `shift` elements behind a 16-byte boundary
+  const int classes = SHIFT ? p.classes : 1, cls = SHIFT ? (int)blockIdx.x % classes : 0;
+  const int lanes = SHIFT ? max((int)gridDim.x / classes, 1) : gridDim.x;
+  const int shift = SHIFT ? (int)((cls * a.x_stride) % EP) : 0;
+  const int first = (int)(threadIdx.x - rb * tpr) * EP - shift;
   auto col = [&](int q) { return first + q * tpr * EP; };
   const uint32_t ring0 = (uint32_t)__cvta_generic_to_shared(ring) + threadIdx.x * 16u;
-  const int64_t step = (int64_t)gridDim.x * p.rpb;
+  const int64_t step = (int64_t)classes * lanes * p.rpb, row0 = cls + (int64_t)classes * (SHIFT ? blockIdx.x / classes : blockIdx.x) * p.rpb;
   const uint32_t piece = blockDim.x * 16u, array = NP * piece, slot_bytes = kArrays * array;
-  int64_t ahead = (int64_t)blockIdx.x * p.rpb + rb;  // the next row to fetch; every row group makes the same rounds
+  int64_t ahead = row0 + classes * rb;  // the next row to fetch; every row group makes the same rounds
   const bool group = rb < p.rpb;
   auto fetch = [&](uint32_t dst) {
     const bool on = group && ahead < a.T;
@@ -113,11 +122,13 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) norm_backward_ring_kernel(con
     const uint8_t* dres = DRES ? static_cast<const uint8_t*>(a.dres) + r * a.dres_stride * es : nullptr;
 #pragma unroll
     for (int q = 0; q < NP; ++q) {
-      const bool in = on && col(q) < H;
-      const uint32_t o = in ? (uint32_t)(col(q) * es) : 0u, at = dst + (uint32_t)q * piece;
-      copy16(at, dy + o, in);
-      copy16(at + array, x + o, in);
-      if (DRES) copy16(at + 2 * array, dres + o, in);
+      const int c = col(q);
+      const int bytes = !on || c >= H ? 0 : SHIFT ? min((H - c) * es, 16) : 16;  // nothing behind the row's end
+      const int o = bytes > 0 ? c * es : 0;
+      const uint32_t at = dst + (uint32_t)q * piece;
+      copy16(at, dy + o, bytes);
+      copy16(at + array, x + o, bytes);
+      if (DRES) copy16(at + 2 * array, dres + o, bytes);
     }
     copy_commit();
     ahead += step;
@@ -126,6 +137,15 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) norm_backward_ring_kernel(con
     uint4 v;
     asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                  : "r"(src + which * array + (uint32_t)q * piece) : "memory");
+    if (SHIFT && q == 0 && first < 0) {  // the row before's last elements
+      uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if (DT == kDtF32) u[k] = k < shift ? 0u : u[k];
+        else u[k] = 2 * k + 1 < shift ? 0u : 2 * k < shift ? u[k] & 0xFFFF0000u : u[k];
+      }
+      v = make_uint4(u[0], u[1], u[2], u[3]);
+    }
     return v;
   };
   // elements 2j and 2j + 1 of a piece
@@ -142,14 +162,22 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) norm_backward_ring_kernel(con
 #pragma unroll
     for (int j = 0; j < EP; ++j) w[q][j] = 0.0f;
     if (c >= H) return;
-    if (DT != kDtF32 && a.weight_dtype == DT) {
-      const uint4 v = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.weight) + c);
+    const bool same = DT != kDtF32 && a.weight_dtype == DT;
+    const uint8_t* at = static_cast<const uint8_t*>(a.weight) + (int64_t)c * (same ? 2 : 4);
+    if (SHIFT && (c < 0 || c + EP > H || (reinterpret_cast<uintptr_t>(at) & 15) != 0)) {
+#pragma unroll
+      for (int j = 0; j < EP; ++j) {
+        if (c + j < 0 || c + j >= H) continue;
+        w[q][j] = same ? load1<DT>(a.weight, c + j) : load1<kDtF32>(a.weight, c + j);
+      }
+    } else if (same) {
+      const uint4 v = *reinterpret_cast<const uint4*>(at);
 #pragma unroll
       for (int j = 0; j < EP / 2; ++j) apart(pair(v, j), w[q][2 * j], w[q][2 * j + 1]);
     } else {
 #pragma unroll
       for (int j = 0; j < EP; j += 4) {
-        const float4 v = *reinterpret_cast<const float4*>(static_cast<const float*>(a.weight) + c + j);
+        const float4 v = *reinterpret_cast<const float4*>(at + 4 * j);
         w[q][j] = v.x, w[q][j + 1] = v.y, w[q][j + 2] = v.z, w[q][j + 3] = v.w;
       }
     }
@@ -163,9 +191,9 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) norm_backward_ring_kernel(con
   for (int s = 0; s < p.stages; ++s) fetch(ring0 + s * slot_bytes);
   int slot = 0, turn = 0;
   const float inv_h = 1.0f / (float)H;
-  int64_t row = (int64_t)blockIdx.x * p.rpb + rb;
+  int64_t row = row0 + classes * rb;
   float next = group && row < a.T ? a.rstd[row] : 0.0f;  // the next round's rstd
-  for (int64_t base = (int64_t)blockIdx.x * p.rpb; base < a.T; base += step, row += step) {
+  for (int64_t base = row0; base < a.T; base += step, row += step) {
     const bool on = group && row < a.T;
     const float rstd = next;
     next = group && row + step < a.T ? a.rstd[row + step] : 0.0f;
@@ -206,13 +234,22 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) norm_backward_ring_kernel(con
         if (DRES) t = add2(t, pair(dres, j));
         apart(fma2(mul2(weight_pair(q, j), pair(dy, j)), rstd2, t), v[2 * j], v[2 * j + 1]);
       }
-      if (on && col(q) < H) {
+      const int c = col(q);
+      if (SHIFT && on && (c < 0 || c + EP > H)) {
+#pragma unroll
+        for (int j = 0; j < EP; ++j) {
+          if (c + j < 0 || c + j >= H) continue;
+          const int64_t o = row * a.dx_stride + c + j;
+          if (DT == kDtF32) static_cast<float*>(a.dx)[o] = v[j];
+          else static_cast<uint16_t*>(a.dx)[o] = (uint16_t)pack2<DT>(v[j], 0.0f);
+        }
+      } else if (on && (SHIFT || c < H)) {
         uint4 r;
         if constexpr (DT == kDtF32)
           r = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
         else
           r = make_uint4(pack2<DT>(v[0], v[1]), pack2<DT>(v[2], v[3]), pack2<DT>(v[4], v[5]), pack2<DT>(v[6], v[7]));
-        *reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.dx) + (row * a.dx_stride + col(q)) * es) = r;
+        *reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.dx) + (row * a.dx_stride + c) * es) = r;
       }
     }
     fetch(src);
@@ -290,11 +327,11 @@ __global__ void __launch_bounds__(kNbMaxThreads, 1) norm_backward_kernel(const _
 
 // dw[c] = the blocks' sums of column c.  32 columns a block, 16 threads a column, each with all its loads in flight.
 constexpr int kSumWays = 16;
-constexpr int kNbParts = 2 * 152;  // the most blocks: two an SM
+constexpr int kNbParts = 3 * 152;  // the most blocks
 __global__ void __launch_bounds__(32 * kSumWays, 1) norm_weight_sum_kernel(const float* partial, int parts, int H, float* dw) {
   __shared__ float sums[kSumWays][32];
   const int lane = threadIdx.x & 31, way = threadIdx.x >> 5, col = blockIdx.x * 32 + lane;
-  constexpr int kEach = kNbParts / kSumWays;
+  constexpr int kEach = (kNbParts + kSumWays - 1) / kSumWays;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   float v[kEach], sum = 0.0f;
 #pragma unroll
@@ -311,6 +348,10 @@ __global__ void __launch_bounds__(32 * kSumWays, 1) norm_weight_sum_kernel(const
   for (int q = 1; q < kSumWays; ++q) sum += sums[q][lane];
   dw[col] = sum;
 }
+
+// Two blocks an SM, three of 16-bit rows that take 256 threads or fewer (37401 x 1570 bf16 140 against 129 us; two rows
+// ahead of fp32 do not fit three times).
+int blocks_an_sm(int H, int es) { return H <= 2 * 8 * kNbThreads && es == 2 ? 3 : 2; }
 
 struct Shape {
   int tpr, rpb;
@@ -340,43 +381,54 @@ cudaError_t allow_smem(K kernel, std::atomic<int> (&ready)[64]) {
   return err;
 }
 
-template <int DT, bool DRES, int NCH, int THREADS, int BLOCKS>
+template <int DT, bool DRES, bool SHIFT, int NCH, int THREADS, int BLOCKS>
 cudaError_t launch_kernel(const NormBackwardParams& p, int grid, int threads, int64_t smem, cudaStream_t s) {
   static std::atomic<int> ready[64];
-  const cudaError_t err = allow_smem(norm_backward_ring_kernel<DT, DRES, NCH, THREADS, BLOCKS>, ready);
+  const cudaError_t err = allow_smem(norm_backward_ring_kernel<DT, DRES, SHIFT, NCH, THREADS, BLOCKS>, ready);
   if (err != cudaSuccess) return err;
-  norm_backward_ring_kernel<DT, DRES, NCH, THREADS, BLOCKS><<<grid, threads, smem, s>>>(p);
+  norm_backward_ring_kernel<DT, DRES, SHIFT, NCH, THREADS, BLOCKS><<<grid, threads, smem, s>>>(p);
   return cudaGetLastError();
 }
 
 template <int DT, int NCH, int THREADS, int BLOCKS>
-cudaError_t launch_ring(const NormBackwardParams& p, int grid, int threads, int64_t smem, cudaStream_t s) {
-  return p.a.dres != nullptr ? launch_kernel<DT, true, NCH, THREADS, BLOCKS>(p, grid, threads, smem, s)
-                             : launch_kernel<DT, false, NCH, THREADS, BLOCKS>(p, grid, threads, smem, s);
+cudaError_t launch_ring(const NormBackwardParams& p, bool shift, int grid, int threads, int64_t smem, cudaStream_t s) {
+  const bool dres = p.a.dres != nullptr;
+  if (shift)
+    return dres ? launch_kernel<DT, true, true, NCH, THREADS, BLOCKS>(p, grid, threads, smem, s)
+                : launch_kernel<DT, false, true, NCH, THREADS, BLOCKS>(p, grid, threads, smem, s);
+  return dres ? launch_kernel<DT, true, false, NCH, THREADS, BLOCKS>(p, grid, threads, smem, s)
+              : launch_kernel<DT, false, false, NCH, THREADS, BLOCKS>(p, grid, threads, smem, s);
 }
 
+// `vec`: rows of whole chunks on 16-byte boundaries; `classes`: how often their shift repeats, or 0 where the matrices'
+// rows do not share one.
 template <int DT>
-cudaError_t launch_typed(const NormBackwardArgs& a, bool vec, cudaStream_t s) {
-  NormBackwardParams p{a, 0, 1, 0};
-  const int chunks = vec ? (a.H + 7) / 8 : (a.H + 255) / 256 * 32;
+cudaError_t launch_typed(const NormBackwardArgs& a, bool vec, int classes, cudaStream_t s) {
+  NormBackwardParams p{a, 0, 1, 0, classes};
+  constexpr int EP = DT == kDtF32 ? 4 : 8;
   const int64_t es = DT == kDtF32 ? 4 : 2, arrays = a.dres != nullptr ? 3 : 2;
+  const int chunks = (a.H + (classes > 1 ? EP - 1 : 0) + 7) / 8;
   const int nch = chunks <= 2 * kNbHeldThreads ? 2 : 4;
-  Shape sh = shape_of(chunks, nch, vec, a.T);
+  Shape sh = shape_of(chunks, nch, true, (a.T + std::max(classes, 1) - 1) / std::max(classes, 1));
   int threads = (sh.tpr * sh.rpb + 31) / 32 * 32;
   const int64_t stage = arrays * nch * 8 * es * threads;
-  p.stages = (int)std::min<int64_t>(kNbMaxStages, kNbRingBytes / stage);
+  p.stages = (int)std::min<int64_t>(kNbMaxStages, kNbMaxRing / blocks_an_sm(a.H, es) / stage);
   if (p.stages < 2) p.stages = (int)std::min<int64_t>(kNbMaxStages, kNbMaxRing / stage);
   cudaError_t err;
-  if (vec && sh.tpr <= kNbMaxThreads && p.stages >= 2) {
+  if (classes > 0 && sh.tpr <= kNbMaxThreads && p.stages >= 2) {
     p.tpr = sh.tpr;
     p.rpb = sh.rpb;
-    const int grid = (int)std::min<int64_t>(norm_backward_parts(a.T, a.H), (a.T + sh.rpb - 1) / sh.rpb);
+    int64_t grid = std::min<int64_t>(152 * blocks_an_sm(a.H, es), (a.T + sh.rpb - 1) / sh.rpb);
+    // the same number of blocks for every class, or one for each of fewer rows than classes
+    grid = std::max<int64_t>(grid / classes * classes, std::min<int64_t>(classes, a.T));
     const int64_t smem = std::max<int64_t>(p.stages * stage, 4 * (int64_t)a.H);
-    err = nch == 2 ? launch_ring<DT, 2, kNbHeldThreads, 2>(p, grid, threads, smem, s)
-                   : launch_ring<DT, 4, kNbMaxThreads, 1>(p, grid, threads, smem, s);
-    p.stages = grid;
+    // a weight off the 16-byte boundaries is read as under a shift
+    const bool shift = classes > 1 || a.H % EP != 0 || reinterpret_cast<uintptr_t>(a.weight) % 16 != 0;
+    err = nch == 2 ? launch_ring<DT, 2, kNbHeldThreads, 2>(p, shift, (int)grid, threads, smem, s)
+                   : launch_ring<DT, 4, kNbMaxThreads, 1>(p, shift, (int)grid, threads, smem, s);
+    p.stages = (int)grid;
   } else {
-    sh = shape_of(chunks, 8, vec, a.T);
+    sh = shape_of(vec ? (a.H + 7) / 8 : (a.H + 255) / 256 * 32, 8, vec, a.T);
     p.tpr = sh.tpr;
     p.rpb = sh.rpb;
     threads = (sh.tpr * sh.rpb + 31) / 32 * 32;
@@ -406,21 +458,27 @@ cudaError_t launch_typed(const NormBackwardArgs& a, bool vec, cudaStream_t s) {
 
 }  // namespace
 
-// Two blocks an SM of the 152, fewer for fewer rows.
-int norm_backward_parts(int64_t T, int) { return (int)std::min<int64_t>(T, kNbParts); }
+// The most blocks that are launched, for either size of elements.
+int norm_backward_parts(int64_t T, int H) { return (int)std::min<int64_t>(T, 152 * blocks_an_sm(H, 2)); }
 
 cudaError_t launch_rms_norm_backward(const NormBackwardArgs& a, cudaStream_t s) {
   if (a.T == 0) return a.dw != nullptr ? cudaMemsetAsync(a.dw, 0, (size_t)a.H * 4, s) : cudaSuccess;
   const int64_t es = dtype_bytes(a.dtype);
-  auto grid16 = [&](const void* q, int64_t stride) {
-    return q == nullptr || (reinterpret_cast<uintptr_t>(q) % 16 == 0 && (a.T == 1 || stride * es % 16 == 0));
-  };
-  const bool vec = a.H % 8 == 0 && grid16(a.dy, a.dy_stride) && grid16(a.x, a.x_stride) &&
-                   grid16(a.dres, a.dres_stride) && grid16(a.dx, a.dx_stride) &&
-                   reinterpret_cast<uintptr_t>(a.weight) % 16 == 0;
-  if (a.dtype == kDtBf16) return launch_typed<kDtBf16>(a, vec, s);
-  if (a.dtype == kDtF16) return launch_typed<kDtF16>(a, vec, s);
-  return launch_typed<kDtF32>(a, vec, s);
+  const int64_t EP = 16 / es;
+  bool bases = true, strides = true, whole = a.H % 8 == 0;
+  for (const auto& m : {std::pair<const void*, int64_t>(a.dy, a.dy_stride), {a.x, a.x_stride}, {a.dres, a.dres_stride},
+                        {a.dx, a.dx_stride}}) {
+    if (m.first == nullptr) continue;
+    bases = bases && reinterpret_cast<uintptr_t>(m.first) % 16 == 0;
+    strides = strides && (a.T == 1 || m.second % EP == a.x_stride % EP);
+    whole = whole && (a.T == 1 || m.second % EP == 0);
+  }
+  const int64_t off = a.T == 1 ? 0 : a.x_stride % EP;
+  const int classes = !bases || !strides ? 0 : off == 0 ? 1 : off % 4 == 0 ? (int)(EP / 4) : off % 2 == 0 ? (int)(EP / 2) : (int)EP;
+  const bool vec = bases && whole && reinterpret_cast<uintptr_t>(a.weight) % 16 == 0;
+  if (a.dtype == kDtBf16) return launch_typed<kDtBf16>(a, vec, classes, s);
+  if (a.dtype == kDtF16) return launch_typed<kDtF16>(a, vec, classes, s);
+  return launch_typed<kDtF32>(a, vec, classes, s);
 }
 
 }  // namespace moe

@@ -209,6 +209,7 @@ def test_norm_backward_refuses(status, args):
 def test_norm_backward_workspace():
     f = moe.moe_rms_norm_backward_workspace_bytes
     assert f(1, 100) == 400 and f(0, 100) == 400 and f(1 << 20, 7168) == 304 * 7168 * 4
+    assert f(1 << 20, 100) == 456 * 100 * 4
     assert f(-1, 100) == 0 and f(5, 0) == 0 and f(5, 40000) == 0
 
 
