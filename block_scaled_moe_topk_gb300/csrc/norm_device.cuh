@@ -121,14 +121,91 @@ __device__ __forceinline__ void store8(void* x, int64_t base, int c, int n, cons
   }
 }
 
-// 8 values in pairs to column c of a row that lies on a 16-byte boundary; nothing from column n on.
+// The chunk at column c of a row, n columns from the thread's first on; the chunk starts on a 16-byte boundary.  SHIFT:
+// the row may begin and end inside it; what else it holds is memory's around the row, of which `room` columns from the
+// thread's first on belong to the matrix, and is trimmed where the chunk is used: a test of what was loaded would wait
+// for it before the next load is on its way.
+template <int DT, bool SHIFT>
+__device__ __forceinline__ Raw8<DT> row_chunk(const uint8_t* row, int c, int n, int room) {
+  constexpr int es = DT == kDtF32 ? 4 : 2, W = DT == kDtF32 ? 8 : 4;
+  if (!SHIFT || c + 8 <= room || c >= n) return raw8<DT>(row, 0, c, n);
+  Raw8<DT> r;  // the matrix's last chunk
+#pragma unroll
+  for (int k = 0; k < W; ++k) r.w[k] = 0;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    if (c + j < 0 || c + j >= n) continue;
+    if (DT == kDtF32) r.w[j & (W - 1)] = *reinterpret_cast<const uint32_t*>(row + (c + j) * es);
+    else r.w[(j / 2) & (W - 1)] |= (uint32_t)*reinterpret_cast<const uint16_t*>(row + (c + j) * es) << (16 * (j & 1));
+  }
+  return r;
+}
+
+// Zeros in place of the first `skip` elements and of those from `left` on.
 template <int DT>
-__device__ __forceinline__ void put8(uint8_t* row, int c, int n, const uint64_t (&v)[4]) {
+__device__ __forceinline__ void trim(Raw8<DT>& r, int skip, int left) {
+#pragma unroll
+  for (int k = 0; k < (DT == kDtF32 ? 8 : 4); ++k) {
+    if (DT == kDtF32) {
+      r.w[k] = k < skip || k >= left ? 0u : r.w[k];
+    } else {
+      const uint32_t lo = 2 * k < skip || 2 * k >= left ? 0u : 0xFFFFu, hi = 2 * k + 1 < skip || 2 * k + 1 >= left ? 0u : 0xFFFF0000u;
+      r.w[k] &= lo | hi;
+    }
+  }
+}
+
+// Elements [8 - S, 16 - S) of two neighbouring chunks.
+template <int DT, int S>
+__device__ __forceinline__ Raw8<DT> moved_up(const Raw8<DT>& lo, const Raw8<DT>& hi) {
+  constexpr int W = DT == kDtF32 ? 8 : 4, up = 8 - S, words = DT == kDtF32 ? up : up / 2;
+  Raw8<DT> r;
+  auto word = [&](int k) { return k < W ? lo.w[k & (W - 1)] : hi.w[k & (W - 1)]; };
+#pragma unroll
+  for (int k = 0; k < W; ++k)
+    r.w[k] = DT != kDtF32 && (up & 1) ? __funnelshift_r(word(k + words), word(k + words + 1), 16) : word(k + words);
+  return r;
+}
+
+// 8 elements of the weight [H], which starts on a 16-byte boundary, from column c = 8 i - shift on: the two chunks that
+// hold them, moved up in registers (a branch that the whole row takes alike).
+template <int DT, bool SHIFT>
+__device__ __forceinline__ Raw8<DT> weight_chunk(const void* w, int c, int H, int shift) {
+  const uint8_t* p = static_cast<const uint8_t*>(w);
+  if (!SHIFT) return raw8<DT>(p, 0, c, H);
+  const int i = c + shift;
+  const Raw8<DT> hi = row_chunk<DT, true>(p, i, H, H);
+  if (shift == 0) return hi;
+  Raw8<DT> lo = hi;
+  if (i >= 8) lo = row_chunk<DT, true>(p, i - 8, H, H);
+  switch (shift) {
+    case 1: return moved_up<DT, 1>(lo, hi);
+    case 2: return moved_up<DT, 2>(lo, hi);
+    case 3: return moved_up<DT, 3>(lo, hi);
+    case 4: return moved_up<DT, 4>(lo, hi);
+    case 5: return moved_up<DT, 5>(lo, hi);
+    case 6: return moved_up<DT, 6>(lo, hi);
+    default: return moved_up<DT, 7>(lo, hi);
+  }
+}
+
+// 8 values in pairs to the chunk at column c of a row; nothing from column n on, nor (SHIFT) in the first `skip`.
+template <int DT, bool SHIFT>
+__device__ __forceinline__ void put_chunk(uint8_t* row, int c, int n, int skip, const uint64_t (&v)[4]) {
   if (c >= n) return;
   float f[8];
 #pragma unroll
   for (int j = 0; j < 4; ++j) apart(v[j], f[2 * j], f[2 * j + 1]);
-  store8<DT, true>(row, 0, c, n, f);
+  if (!SHIFT || (c + 8 <= n && skip == 0)) {
+    store8<DT, true>(row, 0, c, n, f);
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    if (j < skip || c + j >= n) continue;
+    if (DT == kDtF32) reinterpret_cast<float*>(row)[c + j] = f[j];
+    else reinterpret_cast<uint16_t*>(row)[c + j] = (uint16_t)pack2<DT>(f[j], 0.0f);
+  }
 }
 
 // The sum over the tpr threads of a row (a power of two up to 32, or whole warps), the same for all of them, in an
