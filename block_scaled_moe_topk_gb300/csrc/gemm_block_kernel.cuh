@@ -244,10 +244,25 @@ __device__ __forceinline__ void load_rows_x(const BlockParams& p, uint32_t dst, 
   }
 }
 
+// A lane's row of WORDS words, on a 32-byte boundary (vec) or wherever it lies (store_words, store_halves).
+template <int WORDS>
+__device__ __forceinline__ void put_words(uint8_t* dst, uint32_t (&w)[WORDS], bool on, bool vec, bool halves) {
+  if (!vec) {
+    if (halves) store_halves<WORDS>(dst, w, on);
+    else store_words<WORDS>(dst, w, on);
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < WORDS; i += 8) {
+    const uint32_t t[8] = {w[i], w[i + 1], w[i + 2], w[i + 3], w[i + 4], w[i + 5], w[i + 6], w[i + 7]};
+    if (on) st_global_v8(dst + 4 * i, t);
+  }
+}
+
 // 32 rows of 64 columns, a row in each lane's `v`, to columns [c, c + 64) of rows row0... of `out` [M, ld], a.out_dtype:
 // the first `rows` rows, columns up to ld.  A pair's whole rows on 16-byte boundaries go by TMA stores of 128-byte pieces
-// through the warp's staging, two pieces in flight (`slot` counts them); rows on 32-byte boundaries by the
-// lanes; the rest 64 bytes of every row at a time through the staging, consecutive elements by consecutive lanes.
+// through the warp's staging, two pieces in flight (`slot` counts them); others by the lanes; the last columns 64
+// bytes of every row at a time through the staging, consecutive elements by consecutive lanes.
 template <int G>
 __device__ __forceinline__ void put_rows64(const typename BlockGeo<G>::Params& p, const float (&v)[64], void* out,
                                            bool products, int64_t ld, int c, int64_t row0, int rows, uint8_t* stage,
@@ -289,25 +304,24 @@ __device__ __forceinline__ void put_rows64(const typename BlockGeo<G>::Params& p
     }
   }
   uint8_t* base = static_cast<uint8_t*>(out) + (row0 * ld + c) * es;
-  if ((products ? p.gate_up_vec : p.out_vec) && c + 64 <= ld) {
+  // (A pair's kernel has no registers for the shifts of unaligned rows: with them in it aligned rows take 10 % longer.)
+  const bool vec = products ? p.gate_up_vec : p.out_vec;
+  if (c + 64 <= ld && (G == 1 || vec)) {
     uint8_t* dst = base + lane * ld * es;
-    if (lane >= rows) return;
+    const bool on = lane < rows;
     if (dt == kDtF32) {
 #pragma unroll
-      for (int i = 0; i < 64; i += 8) {
-        uint32_t w[8];
+      for (int q = 0; q < 2; ++q) {  // by halves: the products are still in registers
+        uint32_t w[32];
 #pragma unroll
-        for (int q = 0; q < 8; ++q) w[q] = __float_as_uint(v[i + q]);
-        st_global_v8(dst + 4 * i, w);
+        for (int i = 0; i < 32; ++i) w[i] = __float_as_uint(v[32 * q + i]);
+        put_words<32>(dst + 128 * q, w, on, G == 2 || vec, false);
       }
     } else {
+      uint32_t w[32];
 #pragma unroll
-      for (int i = 0; i < 64; i += 16) {
-        uint32_t w[8];
-#pragma unroll
-        for (int q = 0; q < 8; ++q) w[q] = out_pair(v[i + 2 * q], v[i + 2 * q + 1], dt);
-        st_global_v8(dst + 2 * i, w);
-      }
+      for (int i = 0; i < 32; ++i) w[i] = out_pair(v[2 * i], v[2 * i + 1], dt);
+      put_words<32>(dst, w, on, G == 2 || vec, true);
     }
     return;
   }
@@ -326,15 +340,29 @@ __device__ __forceinline__ void put_rows64(const typename BlockGeo<G>::Params& p
                                                   : out_pair(v[(32 * q + 2 * i) & 63], v[(32 * q + 2 * i + 1) & 63], dt);
     __syncwarp();
     if (dt == kDtF32) {
-      const int k = lane & 15;
-      for (int r = lane >> 4; r < nr; r += 2)
-        if (c + k0 + k < ld)
-          reinterpret_cast<uint32_t*>(base)[(int64_t)r * ld + k0 + k] = words[r * 16 + (k ^ ((r >> 1) & 15))];
+      const int k = lane & 15, r1 = lane >> 4;
+      uint32_t* dst = reinterpret_cast<uint32_t*>(base) + (int64_t)r1 * ld + k0 + k;
+      const int n = c + k0 + k < ld ? nr - r1 : 0;
+#pragma unroll 1
+      for (int i0 = 0; i0 < 16; i0 += 8) {  // eight reads, then eight stores
+        uint32_t w[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] = words[(2 * (i0 + i) + r1) * 16 + (k ^ (i0 + i))];
+#pragma unroll
+        for (int i = 0; i < 8; ++i, dst += 2 * ld)
+          if (2 * (i0 + i) < n) *dst = w[i];
+      }
     } else {
-      for (int r = 0; r < nr; ++r) {
-        const uint32_t w = words[r * 16 + ((lane >> 1) ^ ((r >> 1) & 15))];
-        if (c + k0 + lane < ld)
-          reinterpret_cast<uint16_t*>(base)[(int64_t)r * ld + k0 + lane] = (uint16_t)(lane & 1 ? w >> 16 : w);
+      uint16_t* dst = reinterpret_cast<uint16_t*>(base) + k0 + lane;
+      const int n = c + k0 + lane < ld ? nr : 0;
+#pragma unroll 1
+      for (int r0 = 0; r0 < 32; r0 += 8) {
+        uint32_t w[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] = words[(r0 + i) * 16 + ((lane >> 1) ^ ((r0 + i) >> 1))];
+#pragma unroll
+        for (int i = 0; i < 8; ++i, dst += ld)
+          if (r0 + i < n) *dst = (uint16_t)(lane & 1 ? w[i] >> 16 : w[i]);
       }
     }
   }
