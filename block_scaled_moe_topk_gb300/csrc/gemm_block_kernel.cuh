@@ -1388,9 +1388,14 @@ cudaError_t launch_direction(const GemmBlockArgs& a, cudaStream_t s) {
     if (singles <= clusters) break;
   }
   if (split > 1) return launch_tiles<1, KIND, true>(a, singles, split, s);
-  const uint64_t grid = KIND == kGated ? 0 : out_grid(a, a.out, cols);
+  // The gated product's outputs (its codes are always aligned); its pairs' unaligned rows take longer, through the staging:
+  // 48 x 1024 rows, K = 512, single / pair us: I = 2048 to codes 202 / 181, I = 2047 216 / 239; I = 1024, K = 2048, rows a
+  // group: 64 46 / 60, 192 69 / 65, 384 100 / 105, 512 131 / 122, 1024 233 / 207.
+  const uint64_t grid = KIND != kGated ? out_grid(a, a.out, cols)
+                                       : (a.out ? out_grid(a, a.out, a.N / 2) : 0) | (a.gate_up ? out_grid(a, a.gate_up, a.N) : 0);
+  const double pair_rest = grid % 16 == 0 && avg >= 32 ? 2.2 : KIND == kGated && grid % 16 != 0 ? 4.0 : 2.9;
   if (tile_time(a, 128, col_tiles, RB, 0.54, grid % 32 == 0 ? 3.0 : 3.4) <=
-      tile_time(a, 256, col_tiles, RB, 0.47, grid % 16 == 0 && avg >= 32 ? 2.2 : 2.9) + 2.4)
+      tile_time(a, 256, col_tiles, RB, 0.47, pair_rest) + 2.4)
     return launch_tiles<1, KIND, false>(a, singles, 1, s);
   return launch_tiles<2, KIND, false>(a, max_row_tiles(a, BlockGeo<2>::kRows) * col_tiles, 1, s);
 }
