@@ -785,25 +785,33 @@ def moe_gemm_fp8_block_swiglu(x, x_scale, w, w_scale, workspace, out=None, codes
     _want(out is not None or codes is not None, fn, "out or codes are needed")
     _want((codes is None) == (scales is None), fn, "codes and scales come together")
     dev, sw, sx = w.get_device(), w.shape, x.shape
-    if not (_fixed(w, dev, _U8) and len(sw) == 3 and sw[1] % 2 == 0 and dev >= 0):
+    if not (len(sw) == 3 and sw[1] % 2 == 0 and dev >= 0 and w.dtype is _U8 and w.is_contiguous()):
         _table(w, dev, _U8, (None, None, None), fn, "w")
         _want(sw[1] % 2 == 0, fn, f"w has {sw[1]} rows, gate and up make an even number")
     E, N, K = sw
-    if not (len(sx) == 2 and sx[1] == K and _fixed(x, dev, _U8) and _fixed(x_scale, dev, _F32) and
-            x_scale.shape == (sx[0], (K + 127) // 128) and _fixed(w_scale, dev, _F32) and
-            w_scale.shape == (E, (N + 127) // 128, (K + 127) // 128) and workspace.get_device() == dev):
-        _table(w_scale, dev, _F32, (E, (N + 127) // 128, (K + 127) // 128), fn, "w_scale")
+    if not (len(sx) == 2 and sx[1] == K and x.dtype is _U8 and x.get_device() == dev and x.is_contiguous()):
         _table(x, dev, _U8, (None, K), fn, "x")
-        _table(x_scale, dev, _F32, (sx[0], (K + 127) // 128), fn, "x_scale")
+    blocks = (K + 127) // 128
+    xp = _flat_at(x_scale, (sx[0], blocks), _F32, dev, fn, "x_scale")
+    wp = _flat_at(w_scale, (E, (N + 127) // 128, blocks), _F32, dev, fn, "w_scale")
+    _want(xp is not None and wp is not None, fn, "x_scale and w_scale are needed")
+    if workspace.get_device() != dev:
         _place(workspace, dev, fn, "the workspace")
     M, I = sx[0], N // 2
     dt = out.dtype if out is not None else gate_up.dtype if gate_up is not None else torch.bfloat16
     _want(dt in _ROWS, fn, "out and gate_up must be bf16, f16 or f32")
-    op = _flat_at(out, (M, I), dt, dev, fn, "out")
-    gp = _flat_at(gate_up, (M, N), dt, dev, fn, "gate_up")
-    cp = _flat_at(codes, (M, I), _U8, dev, fn, "codes")
-    sp = _flat_at(scales, (M, (I + 127) // 128), _F32, dev, fn, "scales")
-    rp = _flat_at(offsets, (E + 1,), _I64, dev, fn, "offsets")
-    _check(lib().moe_gemm_fp8_block_swiglu(x.data_ptr(), x_scale.data_ptr(), w.data_ptr(), w_scale.data_ptr(), layout,
-                                           rp, M, I, K, E, op, gp, _DTYPES[dt], cp, sp, workspace.data_ptr(),
-                                           workspace.nbytes, _launch_stream(stream, dev, fn)), fn)
+    op = gp = cp = sp = rp = None
+    if out is not None:
+        op = _flat_at(out, (M, I), dt, dev, fn, "out")
+    if gate_up is not None:
+        gp = _flat_at(gate_up, (M, N), dt, dev, fn, "gate_up")
+    if codes is not None:
+        cp = _flat_at(codes, (M, I), _U8, dev, fn, "codes")
+        sp = _flat_at(scales, (M, (I + 127) // 128), _F32, dev, fn, "scales")
+    if offsets is not None:
+        rp = _flat_at(offsets, (E + 1,), _I64, dev, fn, "offsets")
+    status = lib().moe_gemm_fp8_block_swiglu(x.data_ptr(), xp, w.data_ptr(), wp, layout, rp, M, I, K, E, op, gp,
+                                             _DTYPES[dt], cp, sp, workspace.data_ptr(), workspace.nbytes,
+                                             _launch_stream(stream, dev, fn))
+    if status:
+        _check(status, fn)

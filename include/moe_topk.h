@@ -421,14 +421,16 @@ moe_status_t moe_profile_forward(moe_act_fmt_t fmt, const void* x_bf16, const fl
  *
  * The steps of the layer for callers that build their own: token rows to expert rows and back on
  * the permutation of moe_sort_by_expert, experts kept as FP8 codes with one fp32 scale per block
- * of 128, and the gradients that train a router (and what lies before it) through such experts:
- *   moe_topk_route, moe_sort_by_expert, moe_permute_quantize_fp8_block, moe_gemm_fp8_block,
- *   (activation, moe_quantize_fp8_block, moe_gemm_fp8_block,) moe_unpermute; then backward
- *   moe_unpermute_backward, moe_quantize_fp8_block, moe_gemm_fp8_block_dgrad,
- *   moe_permute_backward, moe_topk_route_backward.
+ * of 128, the norm in front of them, and the gradients that train a router (and what lies before it)
+ * through such experts:
+ *   moe_rms_norm_quantize_fp8_block (then moe_permute of codes and scales), or
+ *   moe_permute_quantize_fp8_block; moe_topk_route, moe_sort_by_expert, moe_gemm_fp8_block_swiglu,
+ *   moe_gemm_fp8_block, moe_unpermute; then backward
+ *   moe_unpermute_backward, moe_quantize_fp8_block, moe_gemm_fp8_block_dgrad, moe_swiglu_backward,
+ *   moe_gemm_fp8_block_dgrad, moe_permute_backward, moe_topk_route_backward, moe_rms_norm_backward.
  * The rules of this header hold (device pointers, caller's buffers, argument checks before any
- * launch, one kernel per call, capturable).  Outputs must not overlap inputs, but for
- * moe_unpermute_backward's d_rows, which may be rows itself.
+ * launch, one kernel per call but for a norm's weight gradient, capturable).  Outputs must not overlap
+ * inputs where a call does not say so.
  *
  * Common arguments
  *   inv      int32 [T, k]: the expert row of slot j of token t.  The `inv` of moe_sort_by_expert is
