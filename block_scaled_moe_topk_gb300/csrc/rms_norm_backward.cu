@@ -9,7 +9,7 @@
 // what it will read itself, so no barrier guards the ring.  Rows that start off the 16-byte boundaries are
 // copied from the boundary below: a thread's columns then begin `shift` elements earlier.  The shift repeats
 // every 2 to 8 rows, and a block takes rows of one shift only, so that its columns of dw stay its own
-// (37401 x 1570 bf16 with d_residual 317 us element by element, 129 so; 8192 x 7167 90 against 82 of 7168).  Rows of matrices that disagree on the shift,
+// (37401 x 1570 bf16 with d_residual 317 us element by element, 128 so; 8192 x 7167 86-98 against 82 of 7168).  Rows of matrices that disagree on the shift,
 // and rows too long for the ring, are read directly, twice (the second time from L1 or L2).
 #include <algorithm>
 #include <atomic>
@@ -60,31 +60,41 @@ __device__ __forceinline__ float row_sum_again(float v, int tpr, int rb, int tur
   return v;
 }
 
-// The block's sums of dw, N columns a thread, the q-th at column col(q).  Rows that share a warp meet by shuffles, the
-// warps (or groups of warps) of different rows in shared memory, one after the other: the same order every time.
-template <int N, typename Col>
-__device__ __forceinline__ void leave_dw(const NormBackwardParams& p, Col col, float* sums, float (&dw)[N]) {
-  const int H = p.a.H, tpr = p.tpr, lane = threadIdx.x & 31;
+// The block's sums of dw, N values a thread.  `first` is the place of the thread's first one, `shift` places before which is
+// column 0; the others follow in pieces of EP, 8 tpr apart (EP = 1: 32 apart, eight of them).  Rows that share a warp
+// meet by shuffles; the warps (or groups of warps) of different rows lay theirs side by side in shared memory, where each
+// column is added up in the groups' order and leaves in the columns' order.  A call, once a block: inlined, it costs
+// the loop in front of it registers (8192 x 7168 82 -> 94 us, 37401 x 1570 128 -> 211).
+template <int N, int EP>
+__device__ __noinline__ void leave_dw(float* out, int H, int tpr, int first, int shift, float* sums, float* values) {
+  const int lane = threadIdx.x & 31;
+  float dw[N];
+#pragma unroll
+  for (int q = 0; q < N; ++q) dw[q] = values[q];
+  auto col = [&](int q) {
+    return EP == 1 ? first + (q / 8) * 8 * tpr + 32 * (q % 8) : first + (q / EP) * tpr * EP + q % EP;
+  };
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1)
     if (o >= tpr) {
 #pragma unroll
       for (int q = 0; q < N; ++q) dw[q] += __shfl_xor_sync(0xffffffffu, dw[q], o);
     }
-  const int per = max(tpr, 32), groups = (blockDim.x + per - 1) / per, mine = threadIdx.x / per;
-  for (int g = 0; g < groups; ++g) {
-    if (g == mine && (tpr >= 32 || lane < tpr)) {
+  const int per = max(tpr, 32), groups = (blockDim.x + per - 1) / per, slots = tpr * N;
+  float* mine = sums + (threadIdx.x / per) * slots;
+  if (tpr >= 32 || lane < tpr) {
 #pragma unroll
-      for (int q = 0; q < N; ++q) {
-        const int c = col(q);
-        if (c >= 0 && c < H) sums[c] = g > 0 ? sums[c] + dw[q] : dw[q];
-      }
+    for (int q = 0; q < N; q += EP >= 4 ? 4 : 1) {
+      if (EP >= 4) *reinterpret_cast<float4*>(mine + col(q)) = make_float4(dw[q], dw[(q + 1) % N], dw[(q + 2) % N], dw[(q + 3) % N]);
+      else mine[col(q)] = dw[q];
     }
-    __syncthreads();
   }
-  // a thread's own columns are 16 bytes or more apart from its neighbour's: the row leaves in order instead
-  float* out = p.a.partial + (int64_t)blockIdx.x * H;
-  for (int c = threadIdx.x; c < H; c += blockDim.x) out[c] = sums[c];
+  __syncthreads();
+  for (int c = threadIdx.x; c < H; c += blockDim.x) {
+    float v = sums[c + shift];
+    for (int g = 1; g < groups; ++g) v += sums[g * slots + c + shift];
+    out[c] = v;
+  }
 }
 
 template <int DT, bool VEC>
@@ -161,16 +171,22 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) norm_backward_ring_kernel(con
     const int c = col(q);
 #pragma unroll
     for (int j = 0; j < EP; ++j) w[q][j] = 0.0f;
-    if (c >= H) return;
     const bool same = DT != kDtF32 && a.weight_dtype == DT;
-    const uint8_t* at = static_cast<const uint8_t*>(a.weight) + (int64_t)c * (same ? 2 : 4);
-    if (SHIFT && (c < 0 || c + EP > H || (reinterpret_cast<uintptr_t>(at) & 15) != 0)) {
+    if (SHIFT) {  // element by element, all loads on their way at once: a test each would wait for each
+      auto elements = [&](auto load) {
+        float f[EP];
 #pragma unroll
-      for (int j = 0; j < EP; ++j) {
-        if (c + j < 0 || c + j >= H) continue;
-        w[q][j] = same ? load1<DT>(a.weight, c + j) : load1<kDtF32>(a.weight, c + j);
-      }
-    } else if (same) {
+        for (int j = 0; j < EP; ++j) f[j] = load(min(max(c + j, 0), H - 1));
+#pragma unroll
+        for (int j = 0; j < EP; ++j) w[q][j] = c + j >= 0 && c + j < H ? f[j] : 0.0f;
+      };
+      if (same) elements([&](int k) { return load1<DT>(a.weight, k); });
+      else elements([&](int k) { return load1<kDtF32>(a.weight, k); });
+      return;
+    }
+    if (c >= H) return;
+    const uint8_t* at = static_cast<const uint8_t*>(a.weight) + (int64_t)c * (same ? 2 : 4);
+    if (same) {
       const uint4 v = *reinterpret_cast<const uint4*>(at);
 #pragma unroll
       for (int j = 0; j < EP / 2; ++j) apart(pair(v, j), w[q][2 * j], w[q][2 * j + 1]);
@@ -263,7 +279,7 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) norm_backward_ring_kernel(con
   for (int q = 0; q < NP; ++q)
 #pragma unroll
     for (int j = 0; j < EP / 2; ++j) apart(dw[q][j], sums[q * EP + 2 * j], sums[q * EP + 2 * j + 1]);
-  leave_dw<NP * EP>(p, [&](int q) { return col(q / EP) + q % EP; }, reinterpret_cast<float*>(ring), sums);
+  leave_dw<NP * EP, EP>(a.partial + (int64_t)blockIdx.x * H, H, tpr, first + shift, shift, reinterpret_cast<float*>(ring), sums);
 }
 
 // Rows read directly.
@@ -322,7 +338,7 @@ __global__ void __launch_bounds__(kNbMaxThreads, 1) norm_backward_kernel(const _
   float sums[NCH * 8];
 #pragma unroll
   for (int q = 0; q < NCH * 8; ++q) sums[q] = dw[q / 8][q % 8];
-  leave_dw<NCH * 8>(p, [&](int q) { return map.col(q / 8) + (VEC ? 1 : 32) * (q % 8); }, reinterpret_cast<float*>(ring), sums);
+  leave_dw<NCH * 8, VEC ? 8 : 1>(a.partial + (int64_t)blockIdx.x * H, H, tpr, map.col(0), 0, reinterpret_cast<float*>(ring), sums);
 }
 
 // dw[c] = the blocks' sums of column c.  32 columns a block, 16 threads a column, each with all its loads in flight.
@@ -367,6 +383,12 @@ Shape shape_of(int chunks, int nch, bool vec, int64_t T) {
   }
   s.rpb = (int)std::min<int64_t>(std::max(1, kNbThreads / s.tpr), T);
   return s;
+}
+
+// What leave_dw lays out.
+int64_t sums_bytes(const Shape& s, int threads, int nch) {
+  const int per = std::max(s.tpr, 32);
+  return (int64_t)((threads + per - 1) / per) * s.tpr * nch * 8 * 4;
 }
 
 template <typename K>
@@ -421,7 +443,7 @@ cudaError_t launch_typed(const NormBackwardArgs& a, bool vec, int classes, cudaS
     int64_t grid = std::min<int64_t>(152 * blocks_an_sm(a.H, es), (a.T + sh.rpb - 1) / sh.rpb);
     // the same number of blocks for every class, or one for each of fewer rows than classes
     grid = std::max<int64_t>(grid / classes * classes, std::min<int64_t>(classes, a.T));
-    const int64_t smem = std::max<int64_t>(p.stages * stage, 4 * (int64_t)a.H);
+    const int64_t smem = std::max<int64_t>(p.stages * stage, sums_bytes(sh, threads, nch));
     // a weight off the 16-byte boundaries is read as under a shift
     const bool shift = classes > 1 || a.H % EP != 0 || reinterpret_cast<uintptr_t>(a.weight) % 16 != 0;
     err = nch == 2 ? launch_ring<DT, 2, kNbHeldThreads, 2>(p, shift, (int)grid, threads, smem, s)
@@ -433,7 +455,7 @@ cudaError_t launch_typed(const NormBackwardArgs& a, bool vec, int classes, cudaS
     p.rpb = sh.rpb;
     threads = (sh.tpr * sh.rpb + 31) / 32 * 32;
     const int grid = (int)std::min<int64_t>(norm_backward_parts(a.T, a.H), (a.T + sh.rpb - 1) / sh.rpb);
-    const int64_t smem = 4 * (int64_t)a.H;
+    const int64_t smem = sums_bytes(sh, threads, 8);
     static std::atomic<int> ready[2][64];
     err = vec ? allow_smem(norm_backward_kernel<DT, true>, ready[0]) : allow_smem(norm_backward_kernel<DT, false>, ready[1]);
     if (err != cudaSuccess) return err;
