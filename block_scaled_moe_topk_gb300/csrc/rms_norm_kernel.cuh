@@ -10,7 +10,7 @@
 //
 // A row belongs to `tpr` threads of a block.  With rows on 16-byte boundaries a thread owns chunks of 8
 // columns (one 16-byte access of 16-bit elements), so 16 lanes hold a 1x128 block and 4 lanes an MX
-// block of 32.  16-bit rows with a residual that start off those boundaries, all matrices' alike (contiguous ones of an
+// block of 32.  Long 16-bit rows with a residual that start off those boundaries, all matrices' alike (contiguous ones of an
 // odd width), are read and written the same way from the boundary below (SHIFT: a thread's columns then begin up to 7
 // earlier, and the weight's are moved up to them in registers); for codes y passes through shared memory.  Other rows
 // go element by element, a warp owning spans of 256 columns, element j of a lane at column 32 j + lane.
@@ -188,12 +188,15 @@ __global__ void __launch_bounds__(THREADS, 1) rms_norm_single_kernel(const __gri
 }
 
 constexpr int kRowsBytes = 48 * 1024;  // of y in shared memory
+// Element by element, 20 M elements of bf16, four / one chunks a thread, us: without residual H = 499 42 / 29, 1501 34 /
+// 29, 3001 34 / 32, 6001 33 / 49; to codes with residual 499 89 / 50, 1501 69 / 50, 3001 69 / 54, 6001 69 / 77.
+constexpr int kSingleOnes = 512;  // chunks: 4096 columns
 
-// One chunk a thread while the rows leave SMs idle (more threads in flight, less work behind the last
-// load); else four (fewer threads to bring together a row), eight where four do not hold the row.
-NormParams shape_of(const NormArgs& a, int chunks, bool whole_warps, int* nch, int* threads, unsigned* grid) {
+// One chunk a thread up to `ones` chunks a row, and while the rows leave SMs idle (more threads in flight, less work behind
+// the last load); else four (fewer threads to bring together a row), eight where four do not hold the row.
+NormParams shape_of(const NormArgs& a, int chunks, int ones, bool whole_warps, int* nch, int* threads, unsigned* grid) {
   NormParams p{a, 0, 1};
-  *nch = chunks <= 32 || (a.T <= kSpreadRows && chunks <= 1024) ? 1 : chunks <= 4 * 512 ? 4 : 8;
+  *nch = chunks <= ones || (a.T <= kSpreadRows && chunks <= 1024) ? 1 : chunks <= 4 * 512 ? 4 : 8;
   p.tpr = (chunks + *nch - 1) / *nch;
   if (!whole_warps && p.tpr <= 16) p.tpr = 16;
   else p.tpr = (p.tpr + 31) / 32 * 32;
@@ -209,7 +212,7 @@ cudaError_t launch_chunks(const NormArgs& a, cudaStream_t s) {
   int nch, threads;
   unsigned grid;
   const bool rows = SHIFT && QF != kQuantNone;
-  const NormParams p = shape_of(a, (a.H + (SHIFT ? 16 / dtype_bytes(DT) - 1 : 0) + 7) / 8, rows, &nch, &threads, &grid);
+  const NormParams p = shape_of(a, (a.H + (SHIFT ? 16 / dtype_bytes(DT) - 1 : 0) + 7) / 8, 32, rows, &nch, &threads, &grid);
   const size_t smem = rows ? (size_t)p.rpb * a.H * 4 : 0;
   // Blocks an SM that the registers leave room for, 16-bit rows of up to 7168 columns; 8192 x 7168 bf16, us, with 1,
   // 4, 5, 6 blocks asked for: with residual 69.4, 69.0, 74, 117; to codes 69.9, 62.8, 75, 115; without residual
@@ -231,7 +234,7 @@ template <int DT, int QF>
 cudaError_t launch_single(const NormArgs& a, cudaStream_t s) {
   int nch, threads;
   unsigned grid;
-  const NormParams p = shape_of(a, (a.H + 255) / 256 * 32, true, &nch, &threads, &grid);
+  const NormParams p = shape_of(a, (a.H + 255) / 256 * 32, kSingleOnes, true, &nch, &threads, &grid);
   if (nch == 1) rms_norm_single_kernel<DT, 1, QF, 1024><<<grid, threads, 0, s>>>(p);
   else if (nch == 4) rms_norm_single_kernel<DT, 4, QF, 512><<<grid, threads, 0, s>>>(p);
   else rms_norm_single_kernel<DT, 8, QF, 512><<<grid, threads, 0, s>>>(p);
@@ -243,11 +246,10 @@ template <int DT, int QF>
 cudaError_t launch_typed(const NormArgs& a, bool vec, bool shifted, cudaStream_t s) {
   const bool res = a.residual != nullptr;
   if (vec) return res ? launch_chunks<DT, QF, true, false>(a, s) : launch_chunks<DT, QF, false, false>(a, s);
-  // bf16, shifted / element by element, us: with residual 8192 x 7167 110 / 123, 2000 x 3001 14 / 21, 28083 x 843 57 / 53,
-  // 60000 x 99 20 / 26, to codes 10742 x 5466 162 / 197; without 8192 x 7166 85 / 74, 28083 x 843 45 / 35, to codes 38990
-  // x 753 98 / 68; fp32 38990 x 753 to codes 103 / 67
+  // bf16, shifted / element by element, us: with residual 8192 x 7167 110 / 123, 20 M elements of H = 1501 51 / 42, 3001 35 /
+  // 45, 6001 34 / 52; to codes 3001 62 / 54, 6001 62 / 69; without residual 8192 x 7166 85 / 74; fp32 is no faster
   if constexpr (QF != kQuantMx && DT != kDtF32) {
-    if (shifted && res) return launch_chunks<DT, QF, true, true>(a, s);
+    if (shifted && res && a.H > (QF == kQuantNone ? 2048 : 4096)) return launch_chunks<DT, QF, true, true>(a, s);
   }
   return launch_single<DT, QF>(a, s);
 }
