@@ -25,6 +25,9 @@ __global__ void __launch_bounds__(kGsThreads) gemv_swiglu_kernel(const __grid_co
   constexpr int kCluster = kFp8Block / (kGsWarps * C);  // blocks of a scale block
   __shared__ float warp_max[MR][kGsWarps], block_max[MR][kCluster];
   __shared__ int group;
+  // Every block of the cluster has to run before another one stores into its shared memory; the wait stands before those
+  // stores, so that the loads hide it.
+  if (CODES) cluster_arrive_relaxed();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x < 8)
     a.status[threadIdx.x] = threadIdx.x == kFormWord ? kFormVector : 0;
@@ -38,7 +41,10 @@ __global__ void __launch_bounds__(kGsThreads) gemv_swiglu_kernel(const __grid_co
       if (r0 >= group_start(a.offsets, i, a.M) && r0 < group_start(a.offsets, i + 1, a.M)) group = i;
     __syncthreads();
     e = group;
-    if (e < 0) return;  // the whole cluster has this row
+    if (e < 0) {  // the whole cluster has this row
+      if (CODES) cluster_wait();
+      return;
+    }
   }
   const int K = a.K, KB = (K + kFp8Block - 1) / kFp8Block, NB = (a.N + kFp8Block - 1) / kFp8Block;
   // gate and up rows of the warp's columns; a warp's columns share their scales (C divides 64, and j0 C)
@@ -126,6 +132,7 @@ __global__ void __launch_bounds__(kGsThreads) gemv_swiglu_kernel(const __grid_co
   }
   if (!CODES) return;
   __syncthreads();
+  cluster_wait();
   const uint32_t rank = cluster_ctarank();
   if (threadIdx.x < MR * kCluster) {  // this block's maximum of row m, to block `to` of the cluster
     const int m = threadIdx.x / kCluster, to = threadIdx.x % kCluster;

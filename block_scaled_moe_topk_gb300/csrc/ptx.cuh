@@ -221,6 +221,10 @@ __device__ __forceinline__ uint32_t mapa_shared(uint32_t saddr, uint32_t rank) {
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
+// The same in two halves that order no memory: whoever is past the wait knows that every CTA of the cluster runs, which an
+// access to its shared memory needs.
+__device__ __forceinline__ void cluster_arrive_relaxed() { asm volatile("barrier.cluster.arrive.relaxed.aligned;"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.aligned;" ::: "memory"); }
 // 32-bit load from a shared::cluster address (this CTA's or the peer's shared memory).
 __device__ __forceinline__ uint32_t ld_shared_cluster_u32(uint32_t caddr) {
   uint32_t v;
