@@ -133,11 +133,12 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) norm_backward_ring_kernel(con
     const uint8_t* dy = static_cast<const uint8_t*>(a.dy) + r * a.dy_stride * es;
     const uint8_t* x = static_cast<const uint8_t*>(a.x) + r * a.x_stride * es;
     const uint8_t* dres = DRES ? static_cast<const uint8_t*>(a.dres) + r * a.dres_stride * es : nullptr;
+    const int below = SHIFT && on ? -shift * es : 0;  // the boundary below the row (r = 0 lies on one itself)
 #pragma unroll
     for (int q = 0; q < NP; ++q) {
       const int c = col(q);
       const int bytes = !on || c >= H ? 0 : SHIFT ? min((H - c) * es, 16) : 16;  // nothing behind the row's end
-      const int o = bytes > 0 ? c * es : 0;
+      const int o = bytes > 0 ? c * es : below;  // a copy of nothing has to name a 16-byte boundary too
       const uint32_t at = dst + (uint32_t)q * piece;
       copy16(at, dy + o, bytes);
       copy16(at + array, x + o, bytes);
