@@ -188,7 +188,7 @@ __global__ void __launch_bounds__(THREADS, 1) rms_norm_single_kernel(const __gri
   }
 }
 
-constexpr int kRowsBytes = 48 * 1024;  // of y in shared memory
+constexpr int kRowsBytes = 48 * 1024 - 32 * 4;  // of y in shared memory: a block's default limit less row_sum's 32 words
 // Element by element, 20 M elements of bf16, four / one chunks a thread, us: without residual H = 499 42 / 29, 1501 34 /
 // 29, 3001 34 / 32, 6001 33 / 49; to codes with residual 499 89 / 50, 1501 69 / 50, 3001 69 / 54, 6001 69 / 77.
 constexpr int kSingleOnes = 512;  // chunks: 4096 columns
