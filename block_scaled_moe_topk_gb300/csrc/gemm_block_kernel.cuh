@@ -856,11 +856,21 @@ __global__ void __launch_bounds__(kBThreads, 1)
             if (c < 2 * cols) put_rows64<G>(p, v, a.gate_up, true, 2 * cols, c, row - lane, rows_here, stage, slot);
           }
         }
-        float h[64];
+        // the smallest gate or NaN, in four chains (one chain's latency: 189 us for 186 at 48 x 1024 rows, I = 2048, K = 512)
+        float least[4];
 #pragma unroll
-        for (int i = 0; i < 64; i += 2) {
-          const uint64_t g = two(acc[i], acc[i + 1]);
-          apart(mul2(mul2(g, sigmoid2(g)), two(acc[64 + i], acc[65 + i])), h[i], h[i + 1]);
+        for (int i = 0; i < 64; ++i) least[i & 3] = i < 4 ? acc[i] : min_or_nan(least[i & 3], acc[i]);
+        const bool far = !(min_or_nan(min_or_nan(least[0], least[1]), min_or_nan(least[2], least[3])) >= kFarGate);
+        float h[64];
+        // (gates put right behind a single loop: all of acc and h live at once, 236-352 bytes of spills a thread)
+        if (__any_sync(0xffffffffu, far)) {
+#pragma unroll
+          for (int i = 0; i < 64; i += 2)
+            apart(gated2<true>(two(acc[i], acc[i + 1]), two(acc[64 + i], acc[65 + i])), h[i], h[i + 1]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 64; i += 2)
+            apart(gated2<false>(two(acc[i], acc[i + 1]), two(acc[64 + i], acc[65 + i])), h[i], h[i + 1]);
         }
         if (a.out != nullptr && any) put_rows64<G>(p, h, a.out, false, cols, col0, row - lane, rows_here, stage, slot);
         if (a.codes != nullptr) {

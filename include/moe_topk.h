@@ -575,7 +575,7 @@ typedef enum { MOE_GATE_UP_INTERLEAVED = 0, MOE_GATE_UP_STACKED = 1 } moe_gate_u
  *   d_gate_up  out, or NULL; may be gate_up itself, with its stride
  *   codes, scales  u8 [R, 2I], fp32 [R, ceil(2I / 128)] out: the same as FP8 codes, quantised from fp32 as
  *              moe_quantize_fp8_block does, for moe_gemm_fp8_block_dgrad; or both NULL
- * At least one form of the result is given.
+ * At least one form of the result is given.  A logistic function below 2^-126 (gates below -87) may count as 0.
  */
 moe_status_t moe_swiglu_backward(const void* gate_up, int64_t gate_up_stride, const void* d_h, int64_t d_h_stride,
                                  moe_dtype_t dtype, moe_gate_up_t layout, int64_t R, int I, void* d_gate_up,
@@ -627,7 +627,8 @@ moe_status_t moe_gemm_fp8_block_dgrad(const uint8_t* dy, const float* dy_scale, 
  *              or NULL
  *   codes, scales  u8 [M, I] (16-byte aligned, I % 16 == 0), fp32 [M, ceil(I / 128)]: h as FP8 codes, as
  *              moe_quantize_fp8_block writes them and the next moe_gemm_fp8_block reads them; or both NULL
- * out or codes is given, or both.  2I <= 65536.  The gradient: moe_swiglu_backward, then
+ * out or codes is given, or both.  2I <= 65536.  A logistic function below 2^-126 (gates below -87) may count as 0.  An
+ * infinite or NaN scale leaves its row (its columns) without finite values.  The gradient: moe_swiglu_backward, then
  * moe_gemm_fp8_block_dgrad with w.
  */
 moe_status_t moe_gemm_fp8_block_swiglu(const uint8_t* x, const float* x_scale, const uint8_t* w, const float* w_scale,
