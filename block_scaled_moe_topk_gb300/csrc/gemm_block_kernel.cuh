@@ -468,8 +468,11 @@ __device__ __forceinline__ void gated_split_end(const BlockParams& p, uint8_t* s
     const BlockScale sc = computed_scale(row_amax[r]);
     const float4 hv = hbuf[i];
     const float h[4] = {hv.x, hv.y, hv.z, hv.w};
+    bool infinite = false;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) infinite |= fabsf(h[q]) > 3.402823466e38f;
     uint32_t w[1];
-    encode<4>(h, sc.mult, w);
+    encode_computed<4>(h, sc.mult, infinite, w);
     *reinterpret_cast<uint32_t*>(a.codes + (row0 + r) * I + col) = w[0];
     if (j == 0) a.scales[(row0 + r) * NT + nt] = sc.scale;
   }

@@ -151,8 +151,11 @@ __global__ void __launch_bounds__(kGsThreads) gemv_swiglu_kernel(const __grid_co
     const BlockScale sc = computed_scale(v);
     if (lane != 0 || r0 + m >= a.M) continue;
 #pragma unroll
-    for (int q = 0; q < C; ++q)
-      if (j0 + q < I) a.codes[(r0 + m) * I + j0 + q] = (uint8_t)encode2(h[m][q], 0.0f, sc.mult);
+    for (int q = 0; q < C; ++q) {
+      uint32_t w[1];
+      encode_computed<1>(&h[m][q], sc.mult, fabsf(h[m][q]) > 3.402823466e38f, w);
+      if (j0 + q < I) a.codes[(r0 + m) * I + j0 + q] = (uint8_t)w[0];
+    }
     if (j0 < I && j0 % kFp8Block == 0)
       a.scales[(r0 + m) * ((I + kFp8Block - 1) / kFp8Block) + j0 / kFp8Block] = sc.scale;
   }

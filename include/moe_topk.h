@@ -526,9 +526,9 @@ moe_status_t moe_rms_norm(const void* x, int64_t x_stride, const void* residual,
                           void* out, int64_t out_stride, void* residual_out, int64_t residual_out_stride, float* rstd,
                           void* stream);
 
-/* The same with y as FP8 codes, quantised from fp32 as moe_quantize_fp8_block (block_rows = 1) does, the
- * scale to one unit in the last place: codes u8 [T, H], scales fp32 [T, ceil(H / 128)].  out may be NULL; given, it gets y too (a router
- * reads it while the experts read the codes). */
+/* The same with y as FP8 codes, quantised from fp32 as moe_quantize_fp8_block (block_rows = 1) does: codes u8 [T, H],
+ * scales fp32 [T, ceil(H / 128)].  out may be NULL; given, it gets y too (a router reads it while the experts read the
+ * codes). */
 moe_status_t moe_rms_norm_quantize_fp8_block(const void* x, int64_t x_stride, const void* residual,
                                              int64_t residual_stride, moe_dtype_t dtype, const void* weight,
                                              moe_dtype_t weight_dtype, float eps, int64_t T, int H, uint8_t* codes,
