@@ -373,7 +373,8 @@ __device__ __forceinline__ void red_max_shared_cluster(uint32_t caddr, uint32_t 
   asm volatile("red.relaxed.cluster.shared::cluster.max.u32 [%0], %1;" ::"r"(caddr), "r"(v) : "memory");
 }
 
-// 4 neighbouring elements from element `at` on of an output of rows of `ld`, of which the last `over` are past the row.
+// 4 neighbouring elements from element `at` on of an output, of which the first `left` (all, if it is more) are the row's.
+// vec: they may be stored as one.
 __device__ __forceinline__ void put4(const GemmBlockArgs& a, void* out, bool vec, int64_t at, int left, float4 v) {
   const float f[4] = {v.x, v.y, v.z, v.w};
   if (vec && left >= 4) {

@@ -121,8 +121,8 @@ __device__ __forceinline__ void store8(void* x, int64_t base, int c, int n, cons
   }
 }
 
-// The chunk at column c of a row, n columns from the thread's first on; the chunk starts on a 16-byte boundary.  SHIFT:
-// the row may begin and end inside it; what else it holds is memory's around the row, of which `room` columns from the
+// The chunk at column c of a row, n columns from the thread's first on; the chunk starts on a 16-byte boundary.  SHIFT
+// (16-bit rows, and the weight, which may be fp32): the row may begin and end inside it; what else it holds is memory's around the row, of which `room` columns from the
 // thread's first on belong to the matrix, and is trimmed where the chunk is used: a test of what was loaded would wait
 // for it before the next load is on its way.
 template <int DT, bool SHIFT>
@@ -141,17 +141,15 @@ __device__ __forceinline__ Raw8<DT> row_chunk(const uint8_t* row, int c, int n, 
   return r;
 }
 
-// Zeros in place of the first `skip` elements and of those from `left` on.
+// Zeros in place of the first `skip` of 8 16-bit elements and of those from `left` on.
 template <int DT>
 __device__ __forceinline__ void trim(Raw8<DT>& r, int skip, int left) {
+  static_assert(DT != kDtF32, "shifted rows are 16-bit rows");
 #pragma unroll
-  for (int k = 0; k < (DT == kDtF32 ? 8 : 4); ++k) {
-    if (DT == kDtF32) {
-      r.w[k] = k < skip || k >= left ? 0u : r.w[k];
-    } else {
-      const uint32_t lo = 2 * k < skip || 2 * k >= left ? 0u : 0xFFFFu, hi = 2 * k + 1 < skip || 2 * k + 1 >= left ? 0u : 0xFFFF0000u;
-      r.w[k] &= lo | hi;
-    }
+  for (int k = 0; k < 4; ++k) {
+    const uint32_t lo = 2 * k < skip || 2 * k >= left ? 0u : 0xFFFFu;
+    const uint32_t hi = 2 * k + 1 < skip || 2 * k + 1 >= left ? 0u : 0xFFFF0000u;
+    r.w[k] &= lo | hi;
   }
 }
 
@@ -200,12 +198,10 @@ __device__ __forceinline__ void put_chunk(uint8_t* row, int c, int n, int skip, 
     store8<DT, true>(row, 0, c, n, f);
     return;
   }
+  static_assert(!SHIFT || DT != kDtF32, "shifted rows are 16-bit rows");
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    if (j < skip || c + j >= n) continue;
-    if (DT == kDtF32) reinterpret_cast<float*>(row)[c + j] = f[j];
-    else reinterpret_cast<uint16_t*>(row)[c + j] = (uint16_t)pack2<DT>(f[j], 0.0f);
-  }
+  for (int j = 0; j < 8; ++j)
+    if (j >= skip && c + j < n) reinterpret_cast<uint16_t*>(row)[c + j] = (uint16_t)pack2<DT>(f[j], 0.0f);
 }
 
 // The sum over the tpr threads of a row (a power of two up to 32, or whole warps), the same for all of them, in an

@@ -65,7 +65,7 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) rms_norm_kernel(const __grid_
 #pragma unroll
     for (int c = 0; c < NCH; ++c) wr[c] = weight_chunk<DT, SHIFT>(a.weight, first + c * step, on ? H : 0, shift);
   }
-  if (SHIFT) {
+  if constexpr (SHIFT) {
 #pragma unroll
     for (int c = 0; c < NCH; ++c)
       if ((c == 0 && skip > 0) || c * step + 8 > n) {
