@@ -1403,8 +1403,8 @@ cudaError_t launch_direction(const GemmBlockArgs& a, cudaStream_t s) {
   }
   if (split > 1) return launch_tiles<1, KIND, true>(a, singles, split, s);
   // The gated product's outputs (its codes are always aligned); its pairs' unaligned rows take longer, through the staging:
-  // 48 x 1024 rows, K = 512, single / pair us: I = 2048 to codes 202 / 181, I = 2047 216 / 239; I = 1024, K = 2048, rows a
-  // group: 64 46 / 60, 192 69 / 65, 384 100 / 105, 512 131 / 122, 1024 233 / 207.
+  // 48 x 1024 rows, single / pair us: I = 2048, K = 512 to codes 206 / 185; I = 2047 218 / 244, K = 2048 461 / 460; I = 1024,
+  // K = 2048, rows a group: 64 46 / 60, 192 68 / 64, 512 130 / 122, 1024 233 / 209.
   const uint64_t grid = KIND != kGated ? out_grid(a, a.out, cols)
                                        : (a.out ? out_grid(a, a.out, a.N / 2) : 0) | (a.gate_up ? out_grid(a, a.gate_up, a.N) : 0);
   const double pair_rest = grid % 16 == 0 && avg >= 32 ? 2.2 : KIND == kGated && grid % 16 != 0 ? 4.0 : 2.9;

@@ -7,11 +7,12 @@
 // columns of its row and forms h in registers.  The codes' blocks of 128 columns are two threads', which
 // exchange their row's largest |h| through shared memory.
 //
-// What bounds it: with few rows the weight stream (64 tokens x 6 over 384 experts, I = 640, K = 5120, to codes: 242-248 us,
-// 0.97 of the copy rate; 12288 rows over 128 experts, I = 1152, the products kept: 266-274 us, 0.91); with many, as the
+// What bounds it: with few rows the weight stream (64 tokens x 6 over 384 experts, I = 640, K = 5120, to codes: 248 us,
+// 0.96 of the copy rate; 12288 rows over 128 experts, I = 1152, the products kept: 272-276 us, 0.90); with many, as the
 // plain product of the same weights, the accumulator's round trip and the power limit (49152 rows over 48 experts, I =
-// 2048, K = 7168: 1.20-1.32 ms, the plain product 1.21-1.28).  A tile's end adds 16384 activations, for which the
-// special-function unit needs most of a microsecond: with K = 2048 399 us to codes, 372 to bf16 rows, plain 367.
+// 2048, K = 7168: 1.21-1.32 ms, the plain product 1.21-1.30).  A tile's end adds 16384 activations, for which the
+// special-function unit needs most of a microsecond: with K = 2048 405-408 us to codes, 378 to bf16 rows, plain 373 (of
+// which 3-4 us look for gates that need more than a shared reciprocal).
 #include "gemm_block_kernel.cuh"
 
 namespace moe {

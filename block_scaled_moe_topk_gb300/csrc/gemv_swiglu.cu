@@ -5,7 +5,7 @@
 // up row of one (or two) columns of h, so both sums end in the same warp.  For codes the 128 columns of a block are a
 // cluster of 16 (or 8) blocks of 8 warps, whose row maxima meet in every block's shared memory: the grid stays as wide as
 // without codes, where one block for 128 columns would leave most SMs idle.  Latency bounds it: one row, I = 1152, K =
-// 5120 3.8 us, to codes 5.4 (the cluster's barrier; the plain product of the same weights 4.1).
+// 5120 4.0 us, to codes 5.5-5.8 (the cluster's barrier; the plain product of the same weights 4.4).
 #include <atomic>
 
 #include "fp8_block_device.cuh"
@@ -195,7 +195,7 @@ cudaError_t launch_rows(const GemmBlockArgs& a, cudaStream_t s) {
 
 // Two columns of h a warp make the clusters 8 blocks: faster from three grouped rows on (a cluster a row and 128
 // columns), slower below (I = 1152, K = 5120, rows of 64 experts, one / two columns, us: 1 7.3 / 9.8, 2 9.3 / 10.6, 3
-// 14.1 / 11.3, 4 16.2 / 12.4; dense, one row 5.5 / 5.7).
+// 14.1 / 11.3, 4 16.2 / 12.5; dense, one row 5.5 / 5.7; values, one column: 3 rows 9.1, 4 13.2).
 template <bool CODES>
 cudaError_t launch(const GemmBlockArgs& a, cudaStream_t s) {
   if (CODES && a.offsets != nullptr && a.M > 2) return launch_rows<1, 5, 2, CODES>(a, s);

@@ -2,16 +2,16 @@
 //   dx = rstd (g - xh mean(g xh)) + dres,   dw = sum over rows of dy xh
 // One pass over dy, x and dres.  Blocks stay and walk the rows, so a thread keeps its columns' sums of dw in
 // registers; each block leaves its sums in the workspace and a second kernel adds them up, in the same
-// order every time (no atomics).  8192 x 7168 bf16 with d_residual 82 us (0.86 of the copy rate; 75 without dw), 4095 x
-// 5120 fp32 48-50 (0.75-0.78); 37 x 266 7.4.  Two blocks an SM wait for their rows' sums in turn; one block with a ring of
-// five rows took 111 us.
+// order every time (no atomics).  8192 x 7168 bf16 with d_residual 83 us (0.85 of the copy rate; 75 without dw), 4095 x
+// 5120 fp32 51 (0.74); 37 x 266 7.6.  Two blocks an SM wait for their rows' sums in turn (72 registers a thread, with
+// which the fp32 instances spill 32-68 bytes); one block with a ring of five rows took 111 us.
 //
 // A row's rstd is known, so one sum (of g xh) stands between its loads and its dx.  To keep HBM busy
 // meanwhile, rows come through shared memory by asynchronous 16-byte copies, a few rows ahead; a thread copies
 // what it will read itself, so no barrier guards the ring.  Rows that start off the 16-byte boundaries are
 // copied from the boundary below: a thread's columns then begin `shift` elements earlier.  The shift repeats
 // every 2 to 8 rows, and a block takes rows of one shift only, so that its columns of dw stay its own
-// (37401 x 1570 bf16 with d_residual 317 us element by element, 128 so; 8192 x 7167 86-98 against 82 of 7168).
+// (37401 x 1570 bf16 with d_residual 317 us element by element, 130 so; 8192 x 7167 88-90 against 83 of 7168).
 // Rows of matrices that disagree on the shift, and rows too long for the ring, are read directly, twice (the
 // second time from L1 or L2).
 #include <algorithm>
@@ -469,7 +469,8 @@ cudaError_t launch_typed(const NormBackwardArgs& a, bool vec, int classes, cudaS
     p.stages = grid;
   }
   if (err != cudaSuccess || a.dw == nullptr) return err;
-  // launched while the first kernel ends; it waits for it before it reads
+  // Its launch is prepared under the first kernel, which gives no signal: its blocks start when the first's have left, and
+  // wait for what those wrote.
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)((a.H + 31) / 32));
   cfg.blockDim = dim3(32 * kSumWays);

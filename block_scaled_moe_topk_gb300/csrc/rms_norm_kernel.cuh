@@ -3,8 +3,9 @@
 //   s = x + r,   rstd = 1 / sqrt(mean(s^2) + eps),   y = s rstd w
 // and its gradients (rms_norm_backward.cu).  One pass: a row's sums stay in registers from the load to
 // the output, so x and r are read once and s, y, the codes and the scales written once; it is bound by
-// HBM for many rows (8192 x 7168 bf16 with residual 70 us, to MX codes and rows 79: 1.00 of the copy rate) and by
-// launch latency for a few (one row of 5120 2.4 us).
+// HBM for many rows (8192 x 7168 bf16 with residual 70 us, to rows and MXFP8 codes 79, MXFP4 75: 0.99-1.00 of the copy
+// rate) and by launch latency for a few (one row of 5120 2.5 us).  To codes alone without a residual (47 us, 0.57) 19
+// instructions an element use 66 % of the issue slots, with 28 warps an SM that wait for loads, sums and conversions.
 //
 // The norm and the codes are those of the unrounded fp32 sum x + r; only what is written is rounded
 // (s and y to the rows' type, y to codes straight from fp32).  The sum of squares is fp32.
@@ -215,9 +216,11 @@ cudaError_t launch_chunks(const NormArgs& a, cudaStream_t s) {
   const bool rows = SHIFT && QF != kQuantNone;
   const NormParams p = shape_of(a, (a.H + (SHIFT ? 16 / dtype_bytes(DT) - 1 : 0) + 7) / 8, 32, rows, &nch, &threads, &grid);
   const size_t smem = rows ? (size_t)p.rpb * a.H * 4 : 0;
-  // Blocks an SM that the registers leave room for, 16-bit rows of up to 7168 columns; 8192 x 7168 bf16, us, with 1,
-  // 4, 5, 6 blocks asked for: with residual 69.4, 69.0, 74, 117; to codes 69.9, 62.8, 75, 115; without residual
-  // 45.9, 40.6, 38.0, 48; to codes 54, 47, 45, 60.  fp32, 4096 x 7168 with residual: 70.8, 93.
+  // Blocks an SM that the registers leave room for, where a block has up to 224 threads (16-bit rows of 4097 to 7168
+  // columns; narrower ones mostly fill 256 threads with several rows); 8192 x 7168 bf16, us, with 1, 4, 5, 6 blocks
+  // asked for: with residual 69.4, 69.0, 74, 117; to codes 69.9, 62.8, 75, 115; without residual 45.9, 40.6, 38.0, 48;
+  // to codes 54, 47, 45, 60.  fp32, 4096 x 7168 with residual: 70.8, 93.  Blocks of 256 threads and more run with one
+  // asked for: 8192 x 4096 41 us with residual (0.97 of the copy rate), 27 without (0.73), 8192 x 8192 78 and 75 to codes.
   constexpr int kBlocks = DT == kDtF32 ? 1 : SHIFT ? 3 : RES || QF != kQuantNone ? 4 : 5;
   if constexpr (kBlocks > 1) {
     if (nch == 4 && threads <= 224) {

@@ -3,7 +3,7 @@
 // for rows whose 2I columns hold gate and up in turn (2j gate, 2j + 1 up) or one after the other, leaving as
 // FP8 codes with one fp32 scale per 1x128 block (of the 2I columns, as the next product's reduction reads
 // them), as values, or both.  Elementwise but for the blocks' maxima, bound by HBM: 8 bytes in and out per h of 16-bit
-// rows with codes (49152 x 2048: 126 us, 0.96 of the copy rate), with the issue slots 70 % used.
+// rows with codes (49152 x 2048: 127-128 us, 0.95 of the copy rate), with the issue slots 70 % used.
 //
 // A thread owns 8 columns of h and their 16 of gate and up: on 16-byte boundaries 8 consecutive ones, so
 // that 8 lanes (in turn) or 16 (one after the other) hold a block.  Otherwise a warp owns spans of 256

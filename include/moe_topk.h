@@ -518,8 +518,9 @@ moe_status_t moe_permute_quantize_fp8_block(const void* x, int64_t x_stride, moe
  *   out           y out; may be x or residual itself where that is not residual_out
  *   weight        [H] of `weight_dtype`: `dtype` or F32;  eps >= 0
  *   rstd          fp32 [T] out: 1 / sqrt(mean(s^2) + eps), which the gradient needs; or NULL
- * A row whose squares' sum passes fp32's range (magnitudes of 1e19 and more) has no finite norm; NaN and
- * infinities stay in their row.
+ * The squares and their sum are fp32: a row in which they pass its range (magnitudes of 1e19 and more) gets rstd = 0 and
+ * y = 0, and with eps = 0 one in which they vanish (1e-23 and less, or zeros) rstd = inf.  NaN and infinities stay in
+ * their row.
  */
 moe_status_t moe_rms_norm(const void* x, int64_t x_stride, const void* residual, int64_t residual_stride,
                           moe_dtype_t dtype, const void* weight, moe_dtype_t weight_dtype, float eps, int64_t T, int H,
@@ -549,7 +550,7 @@ moe_status_t moe_rms_norm_quantize_mx(const void* x, int64_t x_stride, const voi
  *   dy, x, dx     [T, H] of `dtype`; dx is the gradient of x and of residual alike
  *   d_residual    [T, H] of `dtype`: the gradient that reaches residual_out from elsewhere; or NULL
  *   rstd          fp32 [T], as the norm wrote it;  weight as there
- *   d_weight      fp32 [H] out, summed in fp32 in an order that depends on the sizes alone; or NULL
+ *   d_weight      fp32 [H] out, summed in fp32 in an order that depends on sizes, strides and alignment alone; or NULL
  *   workspace     device, 256-byte aligned, >= moe_rms_norm_backward_workspace_bytes(T, H); needed with
  *                 d_weight only, for its partial sums (two kernels run then)
  *   dx may be dy, x or d_residual itself, with its stride.
